@@ -26,7 +26,7 @@ own = False
 TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
 FP8 = torch.float8_e4m3fn
 TOP = 448.0  # the largest e4m3 number
-LEAST = 2.0 ** -100  # the least magnitude a block is scaled by, so that no scale is zero or subnormal
+LEAST = 2.0 ** -64  # the least magnitude a block is scaled by, so that no scale is zero or subnormal
 
 
 def listed():
