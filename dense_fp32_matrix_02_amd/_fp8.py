@@ -1,0 +1,283 @@
+"""FP8 products with a scale for each block of 128, and their quantisers.
+
+The C calls of include/sgemm_mi355_fp8.h under their own names, and wrappers
+that take torch tensors on the GPU (argument marshalling only; the arithmetic
+runs in the library's HIP kernels, and there is no fallback).
+
+A quantised matrix is a pair (Q, S): Q of dtype float8_e4m3fn, S float32 with
+one column for each block of 128 columns of Q. Rows of Q are stored at a stride
+that is a multiple of 16 bytes; the scales of rows are stored block by block
+(S.stride() == (1, rows)), those of tiles row by row.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from ._binding import OK, SgemmError, _ld, load
+
+ERR_TYPE, ERR_ROUTE = -13, -14
+F32, BF16, F16 = 0, 1, 2
+
+_P, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+_SCALES = [_P, _LL, _LL]
+_SIGNATURES = {
+    "sgemm_mi355_fp8_quantize_rows": [_I, _I, _I, _P, _I, _P, _I, _P, _I, *_SCALES, _P],
+    "sgemm_mi355_fp8_quantize_cols": [_I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, *_SCALES, _P],
+    "sgemm_mi355_fp8_quantize_tiles": [_I, _I, _I, _P, _I, _P, _I, *_SCALES, _P],
+    "sgemm_mi355_fp8_gemm": [_I] * 4 + [_P, _I, *_SCALES, _P, _I, *_SCALES, _I, _F, _P, _I, _P],
+    "sgemm_mi355_fp8_gemm_experts": [_I] * 5 + [_P, _I, *_SCALES, _P, _I, _LL, *_SCALES, _LL, _I, _P, _P, _I, _P],
+    "sgemm_mi355_fp8_gemm_experts_wgrad": [_I] * 5 + [_P, _I, *_SCALES, _P, _I, *_SCALES, _P, _F, _P, _I, _LL, _P],
+}
+
+
+def _bind(name, argtypes, restype=_I):
+    """The C function `name`, looked up in the library at its first call."""
+    found = []
+
+    def call(*args):
+        if not found:
+            fn = getattr(load(), name)
+            fn.argtypes, fn.restype = argtypes, restype
+            found.append(fn)
+        return found[0](*args)
+
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = f"C function {name}: device addresses and the stream as ints; returns its code."
+    return call
+
+
+for _name, _types in _SIGNATURES.items():
+    globals()[_name] = _bind(_name, _types)
+
+
+def _type_of(dtype, name):
+    import torch
+
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    return code
+
+
+def _stream_of(x, stream):
+    import torch
+
+    return (torch.cuda.current_stream(x.device) if stream is None else stream).cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor from torch's caching allocator, allocated on the stream the
+    call runs on, so that the allocator hands its memory out again only after
+    that stream's work."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _gpu(x, name, dtype=None):
+    if not x.is_cuda or (dtype is not None and x.dtype != dtype):
+        raise TypeError(f"{name} must be a {'' if dtype is None else str(dtype).replace('torch.', '') + ' '}GPU tensor")
+    return x
+
+
+def _ints(x, name, length=None):
+    """Address of a dense 1-D int32 GPU tensor."""
+    import torch
+
+    _gpu(x, name, torch.int32)
+    if x.dim() != 1 or (x.numel() > 1 and x.stride(0) != 1) or (length is not None and x.numel() != length):
+        raise ValueError(f"{name} must be a dense 1-D tensor" + ("" if length is None else f" of {length} values"))
+    return x.data_ptr()
+
+
+def _check(rc, where):
+    if rc != OK:
+        raise SgemmError(rc, where)
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _bytes_out(rows, cols, device, stream):
+    """An uninitialised e4m3 matrix whose row stride is a multiple of 16 bytes."""
+    import torch
+
+    pad = -cols % 16
+    q = _empty((rows, cols + pad), torch.float8_e4m3fn, device, stream)
+    return q[:, :cols] if pad else q
+
+
+def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
+    """(Q, S): the rows of X (float32, bfloat16 or float16, rows may be padded)
+    in e4m3 with a scale for each block of 128 columns.
+
+    ``index`` (int32): row i of Q is row index[i] of X; an index outside X
+    gives zeros. ``blocks``: one scale for each 128 x 128 tile instead, for
+    weights; S then has a row for each 128 rows of X.
+    """
+    import torch
+
+    _gpu(X, "X")
+    kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
+    rows, cols = X.shape
+    s = _stream_of(X, stream)
+    if blocks:
+        if index is not None:
+            raise ValueError("tiles are quantised without an index")
+        Q = _bytes_out(rows, cols, X.device, stream)
+        S = _empty((_blocks(rows), _blocks(cols)), torch.float32, X.device, stream)
+        _check(sgemm_mi355_fp8_quantize_tiles(kind, rows, cols, X.data_ptr(), ldx, Q.data_ptr(), _ld(Q, "Q"),  # noqa: F821
+                                              S.data_ptr(), S.stride(0), S.stride(1), s), "sgemm_mi355_fp8_quantize_tiles")
+        return Q, S
+    n = rows if index is None else index.numel()
+    at = None if index is None else _ints(index, "index")
+    Q = _bytes_out(n, cols, X.device, stream)
+    S = _empty((_blocks(cols), n), torch.float32, X.device, stream)
+    if at is not None and n == 0:
+        return Q, S.t()
+    _check(sgemm_mi355_fp8_quantize_rows(kind, rows, cols, X.data_ptr(), ldx, at, n, Q.data_ptr(), _ld(Q, "Q"),  # noqa: F821
+                                         S.data_ptr(), 1, max(n, 1), s), "sgemm_mi355_fp8_quantize_rows")
+    return Q, S.t()
+
+
+def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
+    """(Q, S): the columns of X in e4m3, stored transposed (row c of Q is
+    column c of X) with a scale for each block of 128 rows of X, for products
+    that sum over X's rows.
+
+    ``index`` (int32): the rows of X to take, in their order. ``offsets``
+    (int32, experts + 1): the rows are sorted by expert and every expert's rows
+    begin a block, expert e's block offsets[e] // 128 + e; Q then has
+    128 * (n // 128 + experts) columns, zero where no row is.
+    """
+    import torch
+
+    _gpu(X, "X")
+    kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
+    rows, cols = X.shape
+    n = rows if index is None else index.numel()
+    at = None if index is None else _ints(index, "index")
+    experts = 0 if offsets is None else offsets.numel() - 1
+    if offsets is not None and experts < 1:
+        raise ValueError("offsets must have experts + 1 values")
+    off = None if offsets is None else _ints(offsets, "offsets")
+    width = n if offsets is None else 128 * (n // 128 + experts)
+    Q = _bytes_out(cols, width, X.device, stream)
+    S = _empty((_blocks(width), cols), torch.float32, X.device, stream)
+    if at is not None and n == 0:
+        at, rows = None, 0
+    _check(sgemm_mi355_fp8_quantize_cols(kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts,  # noqa: F821
+                                         Q.data_ptr(), _ld(Q, "Q"), S.data_ptr(), 1, max(cols, 1),
+                                         _stream_of(X, stream)), "sgemm_mi355_fp8_quantize_cols")
+    return Q, S.t()
+
+
+def _operand(Q, S, name, rows, cols, either=False):
+    """Address, row stride, scales' address and strides, and rows that share a
+    scale, of a quantised matrix (2-D, or the last two axes of a 3-D one)."""
+    import torch
+
+    if Q.dtype != torch.float8_e4m3fn or not Q.is_cuda:
+        raise TypeError(f"{name} must be a float8_e4m3fn GPU tensor")
+    if S.dtype != torch.float32 or not S.is_cuda:
+        raise TypeError(f"the scales of {name} must be a float32 GPU tensor")
+    one = Q if Q.dim() == 2 else Q[0]
+    per, blocks = S.shape[-2:]
+    if blocks != _blocks(cols) or per not in ((rows, _blocks(rows)) if either else (rows,)):
+        raise ValueError(f"the scales of {name} must be {rows}{f' or {_blocks(rows)}' if either else ''} x {_blocks(cols)}, "
+                         f"not {per} x {blocks}")
+    return Q.data_ptr(), _ld(one, name), S.data_ptr(), S.stride(-2), S.stride(-1), 1 if per == rows else 128
+
+
+def _result(C, shape, dtype, device, beta, stream):
+    if C is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs an input C")
+        return _empty(shape, dtype, device, stream)
+    if tuple(C.shape) != tuple(shape):
+        raise ValueError(f"C must be {' x '.join(map(str, shape))}")
+    return _gpu(C, "C")
+
+
+def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, stream=None):
+    """C = A.B^T + beta*C for quantised A (M x K) and B (N x K).
+
+    SA has a scale for each block of a row of A (M x K/128), SB for each block
+    of a row of B (N x K/128) or for each 128 x 128 tile (N/128 x K/128), as
+    the quantisers give them. C is allocated with ``dtype`` (bfloat16 unless
+    given) when omitted.
+    """
+    import torch
+
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    (M, K), (N, K2) = A.shape, B.shape
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    a = _operand(A, SA, "A", M, K)
+    b = _operand(B, SB, "B", N, K, either=True)
+    C = _result(C, (M, N), dtype or torch.bfloat16, A.device, beta, stream)
+    _check(sgemm_mi355_fp8_gemm(_type_of(C.dtype, "C"), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"),  # noqa: F821
+                                _stream_of(A, stream)), "sgemm_mi355_fp8_gemm")
+    return C
+
+
+def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, stream=None):
+    """C[r] = A[r].B[e]^T for expert e's rows r, offsets[e] <= r < offsets[e + 1].
+
+    A (R x K) holds the rows sorted by expert, B is experts x N x K with scales
+    for its rows (experts x N x K/128) or tiles (experts x N/128 x K/128).
+    Rows from offsets[-1] on are set to zero.
+    """
+    import torch
+
+    if A.dim() != 2 or B.dim() != 3 or SB.dim() != 3 or SB.shape[0] != B.shape[0] or B.shape[0] < 1:
+        raise ValueError("A must be 2-D, B and its scales 3-D with the experts first")
+    (R, K), (E, N, K2) = A.shape, B.shape
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    off = _ints(offsets, "offsets", E + 1)
+    a = _operand(A, SA, "A", R, K)
+    b = _operand(B, SB, "B", N, K, either=True)
+    C = _result(C, (R, N), dtype or torch.bfloat16, A.device, 0.0, stream)
+    _check(sgemm_mi355_fp8_gemm_experts(_type_of(C.dtype, "C"), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5],  # noqa: F821
+                                        SB.stride(0), b[5], off, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)),
+           "sgemm_mi355_fp8_gemm_experts")
+    return C
+
+
+def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, dtype=None, stream=None):
+    """C[e] = sum over expert e's rows r of A[:, r].B[:, r]^T + beta*C[e].
+
+    A (M x P) and B (N x P) as quantize_fp8_cols makes them with these
+    ``offsets``; C is experts x M x N, allocated with ``dtype`` (float32 unless
+    given) when omitted.
+    """
+    import torch
+
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    (M, P), (N, P2) = A.shape, B.shape
+    E = offsets.numel() - 1
+    off = _ints(offsets, "offsets")
+    if P != P2:
+        raise ValueError("inner dimensions differ")
+    if E < 1 or P % 128 != 0 or P < 128 * E:
+        raise ValueError("A and B must be quantised by columns with these offsets")
+    # P counts the blocks of rows, so the rows are known to a block: the most
+    # that P has room for. The offsets end before that.
+    rows = P - 128 * E + 127
+    a = _operand(A, SA, "A", M, P)
+    b = _operand(B, SB, "B", N, P)
+    C = _result(C, (E, M, N), dtype or torch.float32, A.device, beta, stream)
+    if C.dim() != 3:
+        raise ValueError("C must be experts x M x N")
+    ldc = _ld(C[0], "C")
+    _check(sgemm_mi355_fp8_gemm_experts_wgrad(_type_of(C.dtype, "C"), rows, M, N, E, *a[:5], *b[:5], off, beta,  # noqa: F821
+                                              C.data_ptr(), ldc, C.stride(0), _stream_of(A, stream)),
+           "sgemm_mi355_fp8_gemm_experts_wgrad")
+    return C

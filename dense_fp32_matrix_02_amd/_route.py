@@ -1,0 +1,157 @@
+"""Routing of tokens to experts, the order of the experts' rows, and the
+weighted return of those rows.
+
+The C calls of include/sgemm_mi355_route.h under their own names, and wrappers
+that take torch tensors on the GPU (argument marshalling only).
+"""
+from __future__ import annotations
+
+import ctypes
+
+from ._binding import _ld
+from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _P, _stream_of, _type_of
+
+SOFTMAX, SIGMOID = 0, 1
+MAX_EXPERTS, MAX_CHOICES = 1024, 32
+
+_SIZE = ctypes.c_size_t
+_SIGNATURES = {
+    "sgemm_mi355_route": [_I, _I, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P],
+    "sgemm_mi355_route_backward": [_I, _I, _I, _P, _I, _P, _P, _I, _I, _I, _F, _P, _I, _P],
+    "sgemm_mi355_route_plan": [_I, _I, _I, _P, _P, _P, _P, _P, _SIZE, _P],
+    "sgemm_mi355_route_combine": [_I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P],
+    "sgemm_mi355_route_combine_backward": [_I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _I, _P, _P],
+}
+for _name, _types in _SIGNATURES.items():
+    globals()[_name] = _bind(_name, _types)
+sgemm_mi355_route_plan_workspace_size = _bind("sgemm_mi355_route_plan_workspace_size", [_I, _I, _I], _SIZE)
+
+
+def _score(score):
+    code = {"softmax": SOFTMAX, "sigmoid": SIGMOID}.get(score)
+    if code is None:
+        raise ValueError(f"unknown score {score!r}")
+    return code
+
+
+def _dense(x, name, dtype, shape):
+    """Address of a dense GPU tensor of this dtype and shape."""
+    _gpu(x, name, dtype)
+    if tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a dense {' x '.join(map(str, shape))} tensor")
+    return x.data_ptr()
+
+
+def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+          renorm: bool = True, scale: float = 1.0, stream=None):
+    """(weights, experts): each token's k experts and their weights, tokens x k
+    (float32 and int32), by descending choice value; of equal values the lower
+    index comes first.
+
+    logits: tokens x experts, float32, bfloat16 or float16. The scores are a
+    softmax or a sigmoid of them; ``bias`` (float32, one for each expert) moves
+    the choice and not the weights; with ``groups`` > 1 only the ``top_groups``
+    groups with the largest sum of their two largest choice values take part;
+    ``renorm`` divides the weights by their sum; ``scale`` multiplies them.
+    """
+    import torch
+
+    _gpu(logits, "logits")
+    kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
+    tokens, experts = logits.shape
+    at = None if bias is None else _dense(bias, "bias", torch.float32, (experts,))
+    weights = _empty((tokens, max(k, 0)), torch.float32, logits.device, stream)
+    ids = _empty((tokens, max(k, 0)), torch.int32, logits.device, stream)
+    _check(sgemm_mi355_route(kind, tokens, experts, logits.data_ptr(), ld, at, how, groups, top_groups, k,  # noqa: F821
+                             int(bool(renorm)), scale, weights.data_ptr(), ids.data_ptr(), _stream_of(logits, stream)),
+           "sgemm_mi355_route")
+    return weights, ids
+
+
+def route_backward(logits, experts, dweights, *, score: str = "softmax", renorm: bool = True, scale: float = 1.0,
+                   stream=None):
+    """The gradient of the logits (float32) for given gradients of route's
+    weights; ``experts`` are the ones it chose."""
+    import torch
+
+    _gpu(logits, "logits")
+    kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
+    tokens, count = logits.shape
+    k = experts.shape[-1]
+    ids = _dense(experts, "experts", torch.int32, (tokens, k))
+    dw = _dense(dweights, "dweights", torch.float32, (tokens, k))
+    out = _empty((tokens, count), torch.float32, logits.device, stream)
+    _check(sgemm_mi355_route_backward(kind, tokens, count, logits.data_ptr(), ld, ids, dw, how, k,  # noqa: F821
+                                      int(bool(renorm)), scale, out.data_ptr(), max(count, 1), _stream_of(logits, stream)),
+           "sgemm_mi355_route_backward")
+    return out
+
+
+def route_plan(experts, num_experts: int, *, stream=None):
+    """(offsets, tokens, place): the tokens' rows sorted by expert.
+
+    experts: tokens x k int32, as route gives them. Expert e's rows are
+    offsets[e] .. offsets[e + 1] - 1 (offsets: num_experts + 1); row r is a row
+    of token tokens[r]; choice j of token t has row place[t, j]. Ids outside
+    the experts come after offsets[-1].
+    """
+    import torch
+
+    if experts.dim() != 2:
+        raise ValueError("experts must be tokens x k")
+    tokens, k = experts.shape
+    ids = _dense(experts, "experts", torch.int32, (tokens, k))
+    need = sgemm_mi355_route_plan_workspace_size(tokens, k, num_experts)
+    # one allocation for the three results and one for the workspace
+    offsets = _empty((max(num_experts, 0) + 1,), torch.int32, experts.device, stream)
+    rows = _empty((tokens * k,), torch.int32, experts.device, stream)
+    place = _empty((tokens, k), torch.int32, experts.device, stream)
+    room = _empty((need // 4,), torch.int32, experts.device, stream)
+    _check(sgemm_mi355_route_plan(tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),  # noqa: F821
+                                  place.data_ptr(), room.data_ptr(), need, _stream_of(experts, stream)),
+           "sgemm_mi355_route_plan")
+    return offsets, rows, place
+
+
+def route_combine(Z, place, weights, Y=None, *, stream=None):
+    """Y[t] = sum_j weights[t, j] * Z[place[t, j]], of Z's dtype; a place
+    outside Z's rows adds nothing."""
+    import torch
+
+    _gpu(Z, "Z")
+    kind, ldz = _type_of(Z.dtype, "Z"), _ld(Z, "Z")
+    rows, cols = Z.shape
+    tokens, k = place.shape
+    at, w = _dense(place, "place", torch.int32, (tokens, k)), _dense(weights, "weights", torch.float32, (tokens, k))
+    if Y is None:
+        Y = _empty((tokens, cols), Z.dtype, Z.device, stream)
+    _gpu(Y, "Y", Z.dtype)
+    if tuple(Y.shape) != (tokens, cols):
+        raise ValueError("Y must be tokens x cols")
+    _check(sgemm_mi355_route_combine(kind, tokens, k, rows, cols, Z.data_ptr(), ldz, at, w, Y.data_ptr(), _ld(Y, "Y"),  # noqa: F821
+                                     _stream_of(Z, stream)), "sgemm_mi355_route_combine")
+    return Y
+
+
+def route_combine_backward(dY, Z, place, weights, *, stream=None):
+    """(dZ, dweights) of route_combine for the gradient dY of its result.
+
+    place must name each row of Z once, as route_plan's does: rows that it does
+    not name are not written.
+    """
+    import torch
+
+    _gpu(Z, "Z")
+    _gpu(dY, "dY", Z.dtype)
+    kind, ldz, ldy = _type_of(Z.dtype, "Z"), _ld(Z, "Z"), _ld(dY, "dY")
+    rows, cols = Z.shape
+    tokens, k = place.shape
+    if tuple(dY.shape) != (tokens, cols):
+        raise ValueError("dY must be tokens x cols")
+    at, w = _dense(place, "place", torch.int32, (tokens, k)), _dense(weights, "weights", torch.float32, (tokens, k))
+    dZ = _empty((rows, cols), Z.dtype, Z.device, stream)
+    dw = _empty((tokens, k), torch.float32, Z.device, stream)
+    _check(sgemm_mi355_route_combine_backward(kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,  # noqa: F821
+                                              dZ.data_ptr(), max(cols, 1), dw.data_ptr(), _stream_of(Z, stream)),
+           "sgemm_mi355_route_combine_backward")
+    return dZ, dw

@@ -1,0 +1,187 @@
+// Declarations shared by the FP8 and routing kernels and their host sides.
+#pragma once
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "sgemm_mi355_route.h"
+
+namespace sgemm_impl {
+
+constexpr int kBlock = 128;  // values of the summed axis that share a scale
+
+struct QuantArgs {
+  const void* X;
+  int64_t ldx;
+  int rows, cols;      // of X
+  const int* index;    // row i of the quantised matrix is row index[i] of X; null: row i
+  int n;               // rows that are quantised
+  const int* offsets;  // expert boundaries of the columns form; null: one run of n rows
+  int experts;
+  uint8_t* Q;
+  int64_t ldq;
+  float* S;
+  int64_t s_row, s_block;
+};
+
+hipError_t launch_quantize_rows(int type, const QuantArgs& q, hipStream_t s);
+hipError_t launch_quantize_cols(int type, const QuantArgs& q, hipStream_t s);
+hipError_t launch_quantize_tiles(int type, const QuantArgs& q, hipStream_t s);
+
+// One FP8 product, or one for each expert. DENSE: C = A.B^T + beta*C. EXPERTS:
+// rows of A and C belong to experts by `offsets`, B_e = B + e*strideB.
+// WGRAD: the summed axis belongs to experts, C_e = C + e*strideC.
+enum Fp8Form { FP8_DENSE = 0, FP8_EXPERTS = 1, FP8_WGRAD = 2 };
+
+struct Fp8Args {
+  int type, M, N, K;  // WGRAD: K = the rows that offsets count
+  const uint8_t* A;
+  int64_t lda;
+  const float* SA;
+  int64_t sa_row, sa_block;
+  const uint8_t* B;
+  int64_t ldb, strideB;
+  const float* SB;
+  int64_t sb_row, sb_block, stride_sb;
+  int sb_rows;  // rows of B that share a scale: 1 or 128
+  const int* offsets;
+  int experts;
+  float beta;
+  void* C;
+  int64_t ldc, strideC;
+};
+
+hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s);
+// Whether the grids launch_fp8_gemm would use for g fit a launch.
+bool fp8_launchable(Fp8Form form, const Fp8Args& g);
+
+// Beginning and end of expert e's rows: offsets limited to 0 .. rows, an end
+// before the beginning gives no rows, and the first expert begins at 0.
+__device__ __forceinline__ void expert_rows(const int* offsets, int e, int rows, int& begin, int& end) {
+  const int b = e == 0 ? 0 : offsets[e], t = offsets[e + 1];
+  begin = b < 0 ? 0 : (b > rows ? rows : b);
+  end = t < begin ? begin : (t > rows ? rows : t);
+}
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int tokens, experts, groups, top_groups, choices, renorm;
+  float scale;
+  float* weights;
+  int* ids;
+  // backward
+  const int* ids_in;
+  const float* dweights;
+  float* dlogits;
+  int64_t ldd;
+};
+
+hipError_t launch_route(int type, int score, const RouteArgs& r, hipStream_t s);
+hipError_t launch_route_backward(int type, int score, const RouteArgs& r, hipStream_t s);
+
+struct PlanArgs {
+  int entries, choices, experts;
+  const int* ids;
+  int *offsets, *row_token, *place;
+  int* counts;  // workspace: entries of each expert in each run of kPlanRun entries
+};
+constexpr int kPlanRun = 1024;
+hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s);
+
+struct CombineArgs {
+  int tokens, choices, rows, cols;
+  const void* Z;
+  int64_t ldz;
+  const int* place;
+  const float* weights;
+  void* Y;
+  int64_t ldy;
+  // backward
+  const void* dY;
+  int64_t lddy;
+  void* dZ;
+  int64_t lddz;
+  float* dweights;
+};
+hipError_t launch_combine(int type, const CombineArgs& c, hipStream_t s);
+hipError_t launch_combine_backward(int type, const CombineArgs& c, hipStream_t s);
+
+// Kernel arguments by value through hipLaunchKernel.
+template <class Args>
+inline hipError_t launch_with(const void* kernel, dim3 grid, dim3 block, const Args& a, hipStream_t s) {
+  Args copy = a;
+  void* args[] = {&copy};
+  return hipLaunchKernel(kernel, grid, block, args, 0, s);
+}
+
+// f(T{}) for the element type that `type` names.
+template <class F>
+inline hipError_t by_type(int type, F&& f) {
+  switch (type) {
+    case SGEMM_MI355_F32: return f(float{});
+    case SGEMM_MI355_BF16: return f(__hip_bfloat16{});
+    default: return f(__half{});
+  }
+}
+
+#if defined(__HIP_DEVICE_COMPILE__) || defined(__HIPCC__)
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__hip_bfloat16 x) {
+  uint16_t u;
+  __builtin_memcpy(&u, &x, 2);
+  return __uint_as_float((uint32_t)u << 16);
+}
+// Rounded to the nearest, half to even; NaN stays NaN.
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __hip_bfloat16 from_f32<__hip_bfloat16>(float x) {
+  const uint32_t u = __float_as_uint(x);
+  uint16_t r = (uint16_t)((u + 0x7FFF + ((u >> 16) & 1)) >> 16);
+  if ((u & 0x7FFFFFFF) > 0x7F800000) r = (uint16_t)((u >> 16) | 0x40);
+  __hip_bfloat16 y;
+  __builtin_memcpy(&y, &r, 2);
+  return y;
+}
+
+// `valid` (any number) of eight consecutive elements at p as FP32, the rest
+// zero. p needs only its element's alignment: a whole vector load needs none
+// on this hardware beyond that.
+template <class T>
+__device__ __forceinline__ void load8(const T* p, int valid, float (&v)[8]) {
+  if (valid >= 8) {
+    T e[8];
+    __builtin_memcpy(e, p, sizeof(e));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < valid ? to_f32(p[i]) : 0.0f;
+  }
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, int valid, const float (&v)[8]) {
+  if (valid >= 8) {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(v[i]);
+    __builtin_memcpy(p, e, sizeof(e));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = from_f32<T>(v[i]);
+  }
+}
+#endif
+
+}  // namespace sgemm_impl

@@ -1040,6 +1040,8 @@ const char* sgemm_mi355_strerror(int code) {
       return "the split-K partial sums exceed the library's static scratch (SGEMM_MI355_SCRATCH_BYTES per device)";
     case SGEMM_MI355_ERR_WORKSPACE:
       return "the workspace is smaller than sgemm_mi355_splitk_workspace_size or sgemm_mi355_streamk_workspace_size";
+    case SGEMM_MI355_ERR_TYPE: return "an element type is not one the call supports";
+    case SGEMM_MI355_ERR_ROUTE: return "the experts, groups or choices are outside what routing supports";
     default: return "unknown error code";
   }
 }

@@ -65,6 +65,9 @@ extern "C" {
 #define SGEMM_MI355_ERR_WORKSPACE (-11) /* split-K or stream-K workspace smaller than required */
 #define SGEMM_MI355_ERR_SCRATCH (-12) /* split-K partial sums larger than SGEMM_MI355_SCRATCH_BYTES */
 
+#define SGEMM_MI355_ERR_TYPE (-13)    /* an element type is not one the call supports */
+#define SGEMM_MI355_ERR_ROUTE (-14)   /* experts, groups or choices outside what routing supports */
+
 /* Size of the library's static device scratch (per device), used only by
  * sgemm_mi355_splitk_noalloc. */
 #define SGEMM_MI355_SCRATCH_BYTES (32u << 20)
