@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libsgemm_mi355.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["kernels_mfma.hip", "kernels_mfma_dma.hip", "kernels_valu.hip", "kernels_util.hip", "sgemm_api.hip",
-           "kernels_fp8_gemm.hip", "kernels_fp8_quantize.hip", "kernels_route.hip", "fp8_api.hip", "route_api.hip"]
+           "kernels_fp8_gemm.hip", "kernels_fp8_tile.hip", "kernels_fp8_skinny.hip",
+           "kernels_fp8_quantize.hip", "kernels_route.hip", "fp8_api.hip", "route_api.hip"]
 ARCH = os.environ.get("SGEMM_MI355_ARCH", "gfx950")
 
 HIPFLAGS = [

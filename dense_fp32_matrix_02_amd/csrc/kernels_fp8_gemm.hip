@@ -2,132 +2,27 @@
 // axis:
 //   C[m][n] = sum_b sA[m][b] * sB[n][b] * P_b[m][n],  P_b = sum_{k in b} A[m][k]*B[n][k].
 //
-// Sums are held in FP32. The FP8 matrix unit does not do that: it adds products
-// in groups of eight, keeping of each only what lies within 13 bits of the
-// group's largest (measured: 16*16 + 2^-6 in one group gives 256; in different
-// groups nothing is lost). So the values are widened to bf16, which holds
-// every e4m3 number, and multiplied with v_mfma_f32_32x32x16_bf16, whose sums
-// measure as FP32 sums. A block's eight such steps start from zero, and one
-// fused multiply-add per element by the block's scale adds P_b to the result.
+// Two ways to a block's sum:
+// * The FP8 matrix unit (v_mfma_f32_16x16x128_f8f6f4) has twice the rate of
+//   bf16, but adds products in groups of eight in fixed point, dropping of
+//   each what lies more than 13 bits below the group's largest (measured:
+//   2^15 + 2^2 in one group is exact, 2^15 + 2^1 gives 2^15; group sums and
+//   the accumulator add up as FP32). On quantised normal data that is 2e-5 of
+//   the result, a hundredth of the rounding to bf16 and a tenth of fp16's, so
+//   it is used where C has 16 bits.
+// * Otherwise values are widened to bf16, which holds every e4m3 number, and
+//   multiplied with bf16 matrix instructions, whose sums measure as FP32 sums.
+// Either starts a block from zero, and one fused multiply-add per element by
+// the block's scale adds P_b to the result in FP32.
 // B's rows are the instruction's rows and A's rows its columns, so that a
 // lane's 16 results are one row of C (one m): sA is then one value per lane,
 // and a lane's results are four runs of four neighbours in C.
 
-#include "fp8_internal.h"
 #include "sgemm_internal.h"
+#include "fp8_device.h"
 
 namespace sgemm_impl {
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// What one workgroup computes: a tile of one product.
-struct Tile {
-  const uint8_t *A, *B;  // row 0 of the operands
-  const float *SA, *SB;
-  int rows_a, rows_b;  // rows that exist
-  int m0, n0;          // first row and column of the tile
-  int K;
-  void* C;  // row 0 of the product's C
-};
-
-// Bytes [k, k + 16) of a row of K, zero from K on; any alignment.
-__device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) v[i / 4] |= (int)((uint32_t)row[k + i] << (8 * (i % 4)));
-  }
-  return v;
-}
-
-// Position of 16-byte chunk c of row r of a 128-byte-row slab: gfx950 serves
-// a 128-bit LDS read 16 lanes at a time from 64 banks, so 16 consecutive rows
-// (each starting at bank 0 or 32) have to hold one chunk in different places.
-__device__ __forceinline__ int swz(int r, int c) { return c ^ ((r >> 1) & 7); }
-
-// Eight e4m3 bytes as bf16, exactly.
-__device__ __forceinline__ bf16x8 widen(int lo, int hi) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-template <class T>
-__device__ __forceinline__ void store4(T* c, int valid, f32x4 v, float beta) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < valid) c[i] = from_f32<T>(beta != 0.0f ? __builtin_fmaf(beta, to_f32(c[i]), v[i]) : v[i]);
-}
-
-// Which tile of which product this workgroup has. False: none.
-template <int FORM, int BM, int BN>
-__device__ __forceinline__ bool find_tile(const Fp8Args& g, Tile& t) {
-  const int tiles_n = (g.N + BN - 1) / BN;
-  t.A = g.A, t.B = g.B, t.SA = g.SA, t.SB = g.SB, t.C = g.C;
-  t.rows_a = g.M, t.rows_b = g.N, t.K = g.K;
-  if constexpr (FORM == FP8_EXPERTS) {
-    // Tiles are numbered expert by expert; the wave counts 64 experts at a time.
-    const int lane = threadIdx.x % 64;
-    const int tm = blockIdx.x / tiles_n;
-    t.n0 = (blockIdx.x - tm * tiles_n) * BN;
-    int before = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 64) {
-      int begin = 0, end = 0;
-      if (e0 + lane < g.experts) expert_rows(g.offsets, e0 + lane, g.M, begin, end);
-      const int own = (end - begin + BM - 1) / BM;
-      int upto = own;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int x = __shfl_up(upto, d, 64);
-        if (lane >= d) upto += x;
-      }
-      const uint64_t past = __ballot(tm < before + upto);
-      if (past != 0) {
-        const int l = __builtin_ctzll(past);
-        const int e = e0 + l;
-        t.m0 = __shfl(begin, l, 64) + (tm - before - __shfl(upto - own, l, 64)) * BM;
-        t.rows_a = __shfl(end, l, 64);
-        t.B = g.B + (int64_t)e * g.strideB;
-        t.SB = g.SB + (int64_t)e * g.stride_sb;
-        return true;
-      }
-      before += __shfl(upto, 63, 64);
-    }
-    // Rows no expert has: a product over nothing.
-    int begin, end;
-    expert_rows(g.offsets, g.experts - 1, g.M, begin, end);
-    t.m0 = end + (tm - before) * BM;
-    t.K = 0;
-    return t.m0 < g.M;
-  } else {
-    const int tiles_m = (g.M + BM - 1) / BM;
-    const int tm = blockIdx.x % tiles_m;
-    t.m0 = tm * BM;
-    t.n0 = (blockIdx.x / tiles_m) * BN;
-    if constexpr (FORM == FP8_WGRAD) {
-      const int e = blockIdx.y;
-      int begin, end;
-      expert_rows(g.offsets, e, g.K, begin, end);
-      const int64_t slot = begin / kBlock + e;
-      t.K = end - begin;
-      t.A += slot * kBlock, t.B += slot * kBlock;
-      t.SA += slot * g.sa_block, t.SB += slot * g.sb_block;
-      const int64_t size = g.type == SGEMM_MI355_F32 ? 4 : 2;
-      t.C = (char*)g.C + (int64_t)e * g.strideC * size;
-    }
-    return true;
-  }
-}
 
 // A 128 x 128 tile by four waves of 64 x 64, slabs of one block staged through
 // registers: operands of any alignment.
@@ -215,10 +110,7 @@ __global__ void __launch_bounds__(256) fp8_gemm_kernel(Fp8Args g) {
       for (int q = 0; q < 4; ++q) {
         const int n = t.n0 + wn + 32 * j + 8 * q + 4 * h;
         const f32x4 v = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
-        const int64_t at = (int64_t)m * g.ldc + n;
-        if (g.type == SGEMM_MI355_F32) store4((float*)t.C + at, g.N - n, v, g.beta);
-        else if (g.type == SGEMM_MI355_BF16) store4((__hip_bfloat16*)t.C + at, g.N - n, v, g.beta);
-        else store4((__half*)t.C + at, g.N - n, v, g.beta);
+        store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
       }
   }
 }
@@ -226,24 +118,49 @@ __global__ void __launch_bounds__(256) fp8_gemm_kernel(Fp8Args g) {
 }  // namespace
 
 namespace {
-// The grid of BM x BN tiles: in the experts' form each expert's last tile of
-// rows may be short, and the rest's.
-int64_t grid_tiles(Fp8Form form, const Fp8Args& g, int bm, int bn) {
-  const int64_t tiles_n = (g.N + bn - 1) / bn;
-  return tiles_n * (form == FP8_EXPERTS ? (int64_t)g.M / bm + g.experts + 1 : (int64_t)((g.M + bm - 1) / bm));
+
+// The kernel for a call and its tile.
+struct Choice {
+  enum Kernel { STAGED, TILE, SKINNY } kernel;
+  bool wide;  // values widened to bf16
+  int bm, bn, threads;
+};
+
+Choice choose(Fp8Form form, const Fp8Args& g) {
+  const bool direct = (((uintptr_t)g.A | (uintptr_t)g.B | (uint64_t)g.lda | (uint64_t)g.ldb | (uint64_t)g.strideB) & 15) == 0 &&
+                      g.lda < 1 << 24 && g.ldb < 1 << 24 && (form == FP8_WGRAD || g.K >= 16);
+  if (!direct) return {Choice::STAGED, true, 128, 128, 256};
+  const bool wide = g.type == SGEMM_MI355_F32;
+  const int64_t rows = form == FP8_EXPERTS ? (2 * (int64_t)g.M + g.experts - 1) / g.experts : g.M;
+  if (form != FP8_WGRAD && rows <= 64) return {Choice::SKINNY, wide, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 16, 512};
+  // Widened values need more registers than a 64 x 128 wave tile leaves. FP8:
+  // a round of the chip is 256 tiles of 256 x 256 or 512 of 128 x 128, which
+  // takes 0.65 of the time (8192^3 with bf16 C: 496 us in 4 rounds, 641 in 8).
+  const int64_t batch = form == FP8_WGRAD ? g.experts : 1;
+  auto rounds = [&](int b, int64_t per_round) {
+    const int64_t tiles_m = form == FP8_EXPERTS ? g.M / b + (g.experts + 1) / 2 : (g.M + b - 1) / b;
+    return (double)((batch * tiles_m * ((g.N + b - 1) / b) + per_round - 1) / per_round);
+  };
+  const bool small = wide || 0.65 * rounds(128, 512) < rounds(256, 256);
+  return {Choice::TILE, wide, small ? 128 : 256, small ? 128 : 256, small ? 256 : 512};
 }
+
 }  // namespace
 
 bool fp8_launchable(Fp8Form form, const Fp8Args& g) {
-  return grid_tiles(form, g, 128, 128) * 256 <= (int64_t)UINT32_MAX && (form != FP8_WGRAD || g.experts <= kMaxGridY);
+  const Choice c = choose(form, g);
+  return grid_tiles(form, g, c.bm, c.bn) * c.threads <= (int64_t)UINT32_MAX && (form != FP8_WGRAD || g.experts <= kMaxGridY);
 }
 
 hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s) {
-  const void* kernel = form == FP8_EXPERTS ? (const void*)&fp8_gemm_kernel<FP8_EXPERTS>
-                       : form == FP8_WGRAD ? (const void*)&fp8_gemm_kernel<FP8_WGRAD>
-                                           : (const void*)&fp8_gemm_kernel<FP8_DENSE>;
-  return launch_with(kernel, dim3((unsigned)grid_tiles(form, g, 128, 128), form == FP8_WGRAD ? (unsigned)g.experts : 1u),
-                     dim3(256), g, s);
+  const Choice c = choose(form, g);
+  const dim3 grid((unsigned)grid_tiles(form, g, c.bm, c.bn), form == FP8_WGRAD ? (unsigned)g.experts : 1u);
+  const void* kernel = c.kernel == Choice::TILE     ? fp8_tile_kernel_for(form, c.wide, g.sb_rows == kBlock, c.bm)
+                       : c.kernel == Choice::SKINNY ? fp8_skinny_kernel_for(form, c.wide, c.bm)
+                       : form == FP8_EXPERTS        ? (const void*)&fp8_gemm_kernel<FP8_EXPERTS>
+                       : form == FP8_WGRAD          ? (const void*)&fp8_gemm_kernel<FP8_WGRAD>
+                                                    : (const void*)&fp8_gemm_kernel<FP8_DENSE>;
+  return launch_with(kernel, grid, dim3((unsigned)c.threads), g, s);
 }
 
 }  // namespace sgemm_impl
