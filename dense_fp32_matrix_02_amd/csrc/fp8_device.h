@@ -137,8 +137,8 @@ __device__ __forceinline__ bool find_tile(const Fp8Args& g, Tile& t) {
     int total = 0, last_end = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
       expert_tiles<BM>(g, e0, lane, begin, end, upto);
-      total += __shfl(upto, 63, 64);
-      last_end = __shfl(end, min(63, g.experts - 1 - e0), 64);
+      total += __builtin_amdgcn_readlane(upto, 63);
+      last_end = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
     }
     total += (g.M - last_end + BM - 1) / BM;
     const int64_t tiles = (int64_t)total * tiles_n;
@@ -154,13 +154,14 @@ __device__ __forceinline__ bool find_tile(const Fp8Args& g, Tile& t) {
       if (past != 0) {
         const int l = __builtin_ctzll(past);
         const int e = e0 + l;
-        t.m0 = __shfl(begin, l, 64) + (tm - before - __shfl(upto - own, l, 64)) * BM;
-        t.rows_a = __shfl(end, l, 64);
+        // The same in every lane: kept in scalar registers.
+        t.m0 = __builtin_amdgcn_readlane(begin, l) + (tm - before - __builtin_amdgcn_readlane(upto - own, l)) * BM;
+        t.rows_a = __builtin_amdgcn_readlane(end, l);
         t.B = g.B + (int64_t)e * g.strideB;
         t.SB = g.SB + (int64_t)e * g.stride_sb;
         return true;
       }
-      before += __shfl(upto, 63, 64);
+      before += __builtin_amdgcn_readlane(upto, 63);
     }
     // Rows no expert has: a product over nothing.
     t.m0 = last_end + (tm - before) * BM;

@@ -128,7 +128,7 @@ struct Choice {
 
 Choice choose(Fp8Form form, const Fp8Args& g) {
   const bool direct = (((uintptr_t)g.A | (uintptr_t)g.B | (uint64_t)g.lda | (uint64_t)g.ldb | (uint64_t)g.strideB) & 15) == 0 &&
-                      g.lda < 1 << 24 && g.ldb < 1 << 24 && (form == FP8_WGRAD || g.K >= 16);
+                      g.lda < 1 << 23 && g.ldb < 1 << 23;  // offsets within a tile fit 31 bits
   if (!direct) return {Choice::STAGED, true, 128, 128, 256};
   const bool wide = g.type == SGEMM_MI355_F32;
   const int64_t rows = form == FP8_EXPERTS ? (2 * (int64_t)g.M + g.experts - 1) / g.experts : g.M;

@@ -9,6 +9,14 @@ namespace {
 
 constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 
+// 16 bytes at base + offset (none beyond base + bytes) to LDS at lds + 16*lane.
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* base, int bytes, uint32_t offset, uint8_t* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass has no type for the buffer
+  const auto buffer = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00027000);  // plain bytes, range-checked
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (lds_void*)lds, 16, offset, 0, 0, 0);
+#endif
+}
+
 template <int BM, int BN, int WM, int WN>
 struct TileShape {
   static constexpr int NW = WM * WN, NT = 64 * NW;
@@ -32,29 +40,31 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int r16 = lane % 16, quad = lane / 16;
   const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
-  const int blocks = (t.K + kBlock - 1) / kBlock;
+  const int full = t.K / kBlock, tail = t.K % kBlock;  // whole blocks, and what is left
 
   // Direct loads: region q of this wave is rows 8*(q*NW + wave) .. +7; a lane
-  // brings one chunk, the same for all its regions.
+  // brings one chunk, the same for all its regions. Rows that do not exist lie
+  // past the buffers' ends and load as zeros.
   const int chunk = swz(8 * wave + lane / 8, lane % 8);
-  uint32_t src[S::REGIONS];  // its row's offset from the tile's first row
+  uint32_t src[S::REGIONS];
 #pragma unroll
   for (int q = 0; q < S::REGIONS; ++q) {
     const int r = 8 * (q * S::NW + wave) + lane / 8;
-    src[q] = q * S::NW * 8 < BM ? (uint32_t)(min(t.m0 + r, t.rows_a - 1) - t.m0) * (uint32_t)g.lda
-                                : (uint32_t)(min(t.n0 + r - BM, t.rows_b - 1) - t.n0) * (uint32_t)g.ldb;
+    src[q] = (q * S::NW * 8 < BM ? (uint32_t)r * (uint32_t)g.lda : (uint32_t)(r - BM) * (uint32_t)g.ldb) + 16 * chunk;
   }
   const uint8_t* a0 = t.A + (int64_t)t.m0 * g.lda;
   const uint8_t* b0 = t.B + (int64_t)t.n0 * g.ldb;
-  auto load = [&](int b, uint8_t* slab) __attribute__((always_inline)) {
-    // A chunk that is not whole is replaced once it has landed; its load
-    // brings the row's first 16 bytes.
-    const int k = b * kBlock + 16 * chunk;
-    const uint32_t at = k + 16 <= t.K ? k : 0;
+  const int a_bytes = (min(t.rows_a - t.m0, BM) - 1) * (int)g.lda + t.K;
+  const int b_bytes = (min(t.rows_b - t.n0, BN) - 1) * (int)g.ldb + t.K;
+  // Slab b, or nothing (and no memory traffic) when there is none.
+  auto load = [&](int b, bool there, uint8_t* slab) __attribute__((always_inline)) {
+    const int64_t k = (int64_t)b * kBlock;
+    const int a_left = there ? a_bytes - (int)k : 0, b_left = there ? b_bytes - (int)k : 0;
 #pragma unroll
-    for (int q = 0; q < S::REGIONS; ++q)
-      __builtin_amdgcn_global_load_lds((global_void*)((q * S::NW * 8 < BM ? a0 : b0) + (src[q] + at)),
-                                       (lds_void*)(slab + (q * S::NW + wave) * 1024), 16, 0, 0);
+    for (int q = 0; q < S::REGIONS; ++q) {
+      const bool a = q * S::NW * 8 < BM;
+      copy16_to_lds((a ? a0 : b0) + k, a ? a_left : b_left, src[q], slab + (q * S::NW + wave) * 1024);
+    }
   };
   // This thread's scales of block b: row tid (+ NT ...) of the slab.
   constexpr int NS = (ROWS + NT - 1) / NT;
@@ -76,89 +86,131 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
       if (ROWS % NT == 0 || tid + i * NT < ROWS) scale[tid + i * NT] = s[i];
   };
 
-  f32x4 acc[NF][MF] = {};
+  // Block b is multiplied in NF groups, one fragment of B with the wave's MF
+  // of A. While the matrix unit works on a group, the group before it enters
+  // the accumulators and the next fragment is read. Before the last group, all
+  // reads of slab b have been made and slab b + 1 has landed: there is the
+  // block's one barrier, after which slab b + 2 is asked for in slab b's place,
+  // and the last group's fragments of A are replaced by the next block's as
+  // soon as they are used, so that the next block begins without a pause.
+  // (Everything in one block, from its barrier to its last product, measured
+  // 496 us at 8192^3.) Scales go one block further ahead, through registers.
+  // There is no branch in a step: the compiler would move additions behind it.
+  f32x4 acc[NF][MF] = {}, p[MF] = {};
+  Frag<WIDE> fa[MF];
+  i32x4 raw[2][2];
+  float sa[MF] = {}, sa_before[MF] = {}, s[NS] = {};
+  f32x4 sv_before, sv = {}, sv_next = {};  // without TALL: B's scales of the groups before, at and after this one
   const int at0 = r16 * kBlock + 16 * swz(r16, quad), at1 = at0 ^ 64;
-  auto compute = [&](const uint8_t* slab, const float* scale) __attribute__((always_inline)) {
-    Frag<WIDE> fa[MF];
-    float sa[MF];
-    i32x4 raw[2][2];
-    const uint8_t* a = slab + wm * kBlock;
-    const uint8_t* b = slab + (BM + wn) * kBlock;
-    auto read_b = [&](int j) __attribute__((always_inline)) {
-      raw[j & 1][0] = *(const i32x4*)(b + j * 16 * kBlock + at0);
-      raw[j & 1][1] = *(const i32x4*)(b + j * 16 * kBlock + at1);
-    };
-    read_b(0);
+  auto read_a = [&](int i, const uint8_t* slab) __attribute__((always_inline)) {
+    const uint8_t* a = slab + (wm + 16 * i) * kBlock;
+    fa[i].set(*(const i32x4*)(a + at0), *(const i32x4*)(a + at1));
+  };
+  auto read_b = [&](int j, const uint8_t* slab, const float* scale) __attribute__((always_inline)) {
+    const uint8_t* b = slab + (BM + wn + 16 * j) * kBlock;
+    raw[j & 1][0] = *(const i32x4*)(b + at0), raw[j & 1][1] = *(const i32x4*)(b + at1);
+    if constexpr (!TALL) sv_next = *(const f32x4*)&scale[BM + wn + 16 * j + 4 * quad];
+  };
+  auto read_scales = [&](const float* scale) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      fa[i].set(*(const i32x4*)(a + i * 16 * kBlock + at0), *(const i32x4*)(a + i * 16 * kBlock + at1));
-      sa[i] = scale[wm + 16 * i + r16];
-    }
+    for (int i = 0; i < MF; ++i) sa[i] = scale[wm + 16 * i + r16];
     if constexpr (TALL) {
       const float sb = scale[BM + wn];
 #pragma unroll
       for (int i = 0; i < MF; ++i) sa[i] *= sb;
     }
-    // Products of fragment j of B with A's, while those of fragment j - 1
-    // enter the accumulators and fragment j + 1 is read.
-    f32x4 p[MF], sv = {};
+  };
+  auto add = [&](f32x4& c, int i, const float (&w)[MF], f32x4 v) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j <= NF; ++j) {
-      Frag<WIDE> fb;
-      if (j + 1 < NF) read_b(j + 1);
+    for (int x = 0; x < 4; ++x) c[x] = __builtin_fmaf(p[i][x], TALL ? w[i] : w[i] * v[x], c[x]);
+  };
+  auto step = [&](int b, uint8_t* cur, float* scur, uint8_t* next, float* snext) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      sv_before = sv, sv = sv_next;
+      if (j + 1 == NF) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        __syncthreads();
+        load(b + 2, b + 2 < full, cur);
+        keep_scale(s, scur);
+        load_scale(min(b + 3, full - 1), s);
+      }
       __builtin_amdgcn_sched_barrier(0);
-      if (j < NF) fb.set(raw[j & 1][0], raw[j & 1][1]);
+      Frag<WIDE> fb;
+      fb.set(raw[j & 1][0], raw[j & 1][1]);
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        if (j > 0)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) acc[j - 1][i][x] = __builtin_fmaf(p[i][x], TALL ? sa[i] : sa[i] * sv[x], acc[j - 1][i][x]);
-        if (j < NF) p[i] = block_product(fb, fa[i]);
+        if (j > 0) add(acc[j - 1][i], i, sa, sv_before);
+        else add(acc[NF - 1][i], i, sa_before, sv_before);
+        p[i] = block_product(fb, fa[i]);
+        // After the group's first product: the compiler waits for every
+        // outstanding LDS read before it.
+        if (i == 0 && j + 1 < NF) read_b(j + 1, cur, scur);
+        if (i == 0 && j + 1 == NF) read_b(0, next, snext);
+        if (j + 1 == NF) read_a(i, next);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (!TALL)
-        if (j < NF) sv = *(const f32x4*)&scale[BM + wn + 16 * j + 4 * quad];
     }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) sa_before[i] = sa[i];
+    read_scales(snext);
   };
-
-  // Step b: slab b has been asked for one step ago; slab b + 1 is asked for
-  // while it is multiplied. Scales go one step further ahead, through
-  // registers. `cur`/`next`: the stages.
-  float s[NS] = {};
-  auto step = [&](int b, uint8_t* cur, float* scur, uint8_t* next, float* snext) __attribute__((always_inline)) {
+  if (full > 0) load(0, true, slab0);
+  if (tail > 0) {
+    // The partial block, before the others: once it has landed, a thread
+    // replaces its row's chunks that are not whole.
+    float part[NS];
+    load(full, true, slab1);
+    load_scale(full, part);
+    keep_scale(part, scale1);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     __syncthreads();
-    const int left = t.K - b * kBlock;
-    if (left < kBlock) {  // the last, partial block: bytes from K on are zero
-      for (int r = tid; r < ROWS; r += NT) {
-        const bool isa = r < BM;
-        const int row = isa ? min(t.m0 + r, t.rows_a - 1) : min(t.n0 + r - BM, t.rows_b - 1);
-        const uint8_t* p = isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb;
-        for (int c = left / 16; c < 8; ++c)
-          *(i32x4*)(cur + r * kBlock + 16 * swz(r, c)) = load16(p, b * kBlock + 16 * c, t.K);
-      }
-      __syncthreads();
+    for (int r = tid; r < ROWS; r += NT) {
+      const bool isa = r < BM;
+      const int row = isa ? min(t.m0 + r, t.rows_a - 1) : min(t.n0 + r - BM, t.rows_b - 1);
+      const uint8_t* line = isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb;
+      *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, tail / 16)) = load16(line, full * kBlock + tail / 16 * 16, t.K);
+      for (int c = tail / 16 + 1; c < 8; ++c) *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, c)) = i32x4{0, 0, 0, 0};
     }
-    if (b + 1 < blocks) {
-      load(b + 1, next);
-      keep_scale(s, snext);
-      if (b + 2 < blocks) load_scale(b + 2, s);
+    __syncthreads();
+    read_scales(scale1);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) read_a(i, slab1);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      Frag<WIDE> fb;
+      read_b(j, slab1, scale1);
+      fb.set(raw[j & 1][0], raw[j & 1][1]);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) p[i] = block_product(fb, fa[i]);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) add(acc[j][i], i, sa, sv_next), p[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    compute(cur, scur);
-  };
-  if (blocks > 0) {
-    load(0, slab0);
-    float first[NS];
-    load_scale(0, first);
-    if (blocks > 1) load_scale(1, s);
-    keep_scale(first, scale0);
+  }
+  if (full > 0) {
+    load_scale(0, s);
+    keep_scale(s, scale0);
+    load_scale(min(2, full - 1), s);
+    float second[NS];
+    load_scale(min(1, full - 1), second);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    __syncthreads();
+    load(1, full > 1, slab1);
+    keep_scale(second, scale1);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) read_a(i, slab0);
+    read_b(0, slab0, scale0);
+    read_scales(scale0);
     int b = 0;
-    do {
+    for (; b + 2 <= full; b += 2) {
       step(b, slab0, scale0, slab1, scale1);
-      if (++b == blocks) break;
-      step(b, slab1, scale1, slab0, scale0);
-    } while (++b < blocks);
+      step(b + 1, slab1, scale1, slab0, scale0);
+    }
+    if (b < full) step(b, slab0, scale0, slab1, scale1);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) add(acc[NF - 1][i], i, sa_before, sv);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the workgroup
   }
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
