@@ -50,19 +50,44 @@ for _name, _types in _SIGNATURES.items():
     globals()[_name] = _bind(_name, _types)
 
 
-def _type_of(dtype, name):
-    import torch
+class _Library:
+    """The same functions without the wrappers' own cost: attribute `x` is C function sgemm_mi355_x, looked up once."""
 
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(dtype)
+    def __init__(self, signatures, results=()):
+        self._signatures, self._results = signatures, dict(results)
+
+    def __getattr__(self, name):
+        name_in_c = "sgemm_mi355_" + name
+        fn = getattr(load(), name_in_c)
+        fn.argtypes, fn.restype = self._signatures[name_in_c], self._results.get(name_in_c, _I)
+        setattr(self, name, fn)
+        return fn
+
+
+_c = _Library(_SIGNATURES)
+
+# The calls below are made for single tokens too, where the host's time counts:
+# what they ask torch for, they ask once.
+_types = {}
+
+
+def _type_of(dtype, name):
+    code = _types.get(dtype)
     if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+        import torch
+
+        _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+        code = _types.get(dtype)
+        if code is None:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16")
     return code
 
 
 def _stream_of(x, stream):
     import torch
 
-    return (torch.cuda.current_stream(x.device) if stream is None else stream).cuda_stream
+    # The handle of torch.cuda.current_stream without a Stream object.
+    return torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -78,9 +103,9 @@ def _empty(shape, dtype, device, stream):
 
 
 def _gpu(x, name, dtype=None):
-    if not x.is_cuda or (dtype is not None and x.dtype != dtype):
-        raise TypeError(f"{name} must be a {'' if dtype is None else str(dtype).replace('torch.', '') + ' '}GPU tensor")
-    return x
+    if x.is_cuda and (dtype is None or x.dtype == dtype):
+        return x
+    raise TypeError(f"{name} must be a {'' if dtype is None else str(dtype).replace('torch.', '') + ' '}GPU tensor")
 
 
 def _ints(x, name, length=None):
@@ -95,7 +120,7 @@ def _ints(x, name, length=None):
 
 def _check(rc, where):
     if rc != OK:
-        raise SgemmError(rc, where)
+        raise SgemmError(rc, "sgemm_mi355_" + where)
 
 
 def _blocks(n):
@@ -103,12 +128,12 @@ def _blocks(n):
 
 
 def _bytes_out(rows, cols, device, stream):
-    """An uninitialised e4m3 matrix whose row stride is a multiple of 16 bytes."""
+    """An uninitialised e4m3 matrix whose row stride is a multiple of 16 bytes, and that stride."""
     import torch
 
     pad = -cols % 16
     q = _empty((rows, cols + pad), torch.float8_e4m3fn, device, stream)
-    return q[:, :cols] if pad else q
+    return (q[:, :cols] if pad else q), max(cols + pad, 1)
 
 
 def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
@@ -128,19 +153,20 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
     if blocks:
         if index is not None:
             raise ValueError("tiles are quantised without an index")
-        Q = _bytes_out(rows, cols, X.device, stream)
-        S = _empty((_blocks(rows), _blocks(cols)), torch.float32, X.device, stream)
-        _check(sgemm_mi355_fp8_quantize_tiles(kind, rows, cols, X.data_ptr(), ldx, Q.data_ptr(), _ld(Q, "Q"),  # noqa: F821
-                                              S.data_ptr(), S.stride(0), S.stride(1), s), "sgemm_mi355_fp8_quantize_tiles")
+        Q, ldq = _bytes_out(rows, cols, X.device, stream)
+        tiles = _blocks(cols)
+        S = _empty((_blocks(rows), tiles), torch.float32, X.device, stream)
+        _check(_c.fp8_quantize_tiles(kind, rows, cols, X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), max(tiles, 1), 1, s),
+               "fp8_quantize_tiles")
         return Q, S
     n = rows if index is None else index.numel()
     at = None if index is None else _ints(index, "index")
-    Q = _bytes_out(n, cols, X.device, stream)
+    Q, ldq = _bytes_out(n, cols, X.device, stream)
     S = _empty((_blocks(cols), n), torch.float32, X.device, stream)
     if at is not None and n == 0:
         return Q, S.t()
-    _check(sgemm_mi355_fp8_quantize_rows(kind, rows, cols, X.data_ptr(), ldx, at, n, Q.data_ptr(), _ld(Q, "Q"),  # noqa: F821
-                                         S.data_ptr(), 1, max(n, 1), s), "sgemm_mi355_fp8_quantize_rows")
+    _check(_c.fp8_quantize_rows(kind, rows, cols, X.data_ptr(), ldx, at, n, Q.data_ptr(), ldq, S.data_ptr(), 1, max(n, 1), s),
+           "fp8_quantize_rows")
     return Q, S.t()
 
 
@@ -166,13 +192,12 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
         raise ValueError("offsets must have experts + 1 values")
     off = None if offsets is None else _ints(offsets, "offsets")
     width = n if offsets is None else 128 * (n // 128 + experts)
-    Q = _bytes_out(cols, width, X.device, stream)
+    Q, ldq = _bytes_out(cols, width, X.device, stream)
     S = _empty((_blocks(width), cols), torch.float32, X.device, stream)
     if at is not None and n == 0:
         at, rows = None, 0
-    _check(sgemm_mi355_fp8_quantize_cols(kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts,  # noqa: F821
-                                         Q.data_ptr(), _ld(Q, "Q"), S.data_ptr(), 1, max(cols, 1),
-                                         _stream_of(X, stream)), "sgemm_mi355_fp8_quantize_cols")
+    _check(_c.fp8_quantize_cols(kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts, Q.data_ptr(), ldq, S.data_ptr(), 1,
+                                max(cols, 1), _stream_of(X, stream)), "fp8_quantize_cols")
     return Q, S.t()
 
 
@@ -185,12 +210,15 @@ def _operand(Q, S, name, rows, cols, either=False):
         raise TypeError(f"{name} must be a float8_e4m3fn GPU tensor")
     if S.dtype != torch.float32 or not S.is_cuda:
         raise TypeError(f"the scales of {name} must be a float32 GPU tensor")
-    one = Q if Q.dim() == 2 else Q[0]
     per, blocks = S.shape[-2:]
-    if blocks != _blocks(cols) or per not in ((rows, _blocks(rows)) if either else (rows,)):
+    if blocks != _blocks(cols) or not (per == rows or (either and per == _blocks(rows))):
         raise ValueError(f"the scales of {name} must be {rows}{f' or {_blocks(rows)}' if either else ''} x {_blocks(cols)}, "
                          f"not {per} x {blocks}")
-    return Q.data_ptr(), _ld(one, name), S.data_ptr(), S.stride(-2), S.stride(-1), 1 if per == rows else 128
+    ld, step = Q.stride()[-2:]
+    if rows <= 1 or step != 1 or ld < cols:
+        ld = _ld(Q if Q.dim() == 2 else Q[0], name)
+    by_row, by_block = S.stride()[-2:]
+    return Q.data_ptr(), max(ld, 1), S.data_ptr(), by_row, by_block, 1 if per == rows else 128
 
 
 def _result(C, shape, dtype, device, beta, stream):
@@ -198,7 +226,7 @@ def _result(C, shape, dtype, device, beta, stream):
         if beta != 0.0:
             raise ValueError("beta != 0 needs an input C")
         return _empty(shape, dtype, device, stream)
-    if tuple(C.shape) != tuple(shape):
+    if C.shape != shape:
         raise ValueError(f"C must be {' x '.join(map(str, shape))}")
     return _gpu(C, "C")
 
@@ -221,8 +249,8 @@ def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, stream=None
     a = _operand(A, SA, "A", M, K)
     b = _operand(B, SB, "B", N, K, either=True)
     C = _result(C, (M, N), dtype or torch.bfloat16, A.device, beta, stream)
-    _check(sgemm_mi355_fp8_gemm(_type_of(C.dtype, "C"), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"),  # noqa: F821
-                                _stream_of(A, stream)), "sgemm_mi355_fp8_gemm")
+    _check(_c.fp8_gemm(_type_of(C.dtype, "C"), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)),
+           "fp8_gemm")
     return C
 
 
@@ -244,9 +272,8 @@ def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, stream=None):
     a = _operand(A, SA, "A", R, K)
     b = _operand(B, SB, "B", N, K, either=True)
     C = _result(C, (R, N), dtype or torch.bfloat16, A.device, 0.0, stream)
-    _check(sgemm_mi355_fp8_gemm_experts(_type_of(C.dtype, "C"), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5],  # noqa: F821
-                                        SB.stride(0), b[5], off, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)),
-           "sgemm_mi355_fp8_gemm_experts")
+    _check(_c.fp8_gemm_experts(_type_of(C.dtype, "C"), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5], off,
+                               C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)), "fp8_gemm_experts")
     return C
 
 
@@ -277,7 +304,6 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
     if C.dim() != 3:
         raise ValueError("C must be experts x M x N")
     ldc = _ld(C[0], "C")
-    _check(sgemm_mi355_fp8_gemm_experts_wgrad(_type_of(C.dtype, "C"), rows, M, N, E, *a[:5], *b[:5], off, beta,  # noqa: F821
-                                              C.data_ptr(), ldc, C.stride(0), _stream_of(A, stream)),
-           "sgemm_mi355_fp8_gemm_experts_wgrad")
+    _check(_c.fp8_gemm_experts_wgrad(_type_of(C.dtype, "C"), rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
+                                     C.stride(0), _stream_of(A, stream)), "fp8_gemm_experts_wgrad")
     return C

@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 
 from ._binding import _ld
-from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _P, _stream_of, _type_of
+from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _Library, _P, _stream_of, _type_of
 
 SOFTMAX, SIGMOID = 0, 1
 MAX_EXPERTS, MAX_CHOICES = 1024, 32
@@ -22,9 +22,11 @@ _SIGNATURES = {
     "sgemm_mi355_route_combine": [_I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P],
     "sgemm_mi355_route_combine_backward": [_I, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _I, _P, _P],
 }
+_SIGNATURES["sgemm_mi355_route_plan_workspace_size"] = [_I, _I, _I]
+_RESULTS = {"sgemm_mi355_route_plan_workspace_size": _SIZE}
 for _name, _types in _SIGNATURES.items():
-    globals()[_name] = _bind(_name, _types)
-sgemm_mi355_route_plan_workspace_size = _bind("sgemm_mi355_route_plan_workspace_size", [_I, _I, _I], _SIZE)
+    globals()[_name] = _bind(_name, _types, _RESULTS.get(_name, _I))
+_c = _Library(_SIGNATURES, _RESULTS)
 
 
 def _score(score):
@@ -37,7 +39,7 @@ def _score(score):
 def _dense(x, name, dtype, shape):
     """Address of a dense GPU tensor of this dtype and shape."""
     _gpu(x, name, dtype)
-    if tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+    if x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be a dense {' x '.join(map(str, shape))} tensor")
     return x.data_ptr()
 
@@ -62,9 +64,9 @@ def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1,
     at = None if bias is None else _dense(bias, "bias", torch.float32, (experts,))
     weights = _empty((tokens, max(k, 0)), torch.float32, logits.device, stream)
     ids = _empty((tokens, max(k, 0)), torch.int32, logits.device, stream)
-    _check(sgemm_mi355_route(kind, tokens, experts, logits.data_ptr(), ld, at, how, groups, top_groups, k,  # noqa: F821
+    _check(_c.route(kind, tokens, experts, logits.data_ptr(), ld, at, how, groups, top_groups, k,
                              int(bool(renorm)), scale, weights.data_ptr(), ids.data_ptr(), _stream_of(logits, stream)),
-           "sgemm_mi355_route")
+           "route")
     return weights, ids
 
 
@@ -81,9 +83,9 @@ def route_backward(logits, experts, dweights, *, score: str = "softmax", renorm:
     ids = _dense(experts, "experts", torch.int32, (tokens, k))
     dw = _dense(dweights, "dweights", torch.float32, (tokens, k))
     out = _empty((tokens, count), torch.float32, logits.device, stream)
-    _check(sgemm_mi355_route_backward(kind, tokens, count, logits.data_ptr(), ld, ids, dw, how, k,  # noqa: F821
+    _check(_c.route_backward(kind, tokens, count, logits.data_ptr(), ld, ids, dw, how, k,
                                       int(bool(renorm)), scale, out.data_ptr(), max(count, 1), _stream_of(logits, stream)),
-           "sgemm_mi355_route_backward")
+           "route_backward")
     return out
 
 
@@ -101,15 +103,15 @@ def route_plan(experts, num_experts: int, *, stream=None):
         raise ValueError("experts must be tokens x k")
     tokens, k = experts.shape
     ids = _dense(experts, "experts", torch.int32, (tokens, k))
-    need = sgemm_mi355_route_plan_workspace_size(tokens, k, num_experts)
+    need = _c.route_plan_workspace_size(tokens, k, num_experts)
     # one allocation for the three results and one for the workspace
     offsets = _empty((max(num_experts, 0) + 1,), torch.int32, experts.device, stream)
     rows = _empty((tokens * k,), torch.int32, experts.device, stream)
     place = _empty((tokens, k), torch.int32, experts.device, stream)
     room = _empty((need // 4,), torch.int32, experts.device, stream)
-    _check(sgemm_mi355_route_plan(tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),  # noqa: F821
+    _check(_c.route_plan(tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),
                                   place.data_ptr(), room.data_ptr(), need, _stream_of(experts, stream)),
-           "sgemm_mi355_route_plan")
+           "route_plan")
     return offsets, rows, place
 
 
@@ -128,8 +130,8 @@ def route_combine(Z, place, weights, Y=None, *, stream=None):
     _gpu(Y, "Y", Z.dtype)
     if tuple(Y.shape) != (tokens, cols):
         raise ValueError("Y must be tokens x cols")
-    _check(sgemm_mi355_route_combine(kind, tokens, k, rows, cols, Z.data_ptr(), ldz, at, w, Y.data_ptr(), _ld(Y, "Y"),  # noqa: F821
-                                     _stream_of(Z, stream)), "sgemm_mi355_route_combine")
+    _check(_c.route_combine(kind, tokens, k, rows, cols, Z.data_ptr(), ldz, at, w, Y.data_ptr(), _ld(Y, "Y"),
+                                     _stream_of(Z, stream)), "route_combine")
     return Y
 
 
@@ -151,7 +153,7 @@ def route_combine_backward(dY, Z, place, weights, *, stream=None):
     at, w = _dense(place, "place", torch.int32, (tokens, k)), _dense(weights, "weights", torch.float32, (tokens, k))
     dZ = _empty((rows, cols), Z.dtype, Z.device, stream)
     dw = _empty((tokens, k), torch.float32, Z.device, stream)
-    _check(sgemm_mi355_route_combine_backward(kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,  # noqa: F821
+    _check(_c.route_combine_backward(kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,
                                               dZ.data_ptr(), max(cols, 1), dw.data_ptr(), _stream_of(Z, stream)),
-           "sgemm_mi355_route_combine_backward")
+           "route_combine_backward")
     return dZ, dw

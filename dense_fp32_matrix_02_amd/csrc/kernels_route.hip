@@ -6,153 +6,193 @@
 namespace sgemm_impl {
 namespace {
 
+constexpr int kNone = 0x7FFFFFFF;
+
 // ---- routing ------------------------------------------------------------------
 //
-// One wave has one token; lane l holds experts l, l + 64, ... (V of them).
-// Scores and choice values are FP64: two experts whose values differ by less
-// than FP32 tells apart are still ordered as the formula orders them, and
-// FP64 vector instructions run at the rate of FP32 ones here.
+// One wave has one token; lane l holds experts l*V .. l*V + V-1. Scores and
+// choice values are FP64: two experts whose values differ by less than FP32
+// tells apart are still ordered as the formula orders them, and FP64 vector
+// instructions run at the rate of FP32 ones here.
+//
+// Reductions over the wave run in the vector unit (DPP), not as shuffles
+// through LDS: 8192 tokens of 256 experts, 8 of 4 of 8 groups, took 52 us with
+// shuffles. A choice value is compared as a 64-bit key whose halves are
+// reduced one after the other: the largest first half, then the largest second
+// half among the lanes that have it, then the first lane that has both.
 
 template <class T>
 __device__ __forceinline__ double to_f64(T x) { return (double)to_f32(x); }
 
+// x of another lane by a DPP control, `none` where there is no such lane.
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t x, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, CONTROL, ROWS, 0xF, false);
+}
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ double dpp(double x, double none) {
+  const uint64_t b = __double_as_longlong(x), n = __double_as_longlong(none);
+  const uint32_t lo = dpp<CONTROL, ROWS>((uint32_t)b, (uint32_t)n), hi = dpp<CONTROL, ROWS>((uint32_t)(b >> 32), (uint32_t)(n >> 32));
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+// f over all lanes, in every lane: shifts by 1, 2, 4, 8 within rows of 16 lanes,
+// then rows 0 to 1 and 2 to 3, then 1 to 3; the last lane has it all.
+template <class X, class F>
+__device__ __forceinline__ X wave_reduce(X x, X none, F&& f) {
+  x = f(x, dpp<0x111, 0xF>(x, none));
+  x = f(x, dpp<0x112, 0xF>(x, none));
+  x = f(x, dpp<0x114, 0xF>(x, none));
+  x = f(x, dpp<0x118, 0xF>(x, none));
+  x = f(x, dpp<0x142, 0xA>(x, none));
+  return f(x, dpp<0x143, 0xC>(x, none));
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)x, lane); }
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t b = __double_as_longlong(x);
+  const uint32_t lo = lane_value((uint32_t)b, lane), hi = lane_value((uint32_t)(b >> 32), lane);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ uint32_t wave_most(uint32_t x) {
+  return lane_value(wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }), 63);
+}
 __device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d, 64);
-  return x;
+  return lane_value(wave_reduce(x, 0.0, [](double a, double b) { return a + b; }), 63);
 }
 __device__ __forceinline__ double wave_max(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x = fmax(x, __shfl_xor(x, d, 64));
-  return x;
+  return lane_value(wave_reduce(x, (double)-INFINITY, [](double a, double b) { return fmax(a, b); }), 63);
+}
+
+// Orders like the number, NaN as minus infinity; never 0, which stands for none.
+__device__ __forceinline__ uint64_t key_of(double x) {
+  if (!(x == x)) x = -INFINITY;
+  const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);  // -0 is 0
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+// The lanes that hold the largest key.
+__device__ __forceinline__ uint64_t lanes_of_most(uint64_t key) {
+  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+  const uint32_t most_hi = wave_most(hi);
+  const uint32_t most_lo = wave_most(hi == most_hi ? lo : 0);
+  return __ballot(hi == most_hi && lo == most_lo);
 }
 
 // Scores of the wave's token; experts past the last get 0. A NaN logit of a
 // softmax makes the whole row NaN.
 template <class T, int SCORE, int V>
 __device__ __forceinline__ void scores(const T* row, int experts, int lane, double (&s)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lane * V + v;
+    s[v] = e < experts ? to_f64(row[e]) : -INFINITY;
+  }
   if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
-    double most = -INFINITY;
+    double most = s[0], sum = 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 64 * v;
-      s[v] = e < experts ? to_f64(row[e]) : -INFINITY;
-      most = fmax(most, s[v]);
-    }
+    for (int v = 1; v < V; ++v) most = fmax(most, s[v]);
     most = wave_max(most);
-    double sum = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      s[v] = lane + 64 * v < experts ? exp(s[v] - most) : 0.0;
+      s[v] = lane * V + v < experts ? exp(s[v] - most) : 0.0;
       sum += s[v];
     }
     sum = wave_sum(sum);
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = lane + 64 * v < experts ? s[v] / sum : 0.0;
+    for (int v = 0; v < V; ++v) s[v] = lane * V + v < experts ? s[v] / sum : 0.0;
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 64 * v;
-      s[v] = e < experts ? 1.0 / (1.0 + exp(-to_f64(row[e]))) : 0.0;
+    for (int v = 0; v < V; ++v) s[v] = 1.0 / (1.0 + exp(-s[v]));
+  }
+}
+
+// Bit v: the lane's expert v is in one of the top_groups strongest groups.
+template <int V>
+__device__ __forceinline__ uint32_t kept_experts(const RouteArgs& a, const double (&c)[V], int lane, double* row) {
+  const int size = a.experts / a.groups;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (lane * V + v < a.experts) row[lane * V + v] = c[v];
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  // Lane l finds the strengths of groups l, l + 64, ..: each lane begins at a
+  // place of its own in its group, so that the lanes read different banks.
+  uint64_t strength[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int g = lane + 64 * v;
+    strength[v] = 0;
+    if (g < a.groups) {
+      double one = -INFINITY, two = -INFINITY;
+      int at = g % size;
+      for (int i = 0; i < size; ++i) {
+        const double x = row[g * size + at];
+        two = fmax(two, fmin(one, x));
+        one = fmax(one, x);
+        at = at + 1 == size ? 0 : at + 1;
+      }
+      strength[v] = key_of(size > 1 ? one + two : one);
     }
   }
-}
-
-// (value, index) pairs: the larger value first, of equal values the lower
-// index. Values are never NaN here.
-__device__ __forceinline__ bool before(double a, int ia, double b, int ib) {
-  return a > b || (a == b && ia < ib);
-}
-__device__ __forceinline__ void wave_first(double& x, int& i) {
+  int group[V];
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double y = __shfl_xor(x, d, 64);
-    const int j = __shfl_xor(i, d, 64);
-    if (before(y, j, x, i)) x = y, i = j;
+  for (int v = 0; v < V; ++v) group[v] = (lane * V + v) / size;
+  uint32_t kept = 0;
+  for (int r = 0; r < a.top_groups; ++r) {
+    uint64_t best = 0;
+    int mine = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (strength[v] > best) best = strength[v], mine = lane + 64 * v;
+    const uint64_t lanes = lanes_of_most(best);
+    int g = (int)lane_value((uint32_t)mine, __builtin_ctzll(lanes));
+    // More than 64 groups: of equal ones the lowest need not be the first lane's.
+    if (a.groups > 64) g = kNone - (int)wave_most(lanes >> lane & 1 ? (uint32_t)(kNone - mine) : 0u);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (lane + 64 * v == g) strength[v] = 0;
+      if (group[v] == g) kept |= 1u << v;
+    }
   }
+  return kept;
 }
-
-// The index that goes with no expert: behind every expert of equal value.
-constexpr int kNone = 0x7FFFFFFF;
 
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
+  __shared__ double rows[4][64 * V];  // choice values, for the groups
   const int lane = threadIdx.x % 64;
   const int token = blockIdx.x * 4 + threadIdx.x / 64;
   if (token >= a.tokens) return;  // whole waves
   double s[V], c[V];
   scores<T, SCORE, V>((const T*)a.logits + (int64_t)token * a.ld, a.experts, lane, s);
-  uint32_t open = 0;  // bit v: the lane's expert v can be chosen
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = lane + 64 * v;
-    if (e < a.experts) open |= 1u << v;
+    const int e = lane * V + v;
     c[v] = s[v];
     if (a.bias != nullptr && e < a.experts) c[v] += (double)a.bias[e];
     if (!(c[v] == c[v])) c[v] = -INFINITY;  // NaN ranks as minus infinity
   }
-  if (a.groups > 1) {
-    const int size = a.experts / a.groups;
-    // A group's strength, on the lane that has its number (modulo 64).
-    double strength[V];
+  uint32_t open = 0xFFFFFFFF;
+  if (a.groups > 1) open = kept_experts<V>(a, c, lane, rows[threadIdx.x / 64]);
+  uint64_t key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) strength[v] = -INFINITY;
-    for (int g = 0; g < a.groups; ++g) {
-      double one = -INFINITY, two = -INFINITY;
-      int at = kNone;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = lane + 64 * v;
-        if (e / size == g && e < a.experts && before(c[v], e, one, at)) one = c[v], at = e;
-      }
-      wave_first(one, at);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = lane + 64 * v;
-        if (e / size == g && e < a.experts && e != at) two = fmax(two, c[v]);
-      }
-      two = wave_max(two);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (lane + 64 * v == g) {
-          const double x = size > 1 ? one + two : one;
-          strength[v] = x == x ? x : -INFINITY;  // infinities of both signs
-        }
-    }
-    uint32_t kept = 0;
-    uint32_t left = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane + 64 * v < a.groups) left |= 1u << v;
-    for (int r = 0; r < a.top_groups; ++r) {
-      double x = -INFINITY;
-      int i = kNone;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if ((left >> v & 1) && before(strength[v], lane + 64 * v, x, i)) x = strength[v], i = lane + 64 * v;
-      wave_first(x, i);
-      if (i % 64 == lane) left &= ~(1u << (i / 64));
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if ((lane + 64 * v) / size == i) kept |= 1u << v;
-    }
-    open &= kept;
-  }
+  for (int v = 0; v < V; ++v) key[v] = lane * V + v < a.experts && (open >> v & 1) ? key_of(c[v]) : 0;
   double total = 0.0, mine = 0.0;
   int my_id = 0;
   for (int k = 0; k < a.choices; ++k) {
-    double x = -INFINITY, w = 0.0;
-    int i = kNone;
+    uint64_t best = key[0];
+    int at = 0;
+    double w = s[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v)
+      if (key[v] > best) best = key[v], at = v, w = s[v];
+    const int owner = __builtin_ctzll(lanes_of_most(best));
+    w = lane_value(w, owner);
+    const int id = owner * V + (int)lane_value((uint32_t)at, owner);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if ((open >> v & 1) && before(c[v], lane + 64 * v, x, i)) x = c[v], i = lane + 64 * v, w = s[v];
-    const int local = i;
-    wave_first(x, i);
-    const uint64_t owner = __ballot(local == i);
-    w = __shfl(w, __builtin_ctzll(owner), 64);
-    if (local == i) open &= ~(1u << (i / 64));
+      if (lane * V + v == id) key[v] = 0;
     total += w;
-    if (lane == k) mine = w, my_id = i;
+    if (lane == k) mine = w, my_id = id;
   }
   if (lane < a.choices) {
     double w = mine;
@@ -162,37 +202,47 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   }
 }
 
+// Lane k has choice k. A sigmoid's gradient needs the chosen experts' scores
+// alone; a softmax's needs the whole row.
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
+  __shared__ double rows[4][SCORE == SGEMM_MI355_SOFTMAX ? 64 * V : 1];
   const int lane = threadIdx.x % 64;
   const int token = blockIdx.x * 4 + threadIdx.x / 64;
   if (token >= a.tokens) return;
-  double s[V], ds[V];
-  scores<T, SCORE, V>((const T*)a.logits + (int64_t)token * a.ld, a.experts, lane, s);
-#pragma unroll
-  for (int v = 0; v < V; ++v) ds[v] = 0.0;
-  // total = S, dot = sum of dw_m s_m over the chosen
-  double total = 0.0, dot = 0.0;
-  for (int k = 0; k < a.choices; ++k) {
-    const int id = a.ids_in[(int64_t)token * a.choices + k];
-    if ((unsigned)id >= (unsigned)a.experts) continue;
-    double w = 0.0;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (id / 64 == v) w = s[v];
-    w = __shfl(w, id % 64, 64);
-    total += w;
-    dot += w * (double)a.dweights[(int64_t)token * a.choices + k];
+  const T* logits = (const T*)a.logits + (int64_t)token * a.ld;
+  int id = -1;
+  double dw = 0.0, w = 0.0;
+  if (lane < a.choices) {
+    id = a.ids_in[(int64_t)token * a.choices + lane];
+    if ((unsigned)id >= (unsigned)a.experts) id = -1;
+    else dw = (double)a.dweights[(int64_t)token * a.choices + lane];
   }
-  if (!a.renorm) total = 1.0, dot = 0.0;
+  double s[V];
+  if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
+    scores<T, SCORE, V>(logits, a.experts, lane, s);
+    double* row = rows[threadIdx.x / 64];
+#pragma unroll
+    for (int v = 0; v < V; ++v) row[lane * V + v] = s[v];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (id >= 0) w = row[id];
+  } else if (id >= 0) {
+    w = 1.0 / (1.0 + exp(-to_f64(logits[id])));
+  }
+  // total = S, dot = sum of dw_m s_m over the chosen
+  double total = 1.0, dot = 0.0;
+  if (a.renorm) total = wave_sum(w), dot = wave_sum(w * dw);
+  double d = id < 0 || total == 0.0 ? 0.0 : (double)a.scale * (dw - dot / total) / total;
+  if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * (1.0 - w);
+  double ds[V] = {};
   for (int k = 0; k < a.choices; ++k) {
-    const int id = a.ids_in[(int64_t)token * a.choices + k];
-    if ((unsigned)id >= (unsigned)a.experts) continue;
-    const double d = total == 0.0 ? 0.0
-        : (double)a.scale * ((double)a.dweights[(int64_t)token * a.choices + k] - dot / total) / total;
+    const int e = (int)lane_value((uint32_t)id, k);
+    const double x = lane_value(d, k);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (id == lane + 64 * v) ds[v] += d;
+      if (e == lane * V + v) ds[v] += x;
   }
   if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
     double inner = 0.0;
@@ -201,61 +251,85 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     inner = wave_sum(inner);
 #pragma unroll
     for (int v = 0; v < V; ++v) ds[v] = s[v] * (ds[v] - inner);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) ds[v] = ds[v] * s[v] * (1.0 - s[v]);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (lane + 64 * v < a.experts) a.dlogits[(int64_t)token * a.ldd + lane + 64 * v] = (float)ds[v];
+    if (lane * V + v < a.experts) a.dlogits[(int64_t)token * a.ldd + lane * V + v] = (float)ds[v];
 }
 
 // ---- the order of the experts' rows ---------------------------------------------
 //
 // A counting sort that keeps the order of equal ids. The entries are cut into
-// runs of kPlanRun. The first kernel counts each run's entries of each expert;
-// in the second every run adds up the counts before it and places its own.
-// Ids outside the experts count as expert number `experts`, the last.
+// runs of kPlanRun, one to a workgroup of 16 waves with 1/16 of the run each.
+// With several runs the first kernel counts each run's entries of each expert.
+// In the second a run adds up the counts before it, and each of its waves,
+// having counted its own entries, knows where its first of each expert goes;
+// then the waves place theirs without waiting for each other. Ids outside the
+// experts count as expert number `experts`, the last.
 
 __device__ __forceinline__ int expert_of(const PlanArgs& p, int entry) {
   const int id = p.ids[entry];
   return (unsigned)id < (unsigned)p.experts ? id : p.experts;
 }
 
-__global__ void __launch_bounds__(256) plan_count_kernel(PlanArgs p) {
+__global__ void __launch_bounds__(1024) plan_count_kernel(PlanArgs p) {
   __shared__ int count[SGEMM_MI355_MAX_EXPERTS + 1];
-  for (int e = threadIdx.x; e <= p.experts; e += 256) count[e] = 0;
+  for (int e = threadIdx.x; e <= p.experts; e += 1024) count[e] = 0;
   __syncthreads();
   const int first = blockIdx.x * kPlanRun;
-  for (int i = first + threadIdx.x; i < min(first + kPlanRun, p.entries); i += 256) atomicAdd(&count[expert_of(p, i)], 1);
+#pragma unroll
+  for (int i = 0; i < kPlanRun / 1024; ++i) {
+    const int entry = first + i * 1024 + threadIdx.x;
+    if (entry < p.entries) atomicAdd(&count[expert_of(p, entry)], 1);
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e <= p.experts; e += 256) p.counts[(int64_t)blockIdx.x * (p.experts + 1) + e] = count[e];
+  for (int e = threadIdx.x; e <= p.experts; e += 1024) p.counts[(int64_t)blockIdx.x * (p.experts + 1) + e] = count[e];
 }
 
-// Lanes of the wave that have the same key (of keys under 2048).
-__device__ __forceinline__ uint64_t same_key(int key, bool active) {
+// Lanes of the wave that have the same key (of `bits` bits).
+__device__ __forceinline__ uint64_t same_key(int key, bool active, int bits) {
   uint64_t same = __ballot(active);
-#pragma unroll
-  for (int b = 0; b < 11; ++b) {
+  for (int b = 0; b < bits; ++b) {
     const uint64_t ones = __ballot(active && (key >> b & 1));
     same &= (key >> b & 1) ? ones : ~ones;
   }
   return same;
 }
 
-__global__ void __launch_bounds__(256) plan_place_kernel(PlanArgs p, int runs) {
-  __shared__ int next[SGEMM_MI355_MAX_EXPERTS + 1];  // the row of the run's next entry of each expert
-  __shared__ int wave_total[4];
-  const int t = threadIdx.x, lane = t % 64, wave = t / 64;
+__global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) {
+  constexpr int WAVES = 16, PER = kPlanRun / WAVES / 64;  // entries per lane
+  // next[w][e]: first the wave's entries of expert e, then the row of its next one.
+  __shared__ int next[WAVES * (SGEMM_MI355_MAX_EXPERTS + 1)];
+  __shared__ int wave_total[WAVES];
+  const int t = threadIdx.x, lane = t % 64, wave = t / 64, width = p.experts + 1;
+  for (int i = t; i < WAVES * width; i += 1024) next[i] = 0;
+  __syncthreads();
+  const int first = blockIdx.x * kPlanRun + wave * (kPlanRun / WAVES);
+  int expert[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int entry = first + i * 64 + lane;
+    expert[i] = entry < p.entries ? expert_of(p, entry) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (expert[i] >= 0) atomicAdd(&next[wave * width + expert[i]], 1);
+  __syncthreads();
   int carry = 0;  // entries of all experts before this turn's
-  for (int e0 = 0; e0 <= p.experts; e0 += 256) {
+  for (int e0 = 0; e0 < width; e0 += 1024) {
     const int e = e0 + t;
-    int here = 0, all = 0;
-    if (e <= p.experts) {
-      for (int r = 0; r < runs; ++r) {
-        const int c = p.counts[(int64_t)r * (p.experts + 1) + e];
-        all += c;
-        if (r < (int)blockIdx.x) here += c;
+    int here = 0, all = 0;  // entries of expert e in earlier runs, and in all
+    if (e < width) {
+      if (runs == 1) {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) all += next[w * width + e];
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < runs; ++r) {
+          const int c = p.counts[(int64_t)r * width + e];
+          all += c;
+          if (r < (int)blockIdx.x) here += c;
+        }
       }
     }
     int upto = all;
@@ -267,86 +341,121 @@ __global__ void __launch_bounds__(256) plan_place_kernel(PlanArgs p, int runs) {
     if (lane == 63) wave_total[wave] = upto;
     __syncthreads();
     int base = carry;
-    for (int w = 0; w < wave; ++w) base += wave_total[w];
-    if (e <= p.experts) {
-      next[e] = base + upto - all + here;
-      if (blockIdx.x == 0) p.offsets[e] = base + upto - all;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      base += w < wave ? wave_total[w] : 0;
+      carry += wave_total[w];
     }
-    carry += wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
+    if (e < width) {
+      if (blockIdx.x == 0) p.offsets[e] = base + upto - all;
+      int row = base + upto - all + here;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const int c = next[w * width + e];
+        next[w * width + e] = row;
+        row += c;
+      }
+    }
     __syncthreads();
   }
-  const int first = blockIdx.x * kPlanRun;
-  const int last = min(first + kPlanRun, p.entries);
-  for (int i0 = first; i0 < last; i0 += 256) {
-    const int i = i0 + t;
-    const bool active = i < last;
-    const int e = active ? expert_of(p, i) : 0;
-    const uint64_t same = same_key(e, active);
+  const int bits = 32 - __builtin_clz(width);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = expert[i], entry = first + i * 64 + lane;
+    const uint64_t same = same_key(e, e >= 0, bits);
     const int rank = __popcll(same & ((1ull << lane) - 1));
     int row = 0;
-    for (int w = 0; w < 4; ++w) {  // the waves in order
-      if (wave == w && active) {
-        row = next[e] + rank;
-      }
-      __syncthreads();
-      if (wave == w && active && rank == 0) next[e] += __popcll(same);
-      __syncthreads();
-    }
-    if (active) {
-      p.place[i] = row;
-      p.row_token[row] = i / p.choices;
+    if (e >= 0) row = next[wave * width + e] + rank;
+    __builtin_amdgcn_wave_barrier();  // the wave's reads before its writes
+    if (e >= 0 && rank == 0) next[wave * width + e] = row + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0) {
+      p.place[entry] = row;
+      p.row_token[row] = entry / p.choices;
     }
   }
 }
 
 // ---- the rows' return --------------------------------------------------------------
+//
+// Bound by the bytes of Z (and dZ). A place and a weight are the same for a
+// whole wave, so they are scalars, and kRows rows of Z are asked for at once.
 
-// A thread has eight columns of one token and adds the choices in order.
+constexpr int kRows = 8;
+
+// A wave has 512 columns of one token and adds the choices in order.
 template <class T>
-__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a, int chunks) {
-  const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t token = item / chunks;
+__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a, int slabs) {
+  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t token = item / slabs;
   if (token >= a.tokens) return;
-  const int col = (int)(item - token * chunks) * 8;
+  const int col = (int)(item - token * slabs) * 512 + 8 * (threadIdx.x % 64);
   const int valid = a.cols - col;
+  const int* place = a.place + token * a.choices;
+  const float* weights = a.weights + token * a.choices;
   float y[8] = {};
-  for (int j = 0; j < a.choices; ++j) {
-    const int row = a.place[token * a.choices + j];
-    if ((unsigned)row >= (unsigned)a.rows) continue;
-    const float w = a.weights[token * a.choices + j];
-    float z[8];
-    load8((const T*)a.Z + (int64_t)row * a.ldz + col, valid, z);
+  for (int j0 = 0; j0 < a.choices; j0 += kRows) {
+    float z[kRows][8], w[kRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(w, z[i], y[i]);
+    for (int j = 0; j < kRows; ++j) {
+      const int row = j0 + j < a.choices ? place[j0 + j] : -1;
+      const bool there = (unsigned)row < (unsigned)a.rows;
+      w[j] = there ? weights[j0 + j] : 0.0f;
+      load8((const T*)a.Z + (int64_t)(there ? row : 0) * a.ldz + col, there ? valid : 0, z[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(w[j], z[j][i], y[i]);
   }
   store8((T*)a.Y + token * a.ldy + col, valid, y);
 }
 
-// A wave has one entry (token, choice).
+// A workgroup has one token.
 template <class T>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs a) {
-  const int lane = threadIdx.x % 64;
-  const int64_t entry = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-  if (entry >= (int64_t)a.tokens * a.choices) return;
-  const int row = a.place[entry];
-  float dot = 0.0f;
-  if ((unsigned)row < (unsigned)a.rows) {
-    const float w = a.weights[entry];
-    const T* dy = (const T*)a.dY + entry / a.choices * a.lddy;
-    const T* z = (const T*)a.Z + (int64_t)row * a.ldz;
-    T* dz = (T*)a.dZ + (int64_t)row * a.lddz;
-    for (int col = 8 * lane; col < a.cols; col += 512) {
-      float g[8], x[8];
-      load8(dy + col, a.cols - col, g);
-      load8(z + col, a.cols - col, x);
+  __shared__ float dots[4][kRows];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t token = blockIdx.x;
+  const int* place = a.place + token * a.choices;
+  const float* weights = a.weights + token * a.choices;
+  const T* dy = (const T*)a.dY + token * a.lddy;
+  for (int j0 = 0; j0 < a.choices; j0 += kRows) {
+    float dot[kRows] = {};
+    for (int col = 8 * threadIdx.x; col < a.cols; col += 2048) {
+      const int valid = a.cols - col;
+      float g[8], z[kRows][8];
+      load8(dy + col, valid, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g[i], x[i], dot), g[i] *= w;
-      store8(dz + col, a.cols - col, g);
+      for (int j = 0; j < kRows; ++j) {
+        const int row = j0 + j < a.choices ? place[j0 + j] : -1;
+        const bool there = (unsigned)row < (unsigned)a.rows;
+        load8((const T*)a.Z + (int64_t)(there ? row : 0) * a.ldz + col, there ? valid : 0, z[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int row = j0 + j < a.choices ? place[j0 + j] : -1;
+        if ((unsigned)row >= (unsigned)a.rows) continue;
+        const float w = weights[j0 + j];
+        float d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(g[i], z[j][i], dot[j]), d[i] = g[i] * w;
+        store8((T*)a.dZ + (int64_t)row * a.lddz + col, valid, d);
+      }
     }
-  }
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d, 64);
-  if (lane == 0) a.dweights[entry] = dot;
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) dot[j] += __shfl_xor(dot[j], d, 64);
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) dots[wave][j] = dot[j];
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j < kRows && j0 + j < a.choices)
+      a.dweights[token * a.choices + j0 + j] = (dots[0][j] + dots[1][j]) + (dots[2][j] + dots[3][j]);
+    __syncthreads();
+  }
 }
 
 // f(V) for the least V of 1, 2, 4, 8, 16 with 64 V >= experts.
@@ -388,29 +497,28 @@ hipError_t launch_route_backward(int type, int score, const RouteArgs& r, hipStr
 hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s) {
   int runs = (p.entries + kPlanRun - 1) / kPlanRun;
   if (runs < 1) runs = 1;  // offsets are written all the same
-  const hipError_t err = launch_with((const void*)&plan_count_kernel, dim3((unsigned)runs), dim3(256), p, s);
-  if (err != hipSuccess) return err;
+  if (runs > 1) {
+    const hipError_t err = launch_with((const void*)&plan_count_kernel, dim3((unsigned)runs), dim3(1024), p, s);
+    if (err != hipSuccess) return err;
+  }
   PlanArgs copy = p;
   void* args[] = {&copy, &runs};
-  return hipLaunchKernel((const void*)&plan_place_kernel, dim3((unsigned)runs), dim3(256), args, 0, s);
+  return hipLaunchKernel((const void*)&plan_place_kernel, dim3((unsigned)runs), dim3(1024), args, 0, s);
 }
 
 hipError_t launch_combine(int type, const CombineArgs& c, hipStream_t s) {
-  int chunks = (c.cols + 7) / 8;
-  const int64_t items = (int64_t)chunks * c.tokens;
+  int slabs = (c.cols + 511) / 512;
+  const int64_t items = (int64_t)slabs * c.tokens;
   return by_type(type, [&](auto t) {
     CombineArgs copy = c;
-    void* args[] = {&copy, &chunks};
-    return hipLaunchKernel((const void*)&combine_kernel<decltype(t)>, dim3((unsigned)((items + 255) / 256)), dim3(256),
-                           args, 0, s);
+    void* args[] = {&copy, &slabs};
+    return hipLaunchKernel((const void*)&combine_kernel<decltype(t)>, dim3((unsigned)((items + 3) / 4)), dim3(256), args, 0, s);
   });
 }
 
 hipError_t launch_combine_backward(int type, const CombineArgs& c, hipStream_t s) {
-  const int64_t entries = (int64_t)c.tokens * c.choices;
   return by_type(type, [&](auto t) {
-    return launch_with((const void*)&combine_backward_kernel<decltype(t)>, dim3((unsigned)((entries + 3) / 4)), dim3(256),
-                       c, s);
+    return launch_with((const void*)&combine_backward_kernel<decltype(t)>, dim3((unsigned)c.tokens), dim3(256), c, s);
   });
 }
 

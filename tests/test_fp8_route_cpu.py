@@ -132,7 +132,7 @@ def test_messages_and_workspace():
     for code in (sg.ERR_TYPE, sg.ERR_ROUTE):
         assert sg.strerror(code) != sg.strerror(12345)
     size = sg.sgemm_mi355_route_plan_workspace_size
-    assert size(10, 8, 64) == 260 and size(1025, 1, 64) == 2 * 260 and size(0, 8, 64) == 260
+    assert size(10, 8, 64) == 260 and size(4096, 1, 64) == 260 and size(4097, 1, 64) == 2 * 260 and size(0, 8, 64) == 260
     assert size(-1, 8, 64) == 0 and size(1, 8, 1025) == 0
 
 
