@@ -39,7 +39,9 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
   if (!find_tile<FORM, BM, BN>(g, t)) return;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int r16 = lane % 16, quad = lane / 16;
-  const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+  // Waves w and w + 4 share a SIMD: their strips of rows lie apart, so that a
+  // tile with half its rows still keeps every SIMD at work.
+  const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
   const int full = t.K / kBlock, tail = t.K % kBlock;  // whole blocks, and what is left
 
   // Direct loads: region q of this wave is rows 8*(q*NW + wave) .. +7; a lane
@@ -86,6 +88,68 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
       if (ROWS % NT == 0 || tid + i * NT < ROWS) scale[tid + i * NT] = s[i];
   };
 
+  // A slab's direct loads are issued over the first half of a block: all at
+  // once they hold up the waves that issue them (8192^3: 466 us, against 440
+  // with two a group and 467 with one, whose last loads land too late).
+  constexpr int PER = (S::REGIONS + NF / 2 - 1) / (NF / 2);
+  float s[NS] = {};
+  if (full > 0) load(0, true, slab0, 0, S::REGIONS);
+  // The partial block goes before the others, in slab 1: once it has landed, a
+  // thread replaces its row's chunks that are not whole.
+  auto stage_tail = [&]() __attribute__((always_inline)) {
+    float part[NS];
+    i32x4 chunks[NS];
+    load(full, true, slab1, 0, S::REGIONS);
+    load_scale(full, part);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int r = tid + i * NT;
+      const bool isa = r < BM;
+      const int row = isa ? min(t.m0 + r, t.rows_a - 1) : min(t.n0 + r - BM, t.rows_b - 1);
+      if (ROWS % NT == 0 || r < ROWS)
+        chunks[i] = load16(isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb, t.K - tail % 16, t.K);
+    }
+    keep_scale(part, scale1);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int r = tid + i * NT;
+      if (ROWS % NT == 0 || r < ROWS) {
+        *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, tail / 16)) = chunks[i];
+        for (int c = tail / 16 + 1; c < 8; ++c) *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, c)) = i32x4{0, 0, 0, 0};
+      }
+    }
+    __syncthreads();
+  };
+  // Block 0 has landed, block 1 is asked for, their scales are in LDS and those of block 2 in registers.
+  auto first_blocks = [&]() __attribute__((always_inline)) {
+    float second[NS];
+    load_scale(0, s);
+    load_scale(min(1, full - 1), second);
+    keep_scale(s, scale0);
+    load_scale(min(2, full - 1), s);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    __syncthreads();
+    load(1, full > 1, slab1, 0, PER);
+    keep_scale(second, scale1);
+  };
+  if (t.m0 + wm >= t.rows_a || t.n0 + wn >= t.rows_b) {
+    // Nothing of C is this wave's: it makes its loads and keeps the barriers.
+    if (tail > 0) stage_tail();
+    if (full > 0) first_blocks();
+    for (int b = 0; b < full; ++b) {
+      load(b + 1, b + 1 < full, b % 2 ? slab0 : slab1, PER, S::REGIONS);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      __syncthreads();
+      load(b + 2, b + 2 < full, b % 2 ? slab1 : slab0, 0, PER);
+      keep_scale(s, b % 2 ? scale1 : scale0);
+      load_scale(min(b + 3, full - 1), s);
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    return;
+  }
+
   // Block b is multiplied in NF groups, one fragment of B with the wave's MF
   // of A. While the matrix unit works on a group, the group before it enters
   // the accumulators and the next fragment is read. Before the last group, all
@@ -99,7 +163,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
   f32x4 acc[NF][MF] = {}, p[MF] = {};
   Frag<WIDE> fa[MF];
   i32x4 raw[2][2];
-  float sa[MF] = {}, sa_before[MF] = {}, s[NS] = {};
+  float sa[MF] = {}, sa_before[MF] = {};
   f32x4 sv_before, sv = {}, sv_next = {};  // without TALL: B's scales of the groups before, at and after this one
   const int at0 = r16 * kBlock + 16 * swz(r16, quad), at1 = at0 ^ 64;
   auto read_a = [&](int i, const uint8_t* slab) __attribute__((always_inline)) {
@@ -124,10 +188,6 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) c[x] = __builtin_fmaf(p[i][x], TALL ? w[i] : w[i] * v[x], c[x]);
   };
-  // A slab's direct loads are issued over the first half of a block: all at
-  // once they hold up the waves that issue them (8192^3: 466 us, against 440
-  // with two a group and 467 with one, whose last loads land too late).
-  constexpr int PER = (S::REGIONS + NF / 2 - 1) / (NF / 2);
   auto step = [&](int b, uint8_t* cur, float* scur, uint8_t* next, float* snext) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
@@ -160,24 +220,8 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
     for (int i = 0; i < MF; ++i) sa_before[i] = sa[i];
     read_scales(snext);
   };
-  if (full > 0) load(0, true, slab0, 0, S::REGIONS);
   if (tail > 0) {
-    // The partial block, before the others: once it has landed, a thread
-    // replaces its row's chunks that are not whole.
-    float part[NS];
-    load(full, true, slab1, 0, S::REGIONS);
-    load_scale(full, part);
-    keep_scale(part, scale1);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();
-    for (int r = tid; r < ROWS; r += NT) {
-      const bool isa = r < BM;
-      const int row = isa ? min(t.m0 + r, t.rows_a - 1) : min(t.n0 + r - BM, t.rows_b - 1);
-      const uint8_t* line = isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb;
-      *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, tail / 16)) = load16(line, full * kBlock + tail / 16 * 16, t.K);
-      for (int c = tail / 16 + 1; c < 8; ++c) *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, c)) = i32x4{0, 0, 0, 0};
-    }
-    __syncthreads();
+    stage_tail();
     read_scales(scale1);
 #pragma unroll
     for (int i = 0; i < MF; ++i) read_a(i, slab1);
@@ -194,15 +238,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
     }
   }
   if (full > 0) {
-    load_scale(0, s);
-    keep_scale(s, scale0);
-    load_scale(min(2, full - 1), s);
-    float second[NS];
-    load_scale(min(1, full - 1), second);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();
-    load(1, full > 1, slab1, 0, PER);
-    keep_scale(second, scale1);
+    first_blocks();
 #pragma unroll
     for (int i = 0; i < MF; ++i) read_a(i, slab0);
     read_b(0, slab0, scale0);
