@@ -82,29 +82,25 @@ __device__ __forceinline__ f32x4 block_product(const Frag<true>& b, const Frag<t
   return p;
 }
 
-template <class T>
-__device__ __forceinline__ void store4(T* c, int valid, f32x4 v, float beta) {
-  if (valid >= 4) {
-    T e[4];
-    if (beta != 0.0f) {
-      __builtin_memcpy(e, c, sizeof(e));
+// `valid` of W neighbours of C at element `at`.
+template <class T, int W>
+__device__ __forceinline__ void store_as(T* c, int valid, const float (&v)[W], float beta) {
+  if (valid >= W && beta == 0.0f) {
+    T e[W];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(beta, to_f32(e[i]), v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = from_f32<T>(v[i]);
+    for (int i = 0; i < W; ++i) e[i] = from_f32<T>(v[i]);
     __builtin_memcpy(c, e, sizeof(e));
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < W; ++i)
     if (i < valid) c[i] = from_f32<T>(beta != 0.0f ? __builtin_fmaf(beta, to_f32(c[i]), v[i]) : v[i]);
 }
-// `valid` of four neighbours of C at element `at`.
-__device__ __forceinline__ void store_c(const Fp8Args& g, void* C, int64_t at, int valid, f32x4 v) {
-  if (g.type == SGEMM_MI355_F32) store4((float*)C + at, valid, v, g.beta);
-  else if (g.type == SGEMM_MI355_BF16) store4((__hip_bfloat16*)C + at, valid, v, g.beta);
-  else store4((__half*)C + at, valid, v, g.beta);
+template <int W>
+__device__ __forceinline__ void store_c(const Fp8Args& g, void* C, int64_t at, int valid, const float (&v)[W]) {
+  if (g.type == SGEMM_MI355_F32) store_as((float*)C + at, valid, v, g.beta);
+  else if (g.type == SGEMM_MI355_BF16) store_as((__hip_bfloat16*)C + at, valid, v, g.beta);
+  else store_as((__half*)C + at, valid, v, g.beta);
 }
 
 // The experts' tiles of BM rows, numbered expert by expert and then those of

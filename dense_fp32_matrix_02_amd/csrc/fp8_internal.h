@@ -150,9 +150,7 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __hip_bfloat16 from_f32<__hip_bfloat16>(float x) {
-  const uint32_t u = __float_as_uint(x);
-  uint16_t r = (uint16_t)((u + 0x7FFF + ((u >> 16) & 1)) >> 16);
-  if ((u & 0x7FFFFFFF) > 0x7F800000) r = (uint16_t)((u >> 16) | 0x40);
+  const __bf16 r = (__bf16)x;
   __hip_bfloat16 y;
   __builtin_memcpy(&y, &r, 2);
   return y;

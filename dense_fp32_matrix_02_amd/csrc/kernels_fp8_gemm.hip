@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256) fp8_gemm_kernel(Fp8Args g) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int n = t.n0 + wn + 32 * j + 8 * q + 4 * h;
-        const f32x4 v = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+        const float v[4] = {acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
         store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
       }
   }

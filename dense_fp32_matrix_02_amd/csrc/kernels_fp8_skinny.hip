@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) fp8_skinny_kernel(Fp8Args g
 #pragma unroll
     for (int w = 1; w < NW; ++w) sum += part[w][wave][lane];
     const int m = t.m0 + 16 * wave + r16, n = t.n0 + 4 * quad;
-    if (m < t.rows_a) store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, sum);
+    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if (m < t.rows_a) store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
   }
 }
 

@@ -1,6 +1,8 @@
 // FP8 products of operands that load directly to LDS (16-byte aligned, row
 // strides multiples of 16): tiles of C from whole slabs of one block of 128.
 
+#include <type_traits>
+
 #include "sgemm_internal.h"
 #include "fp8_device.h"
 
@@ -24,7 +26,6 @@ struct TileShape {
   static constexpr int REGIONS = ROWS / 8 / NW;  // 1 KiB direct loads per wave and slab
   static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
   static_assert(NW % 2 == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole regions of either operand per wave");
-  static_assert(ROWS % NT == 0 || NT % ROWS == 0, "scales per thread");
 };
 
 template <int FORM, bool WIDE, bool TALL, int BM, int BN, int WM, int WN>
@@ -47,45 +48,45 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
   // Direct loads: region q of this wave is rows 8*(q*NW + wave) .. +7; a lane
   // brings one chunk, the same for all its regions. Rows that do not exist lie
   // past the buffers' ends and load as zeros.
-  const int chunk = swz(8 * wave + lane / 8, lane % 8);
-  uint32_t src[S::REGIONS];
-#pragma unroll
-  for (int q = 0; q < S::REGIONS; ++q) {
-    const int r = 8 * (q * S::NW + wave) + lane / 8;
-    src[q] = (q * S::NW * 8 < BM ? (uint32_t)r * (uint32_t)g.lda : (uint32_t)(r - BM) * (uint32_t)g.ldb) + 16 * chunk;
-  }
+  const uint32_t chunk = 16 * swz(8 * wave + lane / 8, lane % 8), row = 8 * wave + lane / 8;
+  const uint32_t a_src = row * (uint32_t)g.lda + chunk, b_src = row * (uint32_t)g.ldb + chunk;
+  const uint32_t a_region = 8 * S::NW * (uint32_t)g.lda, b_region = 8 * S::NW * (uint32_t)g.ldb;
   const uint8_t* a0 = t.A + (int64_t)t.m0 * g.lda;
   const uint8_t* b0 = t.B + (int64_t)t.n0 * g.ldb;
   const int a_bytes = (min(t.rows_a - t.m0, BM) - 1) * (int)g.lda + t.K;
   const int b_bytes = (min(t.rows_b - t.n0, BN) - 1) * (int)g.ldb + t.K;
   // Regions [from, to) of slab b, or nothing (and no memory traffic) when there is none.
   auto load = [&](int b, bool there, uint8_t* slab, int from, int to) __attribute__((always_inline)) {
-    const int64_t k = (int64_t)b * kBlock;
-    const int a_left = there ? a_bytes - (int)k : 0, b_left = there ? b_bytes - (int)k : 0;
 #pragma unroll
     for (int q = from; q < to; ++q) {
       const bool a = q * S::NW * 8 < BM;
-      copy16_to_lds((a ? a0 : b0) + k, a ? a_left : b_left, src[q], slab + (q * S::NW + wave) * 1024);
+      const int left = there ? (a ? a_bytes : b_bytes) - b * kBlock : 0;
+      // An addition here costs less than the registers of an offset for each region.
+      const uint32_t at = a ? a_src + q * a_region : b_src + (q - BM / (8 * S::NW)) * b_region;
+      copy16_to_lds((a ? a0 : b0) + b * kBlock, left, at, slab + (q * S::NW + wave) * 1024);
     }
   };
-  // This thread's scales of block b: row tid (+ NT ...) of the slab.
+  // This thread's scales: rows tid (+ NT ..) of the slab, of the same operand for the whole wave.
   constexpr int NS = (ROWS + NT - 1) / NT;
+  static_assert(ROWS % NT == 0 && BM % 64 == 0, "every thread has scales, a wave's are of one operand");
+  const float* scales[NS];
+  int64_t scale_step[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int r = tid + i * NT;
+    const bool a = 64 * wave + i * NT < BM;
+    const int n = min(t.n0 + r - BM, t.rows_b - 1);
+    scales[i] = a ? t.SA + (int64_t)min(t.m0 + r, t.rows_a - 1) * g.sa_row : t.SB + (int64_t)(TALL ? n / kBlock : n) * g.sb_row;
+    scale_step[i] = a ? g.sa_block : g.sb_block;
+  }
   auto load_scale = [&](int b, float (&s)[NS]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int r = tid + i * NT;
-      if (r < BM) {
-        s[i] = t.SA[(int64_t)min(t.m0 + r, t.rows_a - 1) * g.sa_row + (int64_t)b * g.sa_block];
-      } else if (r < ROWS) {
-        const int n = min(t.n0 + r - BM, t.rows_b - 1);
-        s[i] = t.SB[(int64_t)(TALL ? n / kBlock : n) * g.sb_row + (int64_t)b * g.sb_block];
-      }
-    }
+    for (int i = 0; i < NS; ++i) s[i] = scales[i][b * scale_step[i]];
   };
   auto keep_scale = [&](const float (&s)[NS], float* scale) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-      if (ROWS % NT == 0 || tid + i * NT < ROWS) scale[tid + i * NT] = s[i];
+      scale[tid + i * NT] = s[i];
   };
 
   // A slab's direct loads are issued over the first half of a block: all at
@@ -106,8 +107,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
       const int r = tid + i * NT;
       const bool isa = r < BM;
       const int row = isa ? min(t.m0 + r, t.rows_a - 1) : min(t.n0 + r - BM, t.rows_b - 1);
-      if (ROWS % NT == 0 || r < ROWS)
-        chunks[i] = load16(isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb, t.K - tail % 16, t.K);
+      chunks[i] = load16(isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb, t.K - tail % 16, t.K);
     }
     keep_scale(part, scale1);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
@@ -115,10 +115,8 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int r = tid + i * NT;
-      if (ROWS % NT == 0 || r < ROWS) {
-        *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, tail / 16)) = chunks[i];
-        for (int c = tail / 16 + 1; c < 8; ++c) *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, c)) = i32x4{0, 0, 0, 0};
-      }
+      *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, tail / 16)) = chunks[i];
+      for (int c = tail / 16 + 1; c < 8; ++c) *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, c)) = i32x4{0, 0, 0, 0};
     }
     __syncthreads();
   };
@@ -253,15 +251,54 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
     for (int i = 0; i < MF; ++i) add(acc[NF - 1][i], i, sa_before, sv);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the workgroup
   }
+  // To C by way of LDS, ROUND fragments of A's rows at a time, so that a lane
+  // stores eight neighbours and a row's strip is stored at a stretch. The rows
+  // go round a loop that is not unrolled: this code runs once per tile, and
+  // fetching it costs more than running it (with a copy of the stores for each
+  // fragment this took 3.5 us of a tile, unrolled wholly 8 us of a 256 x 256 one).
+  constexpr int WIDTH = 16 * NF, LANES = WIDTH / 8;  // floats of a row of the strip, and lanes that store one
+  constexpr int ROUND = kBlock * ROWS * 2 / S::NW / (16 * WIDTH * 4) < MF ? kBlock * ROWS * 2 / S::NW / (16 * WIDTH * 4) : MF;
+  static_assert(ROUND >= 1 && MF % ROUND == 0, "whole rounds");
+  float* out = (float*)(wave < S::NW / 2 ? slab0 : slab1) + wave % (S::NW / 2) * (ROUND * 16 * WIDTH);
+  __syncthreads();  // all reads of the slabs have been made
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int m = t.m0 + wm + 16 * i + r16;
-    if (m >= t.rows_a) continue;
+  for (int i0 = 0; i0 < MF; i0 += ROUND) {
+    // Chunk c of four floats of row r lies at place c ^ (r % 16): 16 rows' writes of one chunk meet all banks.
 #pragma unroll
-    for (int j = 0; j < NF; ++j) {
-      const int n = t.n0 + wn + 16 * j + 4 * quad;
-      store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, acc[j][i]);
-    }
+    for (int i = 0; i < ROUND; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        *(f32x4*)(out + (16 * i + r16) * WIDTH + 4 * ((4 * j + quad) ^ r16)) = acc[j][i0 + i];
+    __builtin_amdgcn_wave_barrier();  // LDS serves a wave in order
+    const int c = 2 * (lane % LANES), n = t.n0 + wn + 4 * c;
+    const int rows = min(16 * ROUND, t.rows_a - t.m0 - wm - 16 * i0);
+    auto strip = [&](int r, float (&v)[8]) __attribute__((always_inline)) {
+      *(f32x4*)v = *(const f32x4*)(out + r * WIDTH + 4 * (c ^ (r % 16)));
+      *(f32x4*)(v + 4) = *(const f32x4*)(out + r * WIDTH + 4 * ((c + 1) ^ (r % 16)));
+    };
+    const int64_t at = (int64_t)(t.m0 + wm + 16 * i0) * g.ldc + n;
+    auto rows_to_c = [&](auto* C) __attribute__((always_inline)) {
+      using T = std::remove_pointer_t<decltype(C)>;
+      if (g.beta == 0.0f && n + 8 <= g.N) {
+#pragma unroll 4
+        for (int r = lane / LANES; r < rows; r += 64 / LANES) {
+          float v[8];
+          strip(r, v);
+          store8(C + at + r * g.ldc, 8, v);
+        }
+      } else {
+#pragma unroll 1
+        for (int r = lane / LANES; r < rows; r += 64 / LANES) {
+          float v[8];
+          strip(r, v);
+          store_as<T, 8>(C + at + r * g.ldc, g.N - n, v, g.beta);
+        }
+      }
+    };
+    if (g.type == SGEMM_MI355_F32) rows_to_c((float*)t.C);
+    else if (g.type == SGEMM_MI355_BF16) rows_to_c((__hip_bfloat16*)t.C);
+    else rows_to_c((__half*)t.C);
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
