@@ -18,6 +18,8 @@
 // lane's 16 results are one row of C (one m): sA is then one value per lane,
 // and a lane's results are four runs of four neighbours in C.
 
+#include <cmath>
+
 #include "sgemm_internal.h"
 #include "fp8_device.h"
 
@@ -131,18 +133,39 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
                       g.lda < 1 << 23 && g.ldb < 1 << 23;  // offsets within a tile fit 31 bits
   if (!direct) return {Choice::STAGED, true, 128, 128, 256};
   const bool wide = g.type == SGEMM_MI355_F32;
-  const int64_t rows = form == FP8_EXPERTS ? (2 * (int64_t)g.M + g.experts - 1) / g.experts : g.M;
-  if (form != FP8_WGRAD && rows <= 64) return {Choice::SKINNY, wide, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, 16, 512};
-  // Widened values need more registers than a 64 x 128 wave tile leaves. FP8:
-  // a round of the chip is 256 tiles of 256 x 256 or 512 of 128 x 128, which
-  // takes 0.65 of the time (8192^3 with bf16 C: 496 us in 4 rounds, 641 in 8).
-  const int64_t batch = form == FP8_WGRAD ? g.experts : 1;
-  auto rounds = [&](int b, int64_t per_round) {
-    const int64_t tiles_m = form == FP8_EXPERTS ? g.M / b + (g.experts + 1) / 2 : (g.M + b - 1) / b;
-    return (double)((batch * tiles_m * ((g.N + b - 1) / b) + per_round - 1) / per_round);
+  // The least of the estimated times (us; r: rounds of 256 workgroups, one for
+  // each CU; k: K/1024), fitted to times of M 8 .. 2048, N 256 .. 4096, K 256 ..
+  // 8192 and 8192^3, as K 2048, N 4096, bf16, M 128 / 512 / 2048:
+  //   few-rows kernel, 16, 32, 64 rows   27.2, 18.8, 15.0 / 97, 65, 55 / -, -, 210
+  //   128 x 128 tiles, 256 x 256 tiles   13.0, 17.1 / 14.2, 24.3 / 24.5, 28.3
+  // Widened values need more registers than the strip of a wave of a 256 x 256
+  // tile leaves, so that form has 128 x 128 tiles only (24.4 us at M 512, fp32).
+  const double k = g.K / 1024.0 / (form == FP8_WGRAD ? g.experts : 1);
+  auto groups = [&](int bm, int bn) {
+    // An expert with rows has one tile of rows, and half a tile more on average
+    // where it has many.
+    const int64_t used = g.experts < g.M ? g.experts : g.M, whole = (g.M + bm - 1) / bm;
+    const int64_t tiles_m = form == FP8_EXPERTS ? (whole + used / 2 > used ? whole + used / 2 : used) : whole;
+    return (double)((form == FP8_WGRAD ? g.experts : 1) * tiles_m * ((g.N + bn - 1) / bn)) / 256.0;
   };
-  const bool small = wide || 0.65 * rounds(128, 512) < rounds(256, 256);
-  return {Choice::TILE, wide, small ? 128 : 256, small ? 128 : 256, small ? 256 : 512};
+  Choice best{};
+  double least = 0.0;
+  auto offer = [&](Choice c, double time) {
+    if (best.threads == 0 || time < least) best = c, least = time;
+  };
+  const double r = std::ceil(groups(128, 128));
+  offer({Choice::TILE, wide, 128, 128, 256}, wide ? 2.5 + r * (4.0 + 8.4 * k) : 1.0 + r * (3.3 + 4.2 * k));
+  if (!wide) {
+    const double r = groups(256, 256);
+    offer({Choice::TILE, wide, 256, 256, 512}, 2.5 + std::ceil(r) * (4.0 + (8.75 + 4.5 * (r < 1.0 ? r : 1.0)) * k));
+  }
+  if (form != FP8_WGRAD) {
+    auto rounds = [&](int bm) { return groups(bm, 16) > 1.0 ? groups(bm, 16) : 1.0; };
+    offer({Choice::SKINNY, wide, 64, 16, 512}, 2.4 + rounds(64) * (1.3 + 2.4 * k));
+    offer({Choice::SKINNY, wide, 32, 16, 512}, 2.6 + rounds(32) * (0.8 + 1.41 * k));
+    offer({Choice::SKINNY, wide, 16, 16, 512}, 2.6 + rounds(16) * (0.8 + 0.98 * k));
+  }
+  return best;
 }
 
 }  // namespace
@@ -156,7 +179,7 @@ hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s) {
   const Choice c = choose(form, g);
   const dim3 grid((unsigned)grid_tiles(form, g, c.bm, c.bn), form == FP8_WGRAD ? (unsigned)g.experts : 1u);
   const void* kernel = c.kernel == Choice::TILE     ? fp8_tile_kernel_for(form, c.wide, g.sb_rows == kBlock, c.bm)
-                       : c.kernel == Choice::SKINNY ? fp8_skinny_kernel_for(form, c.wide, c.bm)
+                       : c.kernel == Choice::SKINNY ? fp8_skinny_kernel_for(form, c.wide, g.sb_rows == kBlock, c.bm)
                        : form == FP8_EXPERTS        ? (const void*)&fp8_gemm_kernel<FP8_EXPERTS>
                        : form == FP8_WGRAD          ? (const void*)&fp8_gemm_kernel<FP8_WGRAD>
                                                     : (const void*)&fp8_gemm_kernel<FP8_DENSE>;
