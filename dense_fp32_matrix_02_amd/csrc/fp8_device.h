@@ -38,6 +38,21 @@ __device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
   return v;
 }
 
+// The same for K >= 16, in one load: of the 16 bytes at k or, where they would
+// pass K, of the row's last 16, shifted to their places.
+__device__ __forceinline__ i32x4 load16_end(const uint8_t* row, int k, int K) {
+  const int at = min(k, K - 16), skip = k - at;
+  uint64_t v[2];
+  __builtin_memcpy(v, row + at, 16);
+  if (skip >= 8) v[0] = v[1], v[1] = 0;
+  const int bits = 8 * (skip % 8);
+  if (bits > 0) v[0] = v[0] >> bits | v[1] << (64 - bits), v[1] >>= bits;
+  if (skip >= 16) v[0] = 0;
+  i32x4 r;
+  __builtin_memcpy(&r, v, 16);
+  return r;
+}
+
 // Position of 16-byte chunk c of row r of a 128-byte-row slab: gfx950 serves
 // a 128-bit LDS read 16 lanes at a time from 64 banks, so 16 consecutive rows
 // (each starting at bank 0 or 32) have to hold one chunk in different places.

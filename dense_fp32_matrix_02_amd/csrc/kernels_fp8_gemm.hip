@@ -130,7 +130,8 @@ struct Choice {
 
 Choice choose(Fp8Form form, const Fp8Args& g) {
   const bool direct = (((uintptr_t)g.A | (uintptr_t)g.B | (uint64_t)g.lda | (uint64_t)g.ldb | (uint64_t)g.strideB) & 15) == 0 &&
-                      g.lda < 1 << 23 && g.ldb < 1 << 23;  // offsets within a tile fit 31 bits
+                      g.lda < 1 << 23 && g.ldb < 1 << 23 &&  // offsets within a tile fit 31 bits
+                      (form == FP8_WGRAD || g.K >= 16);
   if (!direct) return {Choice::STAGED, true, 128, 128, 256};
   const bool wide = g.type == SGEMM_MI355_F32;
   // The least of the estimated times (us; r: rounds of 256 workgroups, one for
@@ -148,16 +149,17 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
     const int64_t tiles_m = form == FP8_EXPERTS ? (whole + used / 2 > used ? whole + used / 2 : used) : whole;
     return (double)((form == FP8_WGRAD ? g.experts : 1) * tiles_m * ((g.N + bn - 1) / bn)) / 256.0;
   };
+  const double tail = g.K % kBlock != 0 ? 2.0 : 0.0;  // of the tiles: the partial block is not overlapped
   Choice best{};
   double least = 0.0;
   auto offer = [&](Choice c, double time) {
     if (best.threads == 0 || time < least) best = c, least = time;
   };
   const double r = std::ceil(groups(128, 128));
-  offer({Choice::TILE, wide, 128, 128, 256}, wide ? 2.5 + r * (4.0 + 8.4 * k) : 1.0 + r * (3.3 + 4.2 * k));
+  offer({Choice::TILE, wide, 128, 128, 256}, (wide ? 2.5 + r * (4.0 + 8.4 * k) : 1.0 + r * (3.3 + 4.2 * k)) + tail);
   if (!wide) {
     const double r = groups(256, 256);
-    offer({Choice::TILE, wide, 256, 256, 512}, 2.5 + std::ceil(r) * (4.0 + (8.75 + 4.5 * (r < 1.0 ? r : 1.0)) * k));
+    offer({Choice::TILE, wide, 256, 256, 512}, 2.5 + std::ceil(r) * (4.0 + (8.75 + 4.5 * (r < 1.0 ? r : 1.0)) * k) + tail);
   }
   if (form != FP8_WGRAD) {
     auto rounds = [&](int bm) { return groups(bm, 16) > 1.0 ? groups(bm, 16) : 1.0; };

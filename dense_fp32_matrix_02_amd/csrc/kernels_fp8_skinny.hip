@@ -1,5 +1,5 @@
 // FP8 products of few rows of A (a decoding step), of operands that are
-// 16-byte aligned in rows of a multiple of 16 bytes.
+// 16-byte aligned in rows of a multiple of 16 bytes; K is 16 or more.
 
 #include <type_traits>
 
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves, MF == 4 ? 2 : MF == 1 ? 6 :
     const int k = blk * kBlock + 16 * quad;
     auto chunk = [&](const uint8_t* row, int at) __attribute__((always_inline)) {
       if constexpr (decltype(whole)::value) return *(const i32x4*)(row + at);
-      else return load16(row, at, t.K);
+      else return load16_end(row, at, t.K);
     };
     h.b[0] = chunk(b, k), h.b[1] = chunk(b, k + 64);
     h.sb = sb[(int64_t)blk * g.sb_block];

@@ -1,5 +1,6 @@
 // FP8 products of operands that load directly to LDS (16-byte aligned, row
-// strides multiples of 16): tiles of C from whole slabs of one block of 128.
+// strides multiples of 16, K 16 or more): tiles of C from whole slabs of one
+// block of 128.
 
 #include <type_traits>
 
@@ -107,7 +108,10 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
       const int r = tid + i * NT;
       const bool isa = r < BM;
       const int row = isa ? min(t.m0 + r, t.rows_a - 1) : min(t.n0 + r - BM, t.rows_b - 1);
-      chunks[i] = load16(isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb, t.K - tail % 16, t.K);
+      const uint8_t* line = isa ? t.A + (int64_t)row * g.lda : t.B + (int64_t)row * g.ldb;
+      const int k = t.K - tail % 16;
+      if (FORM != FP8_WGRAD || t.K >= 16) chunks[i] = load16_end(line, k, t.K);
+      else chunks[i] = load16(line, k, t.K);
     }
     keep_scale(part, scale1);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
