@@ -90,16 +90,18 @@ def _stream_of(x, stream):
     return torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, strides=None):
     """A tensor from torch's caching allocator, allocated on the stream the
     call runs on, so that the allocator hands its memory out again only after
     that stream's work."""
     import torch
 
+    if strides is None:
+        strides = (max(shape[-1], 1), 1)[-len(shape):] if len(shape) < 3 else (shape[1] * shape[2], shape[2], 1)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)  # cheaper than torch.empty here
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _gpu(x, name, dtype=None):
@@ -131,9 +133,8 @@ def _bytes_out(rows, cols, device, stream):
     """An uninitialised e4m3 matrix whose row stride is a multiple of 16 bytes, and that stride."""
     import torch
 
-    pad = -cols % 16
-    q = _empty((rows, cols + pad), torch.float8_e4m3fn, device, stream)
-    return (q[:, :cols] if pad else q), max(cols + pad, 1)
+    ld = max(cols + -cols % 16, 1)
+    return _empty((rows, cols), torch.float8_e4m3fn, device, stream, (ld, 1)), ld
 
 
 def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
@@ -162,12 +163,12 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
     n = rows if index is None else index.numel()
     at = None if index is None else _ints(index, "index")
     Q, ldq = _bytes_out(n, cols, X.device, stream)
-    S = _empty((_blocks(cols), n), torch.float32, X.device, stream)
+    S = _empty((n, _blocks(cols)), torch.float32, X.device, stream, (1, max(n, 1)))  # block by block
     if at is not None and n == 0:
-        return Q, S.t()
+        return Q, S
     _check(_c.fp8_quantize_rows(kind, rows, cols, X.data_ptr(), ldx, at, n, Q.data_ptr(), ldq, S.data_ptr(), 1, max(n, 1), s),
            "fp8_quantize_rows")
-    return Q, S.t()
+    return Q, S
 
 
 def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
@@ -193,12 +194,12 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
     off = None if offsets is None else _ints(offsets, "offsets")
     width = n if offsets is None else 128 * (n // 128 + experts)
     Q, ldq = _bytes_out(cols, width, X.device, stream)
-    S = _empty((_blocks(width), cols), torch.float32, X.device, stream)
+    S = _empty((cols, _blocks(width)), torch.float32, X.device, stream, (1, max(cols, 1)))
     if at is not None and n == 0:
         at, rows = None, 0
     _check(_c.fp8_quantize_cols(kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts, Q.data_ptr(), ldq, S.data_ptr(), 1,
                                 max(cols, 1), _stream_of(X, stream)), "fp8_quantize_cols")
-    return Q, S.t()
+    return Q, S
 
 
 def _operand(Q, S, name, rows, cols, either=False):

@@ -104,13 +104,12 @@ def route_plan(experts, num_experts: int, *, stream=None):
     tokens, k = experts.shape
     ids = _dense(experts, "experts", torch.int32, (tokens, k))
     need = _c.route_plan_workspace_size(tokens, k, num_experts)
-    # one allocation for the three results and one for the workspace
     offsets = _empty((max(num_experts, 0) + 1,), torch.int32, experts.device, stream)
     rows = _empty((tokens * k,), torch.int32, experts.device, stream)
     place = _empty((tokens, k), torch.int32, experts.device, stream)
-    room = _empty((need // 4,), torch.int32, experts.device, stream)
+    room = _empty((need // 4,), torch.int32, experts.device, stream) if need else None
     _check(_c.route_plan(tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),
-                                  place.data_ptr(), room.data_ptr(), need, _stream_of(experts, stream)),
+                                  place.data_ptr(), None if room is None else room.data_ptr(), need, _stream_of(experts, stream)),
            "route_plan")
     return offsets, rows, place
 

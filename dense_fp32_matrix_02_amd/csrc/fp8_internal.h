@@ -94,7 +94,7 @@ struct PlanArgs {
   int *offsets, *row_token, *place;
   int* counts;  // workspace: entries of each expert in each run of kPlanRun entries
 };
-constexpr int kPlanRun = 4096;
+constexpr int kPlanRun = 2048;
 hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s);
 
 struct CombineArgs {

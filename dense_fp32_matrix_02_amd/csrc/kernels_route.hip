@@ -18,8 +18,8 @@ constexpr int kNone = 0x7FFFFFFF;
 // Reductions over the wave run in the vector unit (DPP), not as shuffles
 // through LDS: 8192 tokens of 256 experts, 8 of 4 of 8 groups, took 52 us with
 // shuffles. A choice value is compared as a 64-bit key whose halves are
-// reduced one after the other: the largest first half, then the largest second
-// half among the lanes that have it, then the first lane that has both.
+// reduced one after the other: the largest first half, then, if several lanes
+// have it, the largest second half among them, then the first lane that has both.
 
 template <class T>
 __device__ __forceinline__ double to_f64(T x) { return (double)to_f32(x); }
@@ -72,6 +72,8 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 __device__ __forceinline__ uint64_t lanes_of_most(uint64_t key) {
   const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
   const uint32_t most_hi = wave_most(hi);
+  const uint64_t lanes = __ballot(hi == most_hi);
+  if ((lanes & (lanes - 1)) == 0) return lanes;
   const uint32_t most_lo = wave_most(hi == most_hi ? lo : 0);
   return __ballot(hi == most_hi && lo == most_lo);
 }
@@ -114,23 +116,35 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs& a, const doubl
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  // Lane l finds the strengths of groups l, l + 64, ..: each lane begins at a
-  // place of its own in its group, so that the lanes read different banks.
+  // L neighbouring lanes find a group's strength, each from every L-th of its
+  // experts, beginning at places of their own, so that lanes of different
+  // groups read different banks. More than 64 groups take several turns.
+  int L = 1;
+  while (2 * L * a.groups <= 64) L *= 2;
+  const int turn = 64 / L;
   uint64_t strength[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int g = lane + 64 * v;
+    const int g = lane / L + v * turn;
     strength[v] = 0;
-    if (g < a.groups) {
+    if (v == 0 || v * turn < a.groups) {
       double one = -INFINITY, two = -INFINITY;
-      int at = g % size;
-      for (int i = 0; i < size; ++i) {
-        const double x = row[g * size + at];
+      const int n = g < a.groups ? (size - lane % L + L - 1) / L : 0;  // this lane's experts of the group
+      int at = n > 0 ? g % n : 0;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const double x = row[g * size + lane % L + at * L];
         two = fmax(two, fmin(one, x));
         one = fmax(one, x);
-        at = at + 1 == size ? 0 : at + 1;
+        at = at + 1 == n ? 0 : at + 1;
       }
-      strength[v] = key_of(size > 1 ? one + two : one);
+#pragma unroll 1
+      for (int d = 1; d < L; d *= 2) {
+        const double x = __shfl_xor(one, d, 64), y = __shfl_xor(two, d, 64);
+        two = fmax(fmin(one, x), fmax(two, y));
+        one = fmax(one, x);
+      }
+      if (g < a.groups) strength[v] = key_of(size > 1 ? one + two : one);
     }
   }
   int group[V];
@@ -142,14 +156,14 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs& a, const doubl
     int mine = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (strength[v] > best) best = strength[v], mine = lane + 64 * v;
+      if (strength[v] > best) best = strength[v], mine = lane / L + v * turn;
     const uint64_t lanes = lanes_of_most(best);
     int g = (int)lane_value((uint32_t)mine, __builtin_ctzll(lanes));
     // More than 64 groups: of equal ones the lowest need not be the first lane's.
     if (a.groups > 64) g = kNone - (int)wave_most(lanes >> lane & 1 ? (uint32_t)(kNone - mine) : 0u);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (lane + 64 * v == g) strength[v] = 0;
+      if (lane / L + v * turn == g) strength[v] = 0;
       if (group[v] == g) kept |= 1u << v;
     }
   }

@@ -82,7 +82,8 @@ int sgemm_mi355_route_backward(int type, int tokens, int experts, const void* lo
 
 size_t sgemm_mi355_route_plan_workspace_size(int tokens, int choices, int experts) {
   if (tokens < 0 || choices < 0 || experts < 1 || experts > SGEMM_MI355_MAX_EXPERTS) return 0;
-  return (size_t)plan_runs((int64_t)tokens * choices) * ((size_t)experts + 1) * 4;
+  const int runs = plan_runs((int64_t)tokens * choices);
+  return runs == 1 ? 0 : (size_t)runs * ((size_t)experts + 1) * 4;
 }
 
 int sgemm_mi355_route_plan(int tokens, int choices, int experts, const int* ids, int* offsets, int* row_token,
@@ -97,7 +98,7 @@ int sgemm_mi355_route_plan(int tokens, int choices, int experts, const int* ids,
   m.dense(offsets, 1, experts + 1, experts + 1, 4, true);
   m.dense(row_token, 1, entries, entries, 4, true);
   m.dense(place, tokens, choices, choices, 4, true);
-  if (workspace_bytes >= need) m.dense(workspace, 1, (int64_t)(need / 4), (int64_t)(need / 4), 4, true);
+  if (need > 0 && workspace_bytes >= need) m.dense(workspace, 1, (int64_t)(need / 4), (int64_t)(need / 4), 4, true);
   const int c = m.check();
   if (c != SGEMM_MI355_OK) return c;
   if (workspace_bytes < need) return SGEMM_MI355_ERR_WORKSPACE;

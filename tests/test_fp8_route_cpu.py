@@ -89,7 +89,7 @@ ROUTE = dict(type=0, tokens=10, experts=64, logits=X, ld=64, bias=None, score=0,
              scale=1.0, weights=S, ids=I, stream=0)
 BACK = dict(type=0, tokens=10, experts=64, logits=X, ld=64, ids=I, dweights=S, score=1, choices=8, renorm=1, scale=1.0,
             dlogits=C, ldd=64, stream=0)
-PLAN = dict(tokens=10, choices=8, experts=64, ids=I, offsets=O, row_token=X, place=S, workspace=T, bytes=260, stream=0)
+PLAN = dict(tokens=300, choices=8, experts=64, ids=I, offsets=O, row_token=X, place=S, workspace=T, bytes=520, stream=0)
 COMBINE = dict(type=1, tokens=10, choices=8, rows=80, cols=100, Z=X, ldz=100, place=I, weights=S, Y=C, ldy=100, stream=0)
 COMBACK = dict(type=1, tokens=10, choices=8, rows=80, cols=100, dY=X, lddy=100, Z=Q, ldz=100, place=I, weights=S, dZ=C, lddz=100,
                dweights=T, stream=0)
@@ -109,7 +109,7 @@ BAD_ROUTE = [
     (sg.sgemm_mi355_route_plan, PLAN, [
         (dict(tokens=-1), E.ERR_DIM), (dict(experts=0), E.ERR_DIM), (dict(experts=1025), E.ERR_ROUTE), (dict(ids=None), E.ERR_NULL),
         (dict(offsets=None), E.ERR_NULL), (dict(place=None), E.ERR_NULL), (dict(workspace=None), E.ERR_NULL),
-        (dict(bytes=259), E.ERR_WORKSPACE), (dict(workspace=None, bytes=0), E.ERR_WORKSPACE), (dict(workspace=O), E.ERR_ALIAS),
+        (dict(bytes=519), E.ERR_WORKSPACE), (dict(workspace=None, bytes=0), E.ERR_WORKSPACE), (dict(workspace=O), E.ERR_ALIAS),
         (dict(place=I), E.ERR_ALIAS), (dict(offsets=O + 2), E.ERR_ALIGN), (dict(tokens=BIG // 8), E.ERR_EXTENT)]),
     (sg.sgemm_mi355_route_combine, COMBINE, [
         (dict(type=3), E.ERR_TYPE), (dict(choices=-1), E.ERR_DIM), (dict(rows=-1), E.ERR_DIM), (dict(ldz=99), E.ERR_LD),
@@ -132,7 +132,7 @@ def test_messages_and_workspace():
     for code in (sg.ERR_TYPE, sg.ERR_ROUTE):
         assert sg.strerror(code) != sg.strerror(12345)
     size = sg.sgemm_mi355_route_plan_workspace_size
-    assert size(10, 8, 64) == 260 and size(4096, 1, 64) == 260 and size(4097, 1, 64) == 2 * 260 and size(0, 8, 64) == 260
+    assert size(10, 8, 64) == 0 and size(2048, 1, 64) == 0 and size(2049, 1, 64) == 2 * 260 and size(0, 8, 64) == 0
     assert size(-1, 8, 64) == 0 and size(1, 8, 1025) == 0
 
 
