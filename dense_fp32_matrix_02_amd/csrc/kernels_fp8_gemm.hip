@@ -155,17 +155,26 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
   auto offer = [&](Choice c, double time) {
     if (best.threads == 0 || time < least) best = c, least = time;
   };
+  // Experts' tiles with few rows wait for the weights: at 5 TB/s, and the tiled
+  // kernels 1.25 times that. The few-rows kernel loads no rows that do not
+  // exist (16 tokens of 4 of 32 experts, N 2048, K 4096, weights not in a
+  // cache: 43.5 us in 16-row tiles, 54 in 128 x 128, 57 in 256 x 256; 128
+  // tokens 89, 68, 69).
+  const bool experts = form == FP8_EXPERTS;
+  const double weights = experts ? 1.25 * (g.experts < g.M ? g.experts : g.M) * g.N * (double)g.K / 5.0e6 : 0.0;
   const double r = std::ceil(groups(128, 128));
-  offer({Choice::TILE, wide, 128, 128, 256}, (wide ? 2.5 + r * (4.0 + 8.4 * k) : 1.0 + r * (3.3 + 4.2 * k)) + tail);
+  offer({Choice::TILE, wide, 128, 128, 256},
+        std::fmax(weights, (wide ? 2.5 + r * (4.0 + 8.4 * k) : 1.0 + r * (3.3 + 4.2 * k)) + tail));
   if (!wide) {
     const double r = groups(256, 256);
-    offer({Choice::TILE, wide, 256, 256, 512}, 2.5 + std::ceil(r) * (4.0 + (8.75 + 4.5 * (r < 1.0 ? r : 1.0)) * k) + tail);
+    offer({Choice::TILE, wide, 256, 256, 512},
+          std::fmax(weights, 2.5 + std::ceil(r) * (4.0 + (8.75 + 4.5 * (r < 1.0 ? r : 1.0)) * k) + tail));
   }
   if (form != FP8_WGRAD) {
     auto rounds = [&](int bm) { return groups(bm, 16) > 1.0 ? groups(bm, 16) : 1.0; };
-    offer({Choice::SKINNY, wide, 64, 16, 512}, 2.4 + rounds(64) * (1.3 + 2.4 * k));
-    offer({Choice::SKINNY, wide, 32, 16, 512}, 2.6 + rounds(32) * (0.8 + 1.41 * k));
-    offer({Choice::SKINNY, wide, 16, 16, 512}, 2.6 + rounds(16) * (0.8 + 0.98 * k));
+    offer({Choice::SKINNY, wide, 64, 16, 512}, 2.4 + rounds(64) * (1.3 + (experts ? 1.2 : 2.4) * k));
+    offer({Choice::SKINNY, wide, 32, 16, 512}, 2.6 + rounds(32) * (0.8 + (experts ? 0.9 : 1.41) * k));
+    offer({Choice::SKINNY, wide, 16, 16, 512}, 2.6 + rounds(16) * (experts ? 0.6 + 0.74 * k : 0.8 + 0.98 * k));
   }
   return best;
 }
