@@ -184,6 +184,41 @@ __device__ __forceinline__ void store8(T* p, int valid, const float (&v)[8]) {
       if (i < valid) p[i] = from_f32<T>(v[i]);
   }
 }
+
+// load8 and store8, for what is used once.
+template <class T>
+__device__ __forceinline__ void load8_once(const T* p, int valid, float (&v)[8]) {
+  typedef int words __attribute__((ext_vector_type(4), aligned(2)));
+  if (valid >= 8) {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const words w = __builtin_nontemporal_load((const words*)p + i);
+      __builtin_memcpy((char*)e + 16 * i, &w, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+  } else {
+    load8(p, valid, v);
+  }
+}
+template <class T>
+__device__ __forceinline__ void store8_once(T* p, int valid, const float (&v)[8]) {
+  typedef int words __attribute__((ext_vector_type(4), aligned(2)));
+  if (valid >= 8) {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(v[i]);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      words w;
+      __builtin_memcpy(&w, (const char*)e + 16 * i, 16);
+      __builtin_nontemporal_store(w, (words*)p + i);
+    }
+  } else {
+    store8(p, valid, v);
+  }
+}
 #endif
 
 }  // namespace sgemm_impl

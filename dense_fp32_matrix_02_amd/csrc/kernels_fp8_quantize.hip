@@ -51,9 +51,13 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float s) {
   return uint2{(uint32_t)lo, (uint32_t)hi};
 }
 
+template <bool ONCE = false>
 __device__ __forceinline__ void store_bytes(uint8_t* p, uint2 b, int valid) {
+  typedef uint32_t words __attribute__((ext_vector_type(2), aligned(1)));
   if (valid >= 8) {
-    __builtin_memcpy(p, &b, 8);
+    const words w = {b.x, b.y};
+    if constexpr (ONCE) __builtin_nontemporal_store(w, (words*)p);
+    else *(words*)p = w;
   } else {
     const uint64_t w = ((uint64_t)b.y << 32) | b.x;
 #pragma unroll
@@ -153,7 +157,9 @@ __device__ __forceinline__ void slot_rows(const QuantArgs& a, int slot, int& beg
 // Columns. 256 threads hold 128 rows by 128 columns, eight columns of eight
 // consecutive rows each (thread t: columns 8*(t%16) on, rows 8*(t/16) on), so
 // each of a thread's columns is eight bytes of a row of Q. The transposed
-// tile goes through LDS, from where a wave writes whole rows' 128 bytes.
+// tile goes through LDS, from where a wave writes whole rows' 128 bytes. X and Q
+// go past the caches: 8192 x 4096 FP32 takes 39 us (4.3 TB/s), 46 with ordinary
+// loads and stores.
 template <class T>
 __global__ void __launch_bounds__(256) quantize_cols_kernel(QuantArgs a, int slots) {
   constexpr int kPitch = kBlock + 16;
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(QuantArgs a, int slo
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int src = row0 + i < end ? source_row(a, row0 + i) : -1;
-    load8((const T*)a.X + (int64_t)(src < 0 ? 0 : src) * a.ldx + col, src < 0 ? 0 : valid, v[i]);
+    load8_once((const T*)a.X + (int64_t)(src < 0 ? 0 : src) * a.ldx + col, src < 0 ? 0 : valid, v[i]);
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(QuantArgs a, int slo
   for (int i = 0; i < 8; ++i) {
     const int c = t / 16 + 16 * i;
     if (c0 + c < a.cols)
-      store_bytes(a.Q + (int64_t)(c0 + c) * a.ldq + at, *(const uint2*)(tile + c * kPitch + 8 * (t % 16)), room);
+      store_bytes<true>(a.Q + (int64_t)(c0 + c) * a.ldq + at, *(const uint2*)(tile + c * kPitch + 8 * (t % 16)), room);
   }
 }
 

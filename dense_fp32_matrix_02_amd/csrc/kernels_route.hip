@@ -10,16 +10,20 @@ constexpr int kNone = 0x7FFFFFFF;
 
 // ---- routing ------------------------------------------------------------------
 //
-// One wave has one token; lane l holds experts l*V .. l*V + V-1. Scores and
-// choice values are FP64: two experts whose values differ by less than FP32
-// tells apart are still ordered as the formula orders them, and FP64 vector
-// instructions run at the rate of FP32 ones here.
+// A wave has one token; lane l holds experts l*V .. l*V + V-1. Scores and choice
+// values are FP64: two experts whose values differ by less than FP32 tells apart
+// are still ordered as the formula orders them, and FP64 vector instructions run
+// at the rate of FP32 ones here. Bound by the vector unit: a score is about 70
+// instructions, a choice is a search of the lane's experts and a reduction over
+// the lanes. 8192 tokens, 8 of 256 experts from 4 of 8 groups: 18 us; 52 with
+// reductions as shuffles through LDS instead of in the vector unit (DPP), 24
+// with loads of single logits and biases under conditions. With 16 lanes to a
+// token, so that a reduction serves four tokens, it takes 19 us, and 15 where
+// this takes 8 (2048 tokens).
 //
-// Reductions over the wave run in the vector unit (DPP), not as shuffles
-// through LDS: 8192 tokens of 256 experts, 8 of 4 of 8 groups, took 52 us with
-// shuffles. A choice value is compared as a 64-bit key whose halves are
-// reduced one after the other: the largest first half, then, if several lanes
-// have it, the largest second half among them, then the first lane that has both.
+// A choice value is compared as a 64-bit key whose halves are reduced one after
+// the other: the largest first half, then, if several lanes have it, the largest
+// second half among them, then the first lane that has both.
 
 template <class T>
 __device__ __forceinline__ double to_f64(T x) { return (double)to_f32(x); }
@@ -35,31 +39,32 @@ __device__ __forceinline__ double dpp(double x, double none) {
   const uint32_t lo = dpp<CONTROL, ROWS>((uint32_t)b, (uint32_t)n), hi = dpp<CONTROL, ROWS>((uint32_t)(b >> 32), (uint32_t)(n >> 32));
   return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
-// f over all lanes, in every lane: shifts by 1, 2, 4, 8 within rows of 16 lanes,
-// then rows 0 to 1 and 2 to 3, then 1 to 3; the last lane has it all.
-template <class X, class F>
-__device__ __forceinline__ X wave_reduce(X x, X none, F&& f) {
-  x = f(x, dpp<0x111, 0xF>(x, none));
-  x = f(x, dpp<0x112, 0xF>(x, none));
-  x = f(x, dpp<0x114, 0xF>(x, none));
-  x = f(x, dpp<0x118, 0xF>(x, none));
-  x = f(x, dpp<0x142, 0xA>(x, none));
-  return f(x, dpp<0x143, 0xC>(x, none));
-}
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)x, lane); }
 __device__ __forceinline__ double lane_value(double x, int lane) {
   const uint64_t b = __double_as_longlong(x);
   const uint32_t lo = lane_value((uint32_t)b, lane), hi = lane_value((uint32_t)(b >> 32), lane);
   return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
-__device__ __forceinline__ uint32_t wave_most(uint32_t x) {
-  return lane_value(wave_reduce(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }), 63);
+// f over all lanes, in every lane: shifts by 1, 2, 4, 8 within rows of 16 lanes,
+// then rows 0 to 1 and 2 to 3, then 1 to 3; the last lane has it all.
+template <class X, class F>
+__device__ __forceinline__ X reduce(X x, X none, F&& f) {
+  x = f(x, dpp<0x111, 0xF>(x, none));
+  x = f(x, dpp<0x112, 0xF>(x, none));
+  x = f(x, dpp<0x114, 0xF>(x, none));
+  x = f(x, dpp<0x118, 0xF>(x, none));
+  x = f(x, dpp<0x142, 0xA>(x, none));
+  x = f(x, dpp<0x143, 0xC>(x, none));
+  return lane_value(x, 63);
 }
-__device__ __forceinline__ double wave_sum(double x) {
-  return lane_value(wave_reduce(x, 0.0, [](double a, double b) { return a + b; }), 63);
+__device__ __forceinline__ uint32_t most_of(uint32_t x) {
+  return reduce(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ double wave_max(double x) {
-  return lane_value(wave_reduce(x, (double)-INFINITY, [](double a, double b) { return fmax(a, b); }), 63);
+__device__ __forceinline__ double sum_of(double x) {
+  return reduce(x, 0.0, [](double a, double b) { return a + b; });
+}
+__device__ __forceinline__ double max_of(double x) {
+  return reduce(x, (double)-INFINITY, [](double a, double b) { return fmax(a, b); });
 }
 
 // Orders like the number, NaN as minus infinity; never 0, which stands for none.
@@ -71,125 +76,145 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 // The lanes that hold the largest key.
 __device__ __forceinline__ uint64_t lanes_of_most(uint64_t key) {
   const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
-  const uint32_t most_hi = wave_most(hi);
+  const uint32_t most_hi = most_of(hi);
   const uint64_t lanes = __ballot(hi == most_hi);
-  if ((lanes & (lanes - 1)) == 0) return lanes;
-  const uint32_t most_lo = wave_most(hi == most_hi ? lo : 0);
+  if (__popcll(lanes) == 1) return lanes;
+  const uint32_t most_lo = most_of(hi == most_hi ? lo : 0);
   return __ballot(hi == most_hi && lo == most_lo);
 }
 
-// Scores of the wave's token; experts past the last get 0. A NaN logit of a
-// softmax makes the whole row NaN.
+// A wave's accesses to its own LDS stay in order.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Scores of the token; experts past the last get 0. A NaN logit of a softmax
+// makes the whole row NaN.
 template <class T, int SCORE, int V>
-__device__ __forceinline__ void scores(const T* row, int experts, int lane, double (&s)[V]) {
+__device__ __forceinline__ void scores(const T* row, int experts, int l, double (&s)[V]) {
+  if (l * V + V <= experts) {
+    T x[V];
+    __builtin_memcpy(x, row + l * V, sizeof(x));
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane * V + v;
-    s[v] = e < experts ? to_f64(row[e]) : -INFINITY;
+    for (int v = 0; v < V; ++v) s[v] = to_f64(x[v]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = l * V + v < experts ? to_f64(row[l * V + v]) : -INFINITY;
   }
   if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
     double most = s[0], sum = 0.0;
 #pragma unroll
     for (int v = 1; v < V; ++v) most = fmax(most, s[v]);
-    most = wave_max(most);
+    most = max_of(most);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      s[v] = lane * V + v < experts ? exp(s[v] - most) : 0.0;
+      s[v] = l * V + v < experts ? exp(s[v] - most) : 0.0;
       sum += s[v];
     }
-    sum = wave_sum(sum);
+    sum = sum_of(sum);
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = lane * V + v < experts ? s[v] / sum : 0.0;
+    for (int v = 0; v < V; ++v) {
+      s[v] = l * V + v < experts ? s[v] / sum : 0.0;
+    }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 1.0 / (1.0 + exp(-s[v]));
+    for (int v = 0; v < V; ++v) {
+      s[v] = 1.0 / (1.0 + exp(-s[v]));
+    }
   }
 }
 
 // Bit v: the lane's expert v is in one of the top_groups strongest groups.
+// `row`: room for the token's choice values, `keys` for a key of each group.
 template <int V>
-__device__ __forceinline__ uint32_t kept_experts(const RouteArgs& a, const double (&c)[V], int lane, double* row) {
+__device__ __forceinline__ uint32_t kept_experts(const RouteArgs& a, const double (&c)[V], int l, double* row, uint64_t* keys) {
   const int size = a.experts / a.groups;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (lane * V + v < a.experts) row[lane * V + v] = c[v];
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (l * V + v < a.experts) row[l * V + v] = c[v];
+  wave_sync();
   // L neighbouring lanes find a group's strength, each from every L-th of its
   // experts, beginning at places of their own, so that lanes of different
-  // groups read different banks. More than 64 groups take several turns.
+  // groups read different banks.
   int L = 1;
   while (2 * L * a.groups <= 64) L *= 2;
-  const int turn = 64 / L;
-  uint64_t strength[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int g = lane / L + v * turn;
-    strength[v] = 0;
-    if (v == 0 || v * turn < a.groups) {
-      double one = -INFINITY, two = -INFINITY;
-      const int n = g < a.groups ? (size - lane % L + L - 1) / L : 0;  // this lane's experts of the group
-      int at = n > 0 ? g % n : 0;
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const double x = row[g * size + lane % L + at * L];
-        two = fmax(two, fmin(one, x));
-        one = fmax(one, x);
-        at = at + 1 == n ? 0 : at + 1;
-      }
+  for (int g0 = 0; g0 < a.groups; g0 += 64 / L) {
+    const int g = g0 + l / L;
+    const int n = g < a.groups ? (size - l % L + L - 1) / L : 0;  // this lane's experts of the group
+    double one = -INFINITY, two = -INFINITY;
+    int at = n > 0 ? g % n : 0;
 #pragma unroll 1
-      for (int d = 1; d < L; d *= 2) {
-        const double x = __shfl_xor(one, d, 64), y = __shfl_xor(two, d, 64);
-        two = fmax(fmin(one, x), fmax(two, y));
-        one = fmax(one, x);
-      }
-      if (g < a.groups) strength[v] = key_of(size > 1 ? one + two : one);
+    for (int i = 0; i < n; ++i) {
+      const double x = row[g * size + l % L + at * L];
+      two = fmax(two, fmin(one, x));
+      one = fmax(one, x);
+      at = at + 1 == n ? 0 : at + 1;
     }
+#pragma unroll 1
+    for (int d = 1; d < L; d *= 2) {
+      const double x = __shfl_xor(one, d, 64), y = __shfl_xor(two, d, 64);
+      two = fmax(fmin(one, x), fmax(two, y));
+      one = fmax(one, x);
+    }
+    if (g < a.groups && l % L == 0) keys[g] = key_of(size > 1 ? one + two : one);
   }
-  int group[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) group[v] = (lane * V + v) / size;
-  uint32_t kept = 0;
+  wave_sync();
+  int* kept = (int*)row;  // of each group, in the values' place
+  for (int g = l; g < a.groups; g += 64) kept[g] = 0;
   for (int r = 0; r < a.top_groups; ++r) {
     uint64_t best = 0;
     int mine = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (strength[v] > best) best = strength[v], mine = lane / L + v * turn;
+    for (int g = l; g < a.groups; g += 64) {
+      const uint64_t k = keys[g];
+      if (k > best) best = k, mine = g;
+    }
     const uint64_t lanes = lanes_of_most(best);
     int g = (int)lane_value((uint32_t)mine, __builtin_ctzll(lanes));
-    // More than 64 groups: of equal ones the lowest need not be the first lane's.
-    if (a.groups > 64) g = kNone - (int)wave_most(lanes >> lane & 1 ? (uint32_t)(kNone - mine) : 0u);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (lane / L + v * turn == g) strength[v] = 0;
-      if (group[v] == g) kept |= 1u << v;
-    }
+    // More groups than lanes: of equal ones the lowest need not be the first lane's.
+    if (a.groups > 64) g = kNone - (int)most_of(lanes >> l & 1 ? (uint32_t)(kNone - mine) : 0u);
+    if (g % 64 == l) keys[g] = 0, kept[g] = 1;
   }
-  return kept;
+  wave_sync();
+  // e / size for e < 1024 as a product: the quotient's excess is under 2^-10.
+  const uint32_t inverse = ((1u << 20) + size - 1) / size;
+  uint32_t open = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (l * V + v < a.experts && kept[(l * V + v) * inverse >> 20] != 0) open |= 1u << v;
+  return open;
 }
 
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
-  __shared__ double rows[4][64 * V];  // choice values, for the groups
-  const int lane = threadIdx.x % 64;
+  __shared__ double rows[4][64 * V];  // choice values, then which groups are kept
+  __shared__ uint64_t strengths[4][64 * V];
+  const int l = threadIdx.x % 64;
   const int token = blockIdx.x * 4 + threadIdx.x / 64;
   if (token >= a.tokens) return;  // whole waves
   double s[V], c[V];
-  scores<T, SCORE, V>((const T*)a.logits + (int64_t)token * a.ld, a.experts, lane, s);
+  scores<T, SCORE, V>((const T*)a.logits + (int64_t)token * a.ld, a.experts, l, s);
+  float bias[V] = {};
+  if (a.bias != nullptr) {
+    if (l * V + V <= a.experts) {
+      __builtin_memcpy(bias, a.bias + l * V, sizeof(bias));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) bias[v] = l * V + v < a.experts ? a.bias[l * V + v] : 0.0f;
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = lane * V + v;
-    c[v] = s[v];
-    if (a.bias != nullptr && e < a.experts) c[v] += (double)a.bias[e];
+    c[v] = s[v] + (double)bias[v];
     if (!(c[v] == c[v])) c[v] = -INFINITY;  // NaN ranks as minus infinity
   }
   uint32_t open = 0xFFFFFFFF;
-  if (a.groups > 1) open = kept_experts<V>(a, c, lane, rows[threadIdx.x / 64]);
+  if (a.groups > 1) open = kept_experts<V>(a, c, l, rows[threadIdx.x / 64], strengths[threadIdx.x / 64]);
   uint64_t key[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) key[v] = lane * V + v < a.experts && (open >> v & 1) ? key_of(c[v]) : 0;
+  for (int v = 0; v < V; ++v) key[v] = l * V + v < a.experts && (open >> v & 1) ? key_of(c[v]) : 0;
   double total = 0.0, mine = 0.0;
   int my_id = 0;
   for (int k = 0; k < a.choices; ++k) {
@@ -200,24 +225,24 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     for (int v = 1; v < V; ++v)
       if (key[v] > best) best = key[v], at = v, w = s[v];
     const int owner = __builtin_ctzll(lanes_of_most(best));
-    w = lane_value(w, owner);
-    const int id = owner * V + (int)lane_value((uint32_t)at, owner);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (lane * V + v == id) key[v] = 0;
+      if (l == owner && v == at) key[v] = 0;
+    w = lane_value(w, owner);
+    const int id = owner * V + (int)lane_value((uint32_t)at, owner);
     total += w;
-    if (lane == k) mine = w, my_id = id;
+    if (l == k) mine = w, my_id = id;
   }
-  if (lane < a.choices) {
+  if (l < a.choices) {
     double w = mine;
     if (a.renorm) w = total == 0.0 ? 0.0 : w / total;
-    a.weights[(int64_t)token * a.choices + lane] = (float)((double)a.scale * w);
-    a.ids[(int64_t)token * a.choices + lane] = my_id;
+    a.weights[(int64_t)token * a.choices + l] = (float)((double)a.scale * w);
+    a.ids[(int64_t)token * a.choices + l] = my_id;
   }
 }
 
-// Lane k has choice k. A sigmoid's gradient needs the chosen experts' scores
-// alone; a softmax's needs the whole row.
+// A wave has one token, lane k its choice k. A sigmoid's gradient needs the
+// chosen experts' scores alone; a softmax's needs the whole row.
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
   __shared__ double rows[4][SCORE == SGEMM_MI355_SOFTMAX ? 64 * V : 1];
@@ -238,16 +263,14 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     double* row = rows[threadIdx.x / 64];
 #pragma unroll
     for (int v = 0; v < V; ++v) row[lane * V + v] = s[v];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_sync();
     if (id >= 0) w = row[id];
   } else if (id >= 0) {
     w = 1.0 / (1.0 + exp(-to_f64(logits[id])));
   }
   // total = S, dot = sum of dw_m s_m over the chosen
   double total = 1.0, dot = 0.0;
-  if (a.renorm) total = wave_sum(w), dot = wave_sum(w * dw);
+  if (a.renorm) total = sum_of(w), dot = sum_of(w * dw);
   double d = id < 0 || total == 0.0 ? 0.0 : (double)a.scale * (dw - dot / total) / total;
   if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * (1.0 - w);
   double ds[V] = {};
@@ -262,13 +285,21 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     double inner = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) inner += ds[v] * s[v];
-    inner = wave_sum(inner);
+    inner = sum_of(inner);
 #pragma unroll
     for (int v = 0; v < V; ++v) ds[v] = s[v] * (ds[v] - inner);
   }
+  float out[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (lane * V + v < a.experts) a.dlogits[(int64_t)token * a.ldd + lane * V + v] = (float)ds[v];
+  for (int v = 0; v < V; ++v) out[v] = (float)ds[v];
+  float* to = a.dlogits + (int64_t)token * a.ldd + lane * V;
+  if (lane * V + V <= a.experts) {
+    __builtin_memcpy(to, out, sizeof(out));
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane * V + v < a.experts) to[v] = out[v];
+  }
 }
 
 // ---- the order of the experts' rows ---------------------------------------------
@@ -400,41 +431,6 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) 
 // leave fewer waves, 148, and with ordinary loads and stores too, 187.
 
 constexpr int kRows = 4, kRowsBack = 2;
-
-// load8 and store8, for what is used once.
-template <class T>
-__device__ __forceinline__ void load8_once(const T* p, int valid, float (&v)[8]) {
-  typedef int words __attribute__((ext_vector_type(4), aligned(2)));
-  if (valid >= 8) {
-    T e[8];
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      const words w = __builtin_nontemporal_load((const words*)p + i);
-      __builtin_memcpy((char*)e + 16 * i, &w, 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
-  } else {
-    load8(p, valid, v);
-  }
-}
-template <class T>
-__device__ __forceinline__ void store8_once(T* p, int valid, const float (&v)[8]) {
-  typedef int words __attribute__((ext_vector_type(4), aligned(2)));
-  if (valid >= 8) {
-    T e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(v[i]);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      words w;
-      __builtin_memcpy(&w, (const char*)e + 16 * i, 16);
-      __builtin_nontemporal_store(w, (words*)p + i);
-    }
-  } else {
-    store8(p, valid, v);
-  }
-}
 
 // A wave has 512 columns of one token and adds the choices in order.
 template <class T>
