@@ -13,7 +13,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import OK, SgemmError, _ld, load
+from ._binding import OK, SgemmError, load
+from ._binding import _ld as _any_ld
 
 ERR_TYPE, ERR_ROUTE = -13, -14
 F32, BF16, F16 = 0, 1, 2
@@ -67,15 +68,35 @@ class _Library:
 _c = _Library(_SIGNATURES)
 
 # The calls below are made for single tokens too, where the host's time counts:
-# what they ask torch for, they ask once.
+# an import statement in each, or asking a tensor twice, shows.
 _types = {}
+
+
+class _Torch:
+    """torch, imported at the first use of an attribute (the C calls work without it)."""
+
+    def __getattr__(self, name):
+        import torch
+
+        value = getattr(torch, name)
+        setattr(self, name, value)
+        return value
+
+
+torch = _Torch()
+
+
+def _ld(x, name):
+    """Row stride of a 2-D tensor with contiguous rows."""
+    strides, shape = x.stride(), x.shape
+    if len(strides) == 2 and strides[1] == 1 and shape[0] > 1 and strides[0] >= shape[1] > 0:
+        return strides[0]
+    return _any_ld(x, name)
 
 
 def _type_of(dtype, name):
     code = _types.get(dtype)
     if code is None:
-        import torch
-
         _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
         code = _types.get(dtype)
         if code is None:
@@ -84,8 +105,6 @@ def _type_of(dtype, name):
 
 
 def _stream_of(x, stream):
-    import torch
-
     # The handle of torch.cuda.current_stream without a Stream object.
     return torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else stream.cuda_stream
 
@@ -94,8 +113,6 @@ def _empty(shape, dtype, device, stream, strides=None):
     """A tensor from torch's caching allocator, allocated on the stream the
     call runs on, so that the allocator hands its memory out again only after
     that stream's work."""
-    import torch
-
     if strides is None:
         strides = (max(shape[-1], 1), 1)[-len(shape):] if len(shape) < 3 else (shape[1] * shape[2], shape[2], 1)
     if stream is None:
@@ -112,8 +129,6 @@ def _gpu(x, name, dtype=None):
 
 def _ints(x, name, length=None):
     """Address of a dense 1-D int32 GPU tensor."""
-    import torch
-
     _gpu(x, name, torch.int32)
     if x.dim() != 1 or (x.numel() > 1 and x.stride(0) != 1) or (length is not None and x.numel() != length):
         raise ValueError(f"{name} must be a dense 1-D tensor" + ("" if length is None else f" of {length} values"))
@@ -131,8 +146,6 @@ def _blocks(n):
 
 def _bytes_out(rows, cols, device, stream):
     """An uninitialised e4m3 matrix whose row stride is a multiple of 16 bytes, and that stride."""
-    import torch
-
     ld = max(cols + -cols % 16, 1)
     return _empty((rows, cols), torch.float8_e4m3fn, device, stream, (ld, 1)), ld
 
@@ -145,8 +158,6 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
     gives zeros. ``blocks``: one scale for each 128 x 128 tile instead, for
     weights; S then has a row for each 128 rows of X.
     """
-    import torch
-
     _gpu(X, "X")
     kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
     rows, cols = X.shape
@@ -181,8 +192,6 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
     begin a block, expert e's block offsets[e] // 128 + e; Q then has
     128 * (n // 128 + experts) columns, zero where no row is.
     """
-    import torch
-
     _gpu(X, "X")
     kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
     rows, cols = X.shape
@@ -205,8 +214,6 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
 def _operand(Q, S, name, rows, cols, either=False):
     """Address, row stride, scales' address and strides, and rows that share a
     scale, of a quantised matrix (2-D, or the last two axes of a 3-D one)."""
-    import torch
-
     if Q.dtype != torch.float8_e4m3fn or not Q.is_cuda:
         raise TypeError(f"{name} must be a float8_e4m3fn GPU tensor")
     if S.dtype != torch.float32 or not S.is_cuda:
@@ -240,8 +247,6 @@ def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, stream=None
     the quantisers give them. C is allocated with ``dtype`` (bfloat16 unless
     given) when omitted.
     """
-    import torch
-
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
     (M, K), (N, K2) = A.shape, B.shape
@@ -262,8 +267,6 @@ def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, stream=None):
     for its rows (experts x N x K/128) or tiles (experts x N/128 x K/128).
     Rows from offsets[-1] on are set to zero.
     """
-    import torch
-
     if A.dim() != 2 or B.dim() != 3 or SB.dim() != 3 or SB.shape[0] != B.shape[0] or B.shape[0] < 1:
         raise ValueError("A must be 2-D, B and its scales 3-D with the experts first")
     (R, K), (E, N, K2) = A.shape, B.shape
@@ -285,8 +288,6 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
     ``offsets``; C is experts x M x N, allocated with ``dtype`` (float32 unless
     given) when omitted.
     """
-    import torch
-
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
     (M, P), (N, P2) = A.shape, B.shape

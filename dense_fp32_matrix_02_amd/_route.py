@@ -8,8 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import _ld
-from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _Library, _P, _stream_of, _type_of
+from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _ld, _Library, _P, _stream_of, _type_of, torch
 
 SOFTMAX, SIGMOID = 0, 1
 MAX_EXPERTS, MAX_CHOICES = 1024, 32
@@ -56,8 +55,6 @@ def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1,
     groups with the largest sum of their two largest choice values take part;
     ``renorm`` divides the weights by their sum; ``scale`` multiplies them.
     """
-    import torch
-
     _gpu(logits, "logits")
     kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
     tokens, experts = logits.shape
@@ -74,8 +71,6 @@ def route_backward(logits, experts, dweights, *, score: str = "softmax", renorm:
                    stream=None):
     """The gradient of the logits (float32) for given gradients of route's
     weights; ``experts`` are the ones it chose."""
-    import torch
-
     _gpu(logits, "logits")
     kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
     tokens, count = logits.shape
@@ -97,8 +92,6 @@ def route_plan(experts, num_experts: int, *, stream=None):
     of token tokens[r]; choice j of token t has row place[t, j]. Ids outside
     the experts come after offsets[-1].
     """
-    import torch
-
     if experts.dim() != 2:
         raise ValueError("experts must be tokens x k")
     tokens, k = experts.shape
@@ -117,8 +110,6 @@ def route_plan(experts, num_experts: int, *, stream=None):
 def route_combine(Z, place, weights, Y=None, *, stream=None):
     """Y[t] = sum_j weights[t, j] * Z[place[t, j]], of Z's dtype; a place
     outside Z's rows adds nothing."""
-    import torch
-
     _gpu(Z, "Z")
     kind, ldz = _type_of(Z.dtype, "Z"), _ld(Z, "Z")
     rows, cols = Z.shape
@@ -140,8 +131,6 @@ def route_combine_backward(dY, Z, place, weights, *, stream=None):
     place must name each row of Z once, as route_plan's does: rows that it does
     not name are not written.
     """
-    import torch
-
     _gpu(Z, "Z")
     _gpu(dY, "dY", Z.dtype)
     kind, ldz, ldy = _type_of(Z.dtype, "Z"), _ld(Z, "Z"), _ld(dY, "dY")
