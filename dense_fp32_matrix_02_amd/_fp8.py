@@ -114,7 +114,7 @@ def _empty(shape, dtype, device, stream, strides=None):
     call runs on, so that the allocator hands its memory out again only after
     that stream's work."""
     if strides is None:
-        strides = (max(shape[-1], 1), 1)[-len(shape):] if len(shape) < 3 else (shape[1] * shape[2], shape[2], 1)
+        strides = (shape[1] or 1, 1) if len(shape) == 2 else (1,) if len(shape) == 1 else (shape[1] * shape[2], shape[2], 1)
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)  # cheaper than torch.empty here
     with torch.cuda.stream(stream):

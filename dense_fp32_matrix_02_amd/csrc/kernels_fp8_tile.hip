@@ -30,7 +30,7 @@ struct TileShape {
 };
 
 template <int FORM, bool WIDE, bool TALL, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(Fp8Args g) {
+__global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
   using S = TileShape<BM, BN, WM, WN>;
   constexpr int MF = S::MF, NF = S::NF, NT = S::NT, ROWS = S::ROWS;
   // One array per stage, so that the compiler sees that reads of one do not
