@@ -85,15 +85,22 @@ struct Frag<true> {
   }
 };
 
-// The 16 x 16 products of two fragments over a block: rows of the result are
-// b's rows, columns a's; lane l holds rows 4*(l/16) .. +3 of column l%16.
-__device__ __forceinline__ f32x4 block_product(const Frag<false>& b, const Frag<false>& a) {
+// Step x of STEPS of the 16 x 16 products of two fragments over a block: rows
+// of the result are b's rows, columns a's; lane l holds rows 4*(l/16) .. +3 of
+// column l%16. Step 0 begins from zero.
+template <bool WIDE>
+constexpr int kSteps = WIDE ? 4 : 1;
+__device__ __forceinline__ f32x4 block_step(const Frag<false>& b, const Frag<false>& a, int, f32x4) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 block_product(const Frag<true>& b, const Frag<true>& a) {
-  f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+__device__ __forceinline__ f32x4 block_step(const Frag<true>& b, const Frag<true>& a, int x, f32x4 p) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[x], a.v[x], x == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p, 0, 0, 0);
+}
+template <bool WIDE>
+__device__ __forceinline__ f32x4 block_product(const Frag<WIDE>& b, const Frag<WIDE>& a) {
+  f32x4 p = {};
 #pragma unroll
-  for (int x = 0; x < 4; ++x) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[x], a.v[x], p, 0, 0, 0);
+  for (int x = 0; x < kSteps<WIDE>; ++x) p = block_step(b, a, x, p);
   return p;
 }
 

@@ -164,13 +164,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
   // There is no branch in a step: the compiler would move additions behind it.
   f32x4 acc[NF][MF] = {}, p[MF] = {};
   Frag<WIDE> fa[MF];
-  i32x4 raw[2][2];
+  i32x4 raw[2][2], raw_a[MF][2];
   float sa[MF] = {}, sa_before[MF] = {};
   f32x4 sv_before, sv = {}, sv_next = {};  // without TALL: B's scales of the groups before, at and after this one
   const int at0 = r16 * kBlock + 16 * swz(r16, quad), at1 = at0 ^ 64;
   auto read_a = [&](int i, const uint8_t* slab) __attribute__((always_inline)) {
     const uint8_t* a = slab + (wm + 16 * i) * kBlock;
-    fa[i].set(*(const i32x4*)(a + at0), *(const i32x4*)(a + at1));
+    raw_a[i][0] = *(const i32x4*)(a + at0), raw_a[i][1] = *(const i32x4*)(a + at1);
+  };
+  // Apart from the reads, which widening has to wait for.
+  auto set_a = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i) fa[i].set(raw_a[i][0], raw_a[i][1]);
   };
   auto read_b = [&](int j, const uint8_t* slab, const float* scale) __attribute__((always_inline)) {
     const uint8_t* b = slab + (BM + wn + 16 * j) * kBlock;
@@ -203,19 +208,27 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
       }
       if (j + 1 < NF) load(b + 1, b + 1 < full, next, min((j + 1) * PER, S::REGIONS), min((j + 2) * PER, S::REGIONS));
       __builtin_amdgcn_sched_barrier(0);
+      if (j == 0) set_a();
       Frag<WIDE> fb;
       fb.set(raw[j & 1][0], raw[j & 1][1]);
+      // A step of all fragments before the next step of any: a fragment's steps
+      // depend on each other.
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        if (j > 0) add(acc[j - 1][i], i, sa, sv_before);
-        else add(acc[NF - 1][i], i, sa_before, sv_before);
-        p[i] = block_product(fb, fa[i]);
-        // After the group's first product: the compiler waits for every
-        // outstanding LDS read before it.
-        if (i == 0 && j + 1 < NF) read_b(j + 1, cur, scur);
-        if (i == 0 && j + 1 == NF) read_b(0, next, snext);
-        if (j + 1 == NF) read_a(i, next);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int x = 0; x < kSteps<WIDE>; ++x) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          if (x == 0) {
+            if (j > 0) add(acc[j - 1][i], i, sa, sv_before);
+            else add(acc[NF - 1][i], i, sa_before, sv_before);
+          }
+          p[i] = block_step(fb, fa[i], x, p[i]);
+          // After the group's first product: the compiler waits for every
+          // outstanding LDS read before it.
+          if (x == 0 && i == 0 && j + 1 < NF) read_b(j + 1, cur, scur);
+          if (x == 0 && i == 0 && j + 1 == NF) read_b(0, next, snext);
+          if (x == kSteps<WIDE> - 1 && j + 1 == NF) read_a(i, next);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
 #pragma unroll
@@ -227,6 +240,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
     read_scales(scale1);
 #pragma unroll
     for (int i = 0; i < MF; ++i) read_a(i, slab1);
+    set_a();
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       Frag<WIDE> fb;
