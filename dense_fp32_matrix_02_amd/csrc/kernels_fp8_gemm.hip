@@ -140,7 +140,7 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
   //   few-rows kernel, 16, 32, 64 rows   27.2, 18.8, 15.0 / 97, 65, 55 / -, -, 210
   //   128 x 128 tiles, 256 x 256 tiles   13.0, 17.1 / 14.2, 24.3 / 24.5, 28.3
   // Widened values need more registers than the strip of a wave of a 256 x 256
-  // tile leaves, so that form has 128 x 128 tiles only (24.4 us at M 512, fp32).
+  // tile leaves, so that form has smaller tiles only (24.4 us at M 512, fp32).
   const double k = g.K / 1024.0 / (form == FP8_WGRAD ? g.experts : 1);
   auto groups = [&](int bm, int bn) {
     // An expert with rows has one tile of rows, and half a tile more on average
@@ -165,6 +165,11 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
   const double r = std::ceil(groups(128, 128));
   offer({Choice::TILE, wide, 128, 128, 256},
         std::fmax(weights, (wide ? 2.5 + r * (4.0 + 8.4 * k) : 1.0 + r * (3.3 + 4.2 * k)) + tail));
+  // Widened values take 192 x 128 tiles where these fit one round and 128 x 128
+  // tiles do not, so that some CUs would work on two (N 4096, K 2048, fp32: M
+  // 1536 33.3 us against 37.6; else they are slower: M 768 30.2 against 26.4,
+  // M 2304 56.8 against 55.3).
+  if (wide && form == FP8_DENSE && groups(192, 128) <= 1.0) offer({Choice::TILE, wide, 192, 128, 512}, 8.0 + 12.6 * k + tail);
   if (!wide) {
     const double r = groups(256, 256);
     offer({Choice::TILE, wide, 256, 256, 512},

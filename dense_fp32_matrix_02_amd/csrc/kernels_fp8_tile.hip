@@ -36,7 +36,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
   // One array per stage, so that the compiler sees that reads of one do not
   // wait for loads into the other.
   __shared__ __align__(1024) uint8_t slab0[ROWS * kBlock], slab1[ROWS * kBlock];
-  __shared__ __align__(16) float scale0[ROWS], scale1[ROWS];
+  constexpr int NS = (ROWS + NT - 1) / NT;  // scales per thread: every thread has a place for them, so that no step has a branch
+  __shared__ __align__(16) float scale0[NS * NT], scale1[NS * NT];
   Tile t;
   if (!find_tile<FORM, BM, BN>(g, t)) return;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -68,8 +69,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
     }
   };
   // This thread's scales: rows tid (+ NT ..) of the slab, of the same operand for the whole wave.
-  constexpr int NS = (ROWS + NT - 1) / NT;
-  static_assert(ROWS % NT == 0 && BM % 64 == 0, "every thread has scales, a wave's are of one operand");
+  static_assert(ROWS % 64 == 0 && BM % 64 == 0, "a wave's scales are of one operand");
   const float* scales[NS];
   int64_t scale_step[NS];
 #pragma unroll
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int r = tid + i * NT;
+      if (ROWS % NT != 0 && 64 * wave + i * NT >= ROWS) break;
       *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, tail / 16)) = chunks[i];
       for (int c = tail / 16 + 1; c < 8; ++c) *(i32x4*)(slab1 + r * kBlock + 16 * swz(r, c)) = i32x4{0, 0, 0, 0};
     }
@@ -275,7 +276,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
   // fetching it costs more than running it (with a copy of the stores for each
   // fragment this took 3.5 us of a tile, unrolled wholly 8 us of a 256 x 256 one).
   constexpr int WIDTH = 16 * NF, LANES = WIDTH / 8;  // floats of a row of the strip, and lanes that store one
-  constexpr int ROUND = kBlock * ROWS * 2 / S::NW / (16 * WIDTH * 4) < MF ? kBlock * ROWS * 2 / S::NW / (16 * WIDTH * 4) : MF;
+  constexpr int ROOM = kBlock * ROWS * 2 / S::NW / (16 * WIDTH * 4);  // fragments that a wave's share of the slabs holds
+  constexpr int ROUND = ROOM >= MF ? MF : ROOM >= 2 && MF % 2 == 0 ? 2 : 1;
   static_assert(ROUND >= 1 && MF % ROUND == 0, "whole rounds");
   float* out = (float*)(wave < S::NW / 2 ? slab0 : slab1) + wave % (S::NW / 2) * (ROUND * 16 * WIDTH);
   __syncthreads();  // all reads of the slabs have been made
@@ -334,6 +336,9 @@ const void* of_shape(Fp8Form form, bool tall) {
 
 const void* fp8_tile_kernel_for(Fp8Form form, bool wide, bool tall, int bm) {
   if (bm == 256) return of_shape<false, 256, 256, 4, 2>(form, tall);
+  if (bm == 192)  // dense products into FP32 only
+    return tall ? (const void*)&fp8_tile_kernel<FP8_DENSE, true, true, 192, 128, 4, 2>
+                : (const void*)&fp8_tile_kernel<FP8_DENSE, true, false, 192, 128, 4, 2>;
   return wide ? of_shape<true, 128, 128, 2, 2>(form, tall) : of_shape<false, 128, 128, 2, 2>(form, tall);
 }
 

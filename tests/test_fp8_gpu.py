@@ -160,6 +160,20 @@ def test_product(M, N, K, tall):
         check_product(C, R.values(R.bytes_of(A), sa.cpu().numpy()), R.values(R.bytes_of(B), sb.cpu().numpy(), tall), K, kind)
 
 
+@pytest.mark.parametrize("tall", [1, 128])
+@pytest.mark.parametrize("M,N,K,pad", [(1500, 4060, 300, 1), (3001, 2047, 400, 0), (1345, 3969, 128, 4), (2880, 2050, 16, 0)])
+def test_product_of_many_rows_in_fp32(M, N, K, pad, tall):
+    """More 128 x 128 tiles of C than the chip has CUs: some of two rounds, partial rows, columns and blocks."""
+    A, B = R.random_bytes(M, K, 1, -K % 16), R.random_bytes(N, K, 2, -K % 16)
+    sa, sb = R.random_scales(M, -(-K // 128), 3), R.random_scales(-(-N // tall), -(-K // 128), 4, tall == 1)
+    room = torch.randn(M, N + pad, generator=torch.Generator().manual_seed(5)).to("cuda")
+    before = room.clone()
+    sg.gemm_fp8(A, sa, B, sb, room[:, :N], beta=0.5)
+    a, b = R.values(R.bytes_of(A), sa.cpu().numpy()), R.values(R.bytes_of(B), sb.cpu().numpy(), tall)
+    check_product(room[:, :N], a, b, K, "fp32", 0.5 * before[:, :N].double().cpu().numpy())
+    assert torch.equal(room[:, N:], before[:, N:])
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 70, 200), (40, 256, 384), (130, 200, 700), (300, 520, 1300)])
 def test_product_of_whole_numbers_is_exact(M, N, K):
     for tall in (1, 128):
