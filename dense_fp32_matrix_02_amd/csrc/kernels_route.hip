@@ -14,12 +14,14 @@ constexpr int kNone = 0x7FFFFFFF;
 // values are FP64: two experts whose values differ by less than FP32 tells apart
 // are still ordered as the formula orders them, and FP64 vector instructions run
 // at the rate of FP32 ones here. Bound by the vector unit: a score is about 70
-// instructions, a choice is a search of the lane's experts and a reduction over
-// the lanes. 8192 tokens, 8 of 256 experts from 4 of 8 groups: 18 us; 52 with
-// reductions as shuffles through LDS instead of in the vector unit (DPP), 24
-// with loads of single logits and biases under conditions. With 16 lanes to a
-// token, so that a reduction serves four tokens, it takes 19 us, and 15 where
-// this takes 8 (2048 tokens).
+// instructions, a choice is a reduction over the lanes. 8192 tokens, 8 of 256
+// experts from 4 of 8 groups: 13.5 us; 18.6 with groups by way of LDS and a
+// search of the lane's experts for each choice instead of a sort before the
+// first (1 choice without groups 7.3 us, with the sort 8.7). That form took 52
+// with reductions as shuffles through LDS instead of in the vector unit (DPP),
+// 24 with loads of single logits and biases under conditions, and 19 with 16
+// lanes to a token, so that a reduction serves four tokens (15 where it took 8,
+// at 2048 tokens).
 //
 // A choice value is compared as a 64-bit key whose halves are reduced one after
 // the other: the largest first half, then, if several lanes have it, the largest
@@ -113,11 +115,9 @@ __device__ __forceinline__ void scores(const T* row, int experts, int l, double 
       s[v] = l * V + v < experts ? exp(s[v] - most) : 0.0;
       sum += s[v];
     }
-    sum = sum_of(sum);
+    const double inverse = 1.0 / sum_of(sum);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[v] = l * V + v < experts ? s[v] / sum : 0.0;
-    }
+    for (int v = 0; v < V; ++v) s[v] = l * V + v < experts ? s[v] * inverse : 0.0;
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -187,9 +187,42 @@ __device__ __forceinline__ uint32_t kept_experts(const RouteArgs& a, const doubl
   return open;
 }
 
+// With the two largest values of the lane that CONTROL names.
+template <int CONTROL>
+__device__ __forceinline__ void with_two_of(double& one, double& two) {
+  const double x = dpp<CONTROL, 0xF>(one, one), y = dpp<CONTROL, 0xF>(two, two);
+  two = fmax(fmin(one, x), fmax(two, y));
+  one = fmax(one, x);
+}
+
+// The same where a group's experts fill L neighbouring lanes, L a power of 2 of
+// at most 16, so that a group lies in one row of 16 lanes: nothing goes through LDS.
+template <int V>
+__device__ __forceinline__ uint32_t kept_neighbours(const RouteArgs& a, const double (&c)[V], int l, int L) {
+  double one = c[0], two = -INFINITY;
+#pragma unroll
+  for (int v = 1; v < V; ++v) {
+    two = fmax(two, fmin(one, c[v]));
+    one = fmax(one, c[v]);
+  }
+  if (L > 1) with_two_of<0xB1>(one, two);   // lane ^ 1
+  if (L > 2) with_two_of<0x4E>(one, two);   // lane ^ 2
+  if (L > 4) with_two_of<0x141>(one, two);  // 7 - lane of 8
+  if (L > 8) with_two_of<0x140>(one, two);  // 15 - lane of 16
+  const int first = l & -L;
+  uint64_t key = l == first && l < a.groups * L ? key_of(V * L > 1 ? one + two : one) : 0;
+  uint64_t kept = 0;  // the kept groups' first lanes
+  for (int r = 0; r < a.top_groups; ++r) {
+    const int lane = __builtin_ctzll(lanes_of_most(key));
+    kept |= 1ull << lane;
+    if (l == lane) key = 0;
+  }
+  return kept >> first & 1 ? 0xFFFFFFFF : 0;
+}
+
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
-  __shared__ double rows[4][64 * V];  // choice values, then which groups are kept
+  __shared__ double rows[4][64 * V];  // choice values, then which groups are kept, then scores
   __shared__ uint64_t strengths[4][64 * V];
   const int l = threadIdx.x % 64;
   const int token = blockIdx.x * 4 + threadIdx.x / 64;
@@ -211,33 +244,70 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     if (!(c[v] == c[v])) c[v] = -INFINITY;  // NaN ranks as minus infinity
   }
   uint32_t open = 0xFFFFFFFF;
-  if (a.groups > 1) open = kept_experts<V>(a, c, l, rows[threadIdx.x / 64], strengths[threadIdx.x / 64]);
+  double* row = rows[threadIdx.x / 64];
+  if (a.groups > 1) {
+    const int size = a.experts / a.groups, L = size / V;
+    open = L * V == size && (L & (L - 1)) == 0 && L <= 16 ? kept_neighbours<V>(a, c, l, L)
+                                                          : kept_experts<V>(a, c, l, row, strengths[threadIdx.x / 64]);
+  }
   uint64_t key[V];
+  int at[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) key[v] = l * V + v < a.experts && (open >> v & 1) ? key_of(c[v]) : 0;
-  double total = 0.0, mine = 0.0;
-  int my_id = 0;
+  for (int v = 0; v < V; ++v) key[v] = l * V + v < a.experts && (open >> v & 1) ? key_of(c[v]) : 0, at[v] = v;
+  wave_sync();
+#pragma unroll
+  for (int v = 0; v < V; ++v) row[l * V + v] = s[v];
+  // A lane's experts in their order, equal ones by index, so that a choice takes
+  // the first of them and moves up the rest. More than 4 are searched anew for
+  // each choice instead, since the sort grows with their square.
+  constexpr bool SORTED = V <= 4;
+  if constexpr (SORTED) {
+#pragma unroll
+    for (int round = 0; round < V; ++round)
+#pragma unroll
+      for (int v = round % 2; v + 1 < V; v += 2) {
+        const bool swap = key[v + 1] > key[v];
+        const uint64_t high = swap ? key[v + 1] : key[v], low = swap ? key[v] : key[v + 1];
+        const int first = swap ? at[v + 1] : at[v], second = swap ? at[v] : at[v + 1];
+        key[v] = high, key[v + 1] = low, at[v] = first, at[v + 1] = second;
+      }
+  }
+  uint32_t order = 0;  // the experts' numbers in the lane, a byte each
+  if constexpr (SORTED) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) order |= (uint32_t)at[v] << (8 * v);
+  }
+  int id = 0;  // of choice l
   for (int k = 0; k < a.choices; ++k) {
     uint64_t best = key[0];
-    int at = 0;
-    double w = s[0];
+    if constexpr (!SORTED) {
+      order = 0;
 #pragma unroll
-    for (int v = 1; v < V; ++v)
-      if (key[v] > best) best = key[v], at = v, w = s[v];
+      for (int v = 1; v < V; ++v)
+        if (key[v] > best) best = key[v], order = v;
+    }
     const int owner = __builtin_ctzll(lanes_of_most(best));
+    const int chosen = owner * V + (int)(lane_value(order, owner) & 0xFF);
+    if (l == k) id = chosen;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (l == owner && v == at) key[v] = 0;
-    w = lane_value(w, owner);
-    const int id = owner * V + (int)lane_value((uint32_t)at, owner);
-    total += w;
-    if (l == k) mine = w, my_id = id;
+    for (int v = 0; v < V; ++v) {
+      if constexpr (SORTED) {
+        key[v] = l != owner ? key[v] : v + 1 < V ? key[v + 1] : 0;
+      } else if (l == owner && v == (int)order) {
+        key[v] = 0;
+      }
+    }
+    if constexpr (SORTED) order = l != owner ? order : order >> 8;
+  }
+  wave_sync();
+  double w = l < a.choices ? row[id] : 0.0;
+  if (a.renorm) {
+    const double total = sum_of(w);
+    w = total == 0.0 ? 0.0 : w / total;
   }
   if (l < a.choices) {
-    double w = mine;
-    if (a.renorm) w = total == 0.0 ? 0.0 : w / total;
     a.weights[(int64_t)token * a.choices + l] = (float)((double)a.scale * w);
-    a.ids[(int64_t)token * a.choices + l] = my_id;
+    a.ids[(int64_t)token * a.choices + l] = id;
   }
 }
 
@@ -245,7 +315,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 // chosen experts' scores alone; a softmax's needs the whole row.
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
-  __shared__ double rows[4][SCORE == SGEMM_MI355_SOFTMAX ? 64 * V : 1];
+  __shared__ double rows[4][64 * V];  // scores, then the lanes of the chosen experts' choices, then their gradients
   const int lane = threadIdx.x % 64;
   const int token = blockIdx.x * 4 + threadIdx.x / 64;
   if (token >= a.tokens) return;
@@ -258,9 +328,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     else dw = (double)a.dweights[(int64_t)token * a.choices + lane];
   }
   double s[V];
+  double* row = rows[threadIdx.x / 64];
   if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
     scores<T, SCORE, V>(logits, a.experts, lane, s);
-    double* row = rows[threadIdx.x / 64];
 #pragma unroll
     for (int v = 0; v < V; ++v) row[lane * V + v] = s[v];
     wave_sync();
@@ -273,13 +343,31 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
   if (a.renorm) total = sum_of(w), dot = sum_of(w * dw);
   double d = id < 0 || total == 0.0 ? 0.0 : (double)a.scale * (dw - dot / total) / total;
   if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * (1.0 - w);
+  // Through LDS to the lanes that hold the experts (8192 tokens, 8 of 256: 6.1 us;
+  // 8.5 with every choice compared with all experts). Experts that are chosen
+  // more than once are found first, and added up in the choices' order.
   double ds[V] = {};
-  for (int k = 0; k < a.choices; ++k) {
-    const int e = (int)lane_value((uint32_t)id, k);
-    const double x = lane_value(d, k);
+  wave_sync();
+  if (id >= 0) *(int*)&row[id] = lane;
+  wave_sync();
+  const bool twice = __ballot(id >= 0 && *(int*)&row[id >= 0 ? id : 0] != lane) != 0;
+  wave_sync();
+  if (!twice) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == lane * V + v) ds[v] += x;
+    for (int v = 0; v < V; ++v) row[lane * V + v] = 0.0;
+    wave_sync();
+    if (id >= 0) row[id] = d;
+    wave_sync();
+#pragma unroll
+    for (int v = 0; v < V; ++v) ds[v] = row[lane * V + v];
+  } else {
+    for (int k = 0; k < a.choices; ++k) {
+      const int e = (int)lane_value((uint32_t)id, k);
+      const double x = lane_value(d, k);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e == lane * V + v) ds[v] += x;
+    }
   }
   if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
     double inner = 0.0;

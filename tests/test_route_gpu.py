@@ -63,6 +63,40 @@ def test_route_and_gradient(case):
     assert (np.abs(dl - grad) <= 1.01 * STEP * np.abs(grad) + 1e-13 * size).all()
 
 
+@pytest.mark.parametrize("experts,groups", [
+    (2, 2), (6, 3), (48, 3), (64, 2), (64, 8), (64, 16), (128, 64), (120, 15), (128, 4), (256, 4), (256, 16), (256, 64), (240, 60),
+    (512, 4), (512, 2), (1024, 8), (1024, 64), (960, 15)])
+def test_groups_of_many_sizes(experts, groups):
+    for score in ("softmax", "sigmoid"):
+        for top in {1, (groups + 1) // 2, groups}:
+            test_route_and_gradient((11, experts, min(8, experts // groups * top), score, True, groups, top, True, 1.0, "fp32", 0))
+    # equal values, within a group and between groups
+    L = torch.randint(0, 3, (20, experts), generator=torch.Generator().manual_seed(1)).float()
+    top = (groups + 1) // 2
+    for score in ("softmax", "sigmoid"):
+        k = min(32, experts // groups * top)
+        _, ids = sg.route(L.to("cuda"), k, score=score, groups=groups, top_groups=top)
+        np.testing.assert_array_equal(ids.cpu().numpy(), R.route(L.numpy(), k, None, score, groups, top)[1])
+
+
+@pytest.mark.parametrize("experts", [5, 64, 100, 256, 700])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_repeated_ids(score, experts):
+    """Ids that are not route's own may name an expert twice: both parts count."""
+    L = logits_of(9, experts, 4)
+    ids = torch.randint(0, experts, (9, 6), generator=torch.Generator().manual_seed(2))
+    ids[0] = torch.tensor([3, 1, 3, 3, 4, 1])
+    ids[1] = 2
+    dw = torch.randn(9, 6, generator=torch.Generator().manual_seed(3))
+    got = sg.route_backward(L, ids.int().to("cuda"), dw.to("cuda"), score=score, renorm=False, scale=1.5).double().cpu().numpy()
+    S = R.route(L.cpu().numpy(), 1, None, score)[2]
+    want = np.zeros((9, experts))
+    for k in range(6):
+        want += R.route_grad(S, ids[:, k:k + 1].numpy(), dw[:, k:k + 1].double().numpy(), score, False, 1.5)
+    size = 1.5 * np.abs(dw.double().numpy()).sum(1, keepdims=True)
+    assert (np.abs(got - want) <= 1.01 * STEP * np.abs(want) + 1e-13 * size).all()
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_gradient_against_differences(score, renorm):
