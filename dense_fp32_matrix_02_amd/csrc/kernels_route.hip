@@ -529,13 +529,15 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) 
 // ---- the rows' return --------------------------------------------------------------
 //
 // Bound by the bytes of Z and dZ. A place and a weight are the same for a whole
-// wave, so they are scalars, and some rows of Z are asked for at once: 4, in
-// the backward pass 2. Z is read and Y and dZ are written past the caches (each
-// once). 4096 tokens of 8 choices of 4096 bf16 columns: 53 us forward (5.7
-// TB/s) and 122 back (4.7 TB/s); back with 8 rows at a time, whose registers
-// leave fewer waves, 148, and with ordinary loads and stores too, 187.
+// wave, so they are scalars; forward, 4 rows of Z are asked for at once. Z is
+// read and Y and dZ are written past the caches (each once). 4096 tokens of 8
+// choices of 4096 bf16 columns: 51 us forward (5.7 TB/s) and 113 back (5.0
+// TB/s, as a copy). Back with a token to a workgroup, 2 of its rows at a time,
+// 121 (512 columns, 16384 tokens: 127, here 59); with 2, 4, 8 pieces of a row at
+// once 117, 118, 151: their registers leave fewer waves. Few tokens of long
+// rows are slower this way (8 of 2 choices, 16384 columns: 16.5 us, 13.6).
 
-constexpr int kRows = 4, kRowsBack = 2;
+constexpr int kRows = 4;
 
 // A wave has 512 columns of one token and adds the choices in order.
 template <class T>
@@ -565,51 +567,33 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a, int slabs) 
   store8_once((T*)a.Y + token * a.ldy + col, valid, y);
 }
 
-// A workgroup has one token.
+// A wave has one choice of a token, and so a row of Z and dZ: nothing is shared
+// between waves, and nothing waits for another row's sum.
 template <class T>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs a) {
-  __shared__ float dots[4][kRowsBack];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t token = blockIdx.x;
-  const int* place = a.place + token * a.choices;
-  const float* weights = a.weights + token * a.choices;
-  const T* dy = (const T*)a.dY + token * a.lddy;
-  for (int j0 = 0; j0 < a.choices; j0 += kRowsBack) {
-    float dot[kRowsBack] = {};
-    for (int col = 8 * threadIdx.x; col < a.cols; col += 2048) {
-      const int valid = a.cols - col;
-      float g[8], z[kRowsBack][8];
+  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t token = item / a.choices;
+  if (token >= a.tokens) return;
+  const int lane = threadIdx.x % 64, row = a.place[item];
+  float dot = 0.0f;
+  if ((unsigned)row < (unsigned)a.rows) {
+    const float w = a.weights[item];
+    const T* dy = (const T*)a.dY + token * a.lddy;
+    const T* from = (const T*)a.Z + (int64_t)row * a.ldz;
+    T* to = (T*)a.dZ + (int64_t)row * a.lddz;
+    for (uint32_t col = 8 * lane; col < (uint32_t)a.cols; col += 512) {
+      const int valid = (int)((uint32_t)a.cols - col);
+      float g[8], z[8], d[8];
       load8(dy + col, valid, g);
+      load8_once(from + col, valid, z);
 #pragma unroll
-      for (int j = 0; j < kRowsBack; ++j) {
-        const int row = j0 + j < a.choices ? place[j0 + j] : -1;
-        const bool there = (unsigned)row < (unsigned)a.rows;
-        load8_once((const T*)a.Z + (int64_t)(there ? row : 0) * a.ldz + col, there ? valid : 0, z[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kRowsBack; ++j) {
-        const int row = j0 + j < a.choices ? place[j0 + j] : -1;
-        if ((unsigned)row >= (unsigned)a.rows) continue;
-        const float w = weights[j0 + j];
-        float d[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(g[i], z[j][i], dot[j]), d[i] = g[i] * w;
-        store8_once((T*)a.dZ + (int64_t)row * a.lddz + col, valid, d);
-      }
+      for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g[i], z[i], dot), d[i] = g[i] * w;
+      store8_once(to + col, valid, d);
     }
-#pragma unroll
-    for (int j = 0; j < kRowsBack; ++j)
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) dot[j] += __shfl_xor(dot[j], d, 64);
-    if (lane == 0)
-#pragma unroll
-      for (int j = 0; j < kRowsBack; ++j) dots[wave][j] = dot[j];
-    __syncthreads();
-    const int j = threadIdx.x;
-    if (j < kRowsBack && j0 + j < a.choices)
-      a.dweights[token * a.choices + j0 + j] = (dots[0][j] + dots[1][j]) + (dots[2][j] + dots[3][j]);
-    __syncthreads();
   }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d, 64);
+  if (lane == 0) a.dweights[item] = dot;
 }
 
 // f(V) for the least V of 1, 2, 4, 8, 16 with 64 V >= experts.
@@ -671,8 +655,9 @@ hipError_t launch_combine(int type, const CombineArgs& c, hipStream_t s) {
 }
 
 hipError_t launch_combine_backward(int type, const CombineArgs& c, hipStream_t s) {
+  const int64_t items = (int64_t)c.tokens * c.choices;
   return by_type(type, [&](auto t) {
-    return launch_with((const void*)&combine_backward_kernel<decltype(t)>, dim3((unsigned)c.tokens), dim3(256), c, s);
+    return launch_with((const void*)&combine_backward_kernel<decltype(t)>, dim3((unsigned)((items + 3) / 4)), dim3(256), c, s);
   });
 }
 

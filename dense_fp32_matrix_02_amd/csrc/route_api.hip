@@ -133,7 +133,7 @@ int sgemm_mi355_route_combine_backward(int type, int tokens, int choices, int ro
   if (v != SGEMM_MI355_OK) return v;
   if (lddy < at_least_1(cols) || ldz < at_least_1(cols) || lddz < at_least_1(cols)) return SGEMM_MI355_ERR_LD;
   if (tokens == 0 || choices == 0) return SGEMM_MI355_OK;
-  if (!launchable(tokens, 256)) return SGEMM_MI355_ERR_EXTENT;
+  if (!launchable(((int64_t)tokens * choices + 3) / 4, 256)) return SGEMM_MI355_ERR_EXTENT;
   Matrices m;
   m.dense(dY, tokens, cols, lddy, element_size(type), false);
   m.dense(Z, rows, cols, ldz, element_size(type), false);
