@@ -18,6 +18,7 @@ from ._binding import _ld as _any_ld
 
 ERR_TYPE, ERR_ROUTE = -13, -14
 F32, BF16, F16 = 0, 1, 2
+FP8_DENSE, FP8_EXPERTS, FP8_WGRAD = 0, 1, 2
 
 _P, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 _SCALES = [_P, _LL, _LL]
@@ -49,6 +50,15 @@ def _bind(name, argtypes, restype=_I):
 
 for _name, _types in _SIGNATURES.items():
     globals()[_name] = _bind(_name, _types)
+
+
+_kernel_name = _bind("sgemm_mi355_fp8_kernel_name", [_I] * 6 + [_P, _I, _P, _I, _LL], ctypes.c_char_p)
+
+
+def sgemm_mi355_fp8_kernel_name(form, type, M, N, K, experts, A, lda, B, ldb, strideB=0) -> str | None:
+    """Name of the kernel that a product with these arguments runs, or None."""
+    r = _kernel_name(form, type, M, N, K, experts, A, lda, B, ldb, strideB)
+    return r.decode() if r is not None else None
 
 
 class _Library:

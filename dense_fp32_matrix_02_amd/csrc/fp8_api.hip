@@ -152,4 +152,14 @@ int sgemm_mi355_fp8_gemm_experts_wgrad(int type, int rows, int M, int N, int exp
   return done(launch_fp8_gemm(FP8_WGRAD, g, stream));
 }
 
+const char* sgemm_mi355_fp8_kernel_name(int form, int type, int M, int N, int K, int experts, const unsigned char* A,
+                                        int lda, const unsigned char* B, int ldb, long long strideB) {
+  if (form < FP8_DENSE || form > FP8_WGRAD || !known_type(type) || M < 1 || N < 1 || K < 0) return nullptr;
+  if ((form != FP8_DENSE && experts < 1) || lda < 1 || ldb < 1 || strideB < 0) return nullptr;
+  Fp8Args g{};
+  g.type = type, g.M = M, g.N = N, g.K = K, g.experts = experts, g.A = A, g.lda = lda, g.B = B, g.ldb = ldb;
+  if (form == FP8_EXPERTS) g.strideB = strideB;
+  return fp8_kernel_name((Fp8Form)form, g);
+}
+
 }  // extern "C"

@@ -61,6 +61,8 @@ const void* fp8_tile_kernel_for(Fp8Form form, bool wide, bool tall, int bm);
 const void* fp8_skinny_kernel_for(Fp8Form form, bool wide, bool tall, int bm);
 // Whether the grids launch_fp8_gemm would use for g fit a launch.
 bool fp8_launchable(Fp8Form form, const Fp8Args& g);
+// The name of the kernel that launch_fp8_gemm would run for g.
+const char* fp8_kernel_name(Fp8Form form, const Fp8Args& g);
 
 // Beginning and end of expert e's rows: offsets limited to 0 .. rows, an end
 // before the beginning gives no rows, and the first expert begins at 0.

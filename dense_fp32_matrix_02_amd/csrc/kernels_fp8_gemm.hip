@@ -191,6 +191,16 @@ bool fp8_launchable(Fp8Form form, const Fp8Args& g) {
   return grid_tiles(form, g, c.bm, c.bn) * c.threads <= (int64_t)UINT32_MAX && (form != FP8_WGRAD || g.experts <= kMaxGridY);
 }
 
+const char* fp8_kernel_name(Fp8Form form, const Fp8Args& g) {
+  const Choice c = choose(form, g);
+  if (c.kernel == Choice::STAGED) return "staged_128x128_bf16";
+  if (c.kernel == Choice::TILE)
+    return c.bm == 256 ? "tile_256x256_fp8" : c.bm == 192 ? "tile_192x128_bf16" : c.wide ? "tile_128x128_bf16" : "tile_128x128_fp8";
+  if (c.bm == 64) return c.wide ? "rows_64_bf16" : "rows_64_fp8";
+  if (c.bm == 32) return c.wide ? "rows_32_bf16" : "rows_32_fp8";
+  return c.wide ? "rows_16_bf16" : "rows_16_fp8";
+}
+
 hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s) {
   const Choice c = choose(form, g);
   const dim3 grid((unsigned)grid_tiles(form, g, c.bm, c.bn), form == FP8_WGRAD ? (unsigned)g.experts : 1u);

@@ -125,6 +125,21 @@ int sgemm_mi355_fp8_gemm_experts_wgrad(int type, int rows, int M, int N, int exp
                                        const unsigned char *B, int ldb, const float *SB, long long sb_row, long long sb_block,
                                        const int *offsets, float beta, void *C, int ldc, long long strideC, hipStream_t stream);
 
+/*
+ * Name of the kernel that a product with these arguments runs (host only; the
+ * pointers are inspected, never read): staged_*, rows_* or tile_*, then its
+ * tile of C (rows_*: the rows of A in it), then the matrix instructions that
+ * form a block's sum, fp8 or bf16. form: one of the three below; the sizes are
+ * those of the call (weight gradients: K is `rows`), experts and strideB count
+ * where the form has them. Null where nothing would be launched.
+ */
+#define SGEMM_MI355_FP8_DENSE 0   /* sgemm_mi355_fp8_gemm */
+#define SGEMM_MI355_FP8_EXPERTS 1 /* sgemm_mi355_fp8_gemm_experts */
+#define SGEMM_MI355_FP8_WGRAD 2   /* sgemm_mi355_fp8_gemm_experts_wgrad */
+const char *sgemm_mi355_fp8_kernel_name(int form, int type, int M, int N, int K, int experts,
+                                        const unsigned char *A, int lda,
+                                        const unsigned char *B, int ldb, long long strideB);
+
 #ifdef __cplusplus
 }
 #endif
