@@ -18,6 +18,7 @@ from ._binding import _ld as _any_ld
 
 ERR_TYPE, ERR_ROUTE = -13, -14
 F32, BF16, F16 = 0, 1, 2
+FP32_SUMS = 0x100  # added to a product's type
 FP8_DENSE, FP8_EXPERTS, FP8_WGRAD = 0, 1, 2
 
 _P, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
@@ -239,6 +240,10 @@ def _operand(Q, S, name, rows, cols, either=False):
     return Q.data_ptr(), max(ld, 1), S.data_ptr(), by_row, by_block, 1 if per == rows else 128
 
 
+def _type_and_sums(C, fp32_sums):
+    return _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
+
+
 def _result(C, shape, dtype, device, beta, stream):
     if C is None:
         if beta != 0.0:
@@ -249,13 +254,14 @@ def _result(C, shape, dtype, device, beta, stream):
     return _gpu(C, "C")
 
 
-def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, stream=None):
+def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, fp32_sums: bool = False, stream=None):
     """C = A.B^T + beta*C for quantised A (M x K) and B (N x K).
 
     SA has a scale for each block of a row of A (M x K/128), SB for each block
     of a row of B (N x K/128) or for each 128 x 128 tile (N/128 x K/128), as
     the quantisers give them. C is allocated with ``dtype`` (bfloat16 unless
-    given) when omitted.
+    given) when omitted. ``fp32_sums``: the sums over a block's products are
+    FP32 into a 16-bit C too, at up to twice the time (see the C header).
     """
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
@@ -265,17 +271,18 @@ def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, stream=None
     a = _operand(A, SA, "A", M, K)
     b = _operand(B, SB, "B", N, K, either=True)
     C = _result(C, (M, N), dtype or torch.bfloat16, A.device, beta, stream)
-    _check(_c.fp8_gemm(_type_of(C.dtype, "C"), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)),
+    _check(_c.fp8_gemm(_type_and_sums(C, fp32_sums), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)),
            "fp8_gemm")
     return C
 
 
-def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, stream=None):
+def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, fp32_sums: bool = False, stream=None):
     """C[r] = A[r].B[e]^T for expert e's rows r, offsets[e] <= r < offsets[e + 1].
 
     A (R x K) holds the rows sorted by expert, B is experts x N x K with scales
     for its rows (experts x N x K/128) or tiles (experts x N/128 x K/128).
-    Rows from offsets[-1] on are set to zero.
+    Rows from offsets[-1] on are set to zero. ``dtype`` and ``fp32_sums`` as in
+    gemm_fp8.
     """
     if A.dim() != 2 or B.dim() != 3 or SB.dim() != 3 or SB.shape[0] != B.shape[0] or B.shape[0] < 1:
         raise ValueError("A must be 2-D, B and its scales 3-D with the experts first")
@@ -286,17 +293,18 @@ def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, stream=None):
     a = _operand(A, SA, "A", R, K)
     b = _operand(B, SB, "B", N, K, either=True)
     C = _result(C, (R, N), dtype or torch.bfloat16, A.device, 0.0, stream)
-    _check(_c.fp8_gemm_experts(_type_of(C.dtype, "C"), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5], off,
-                               C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)), "fp8_gemm_experts")
+    _check(_c.fp8_gemm_experts(_type_and_sums(C, fp32_sums), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5],
+                               off, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)), "fp8_gemm_experts")
     return C
 
 
-def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, dtype=None, stream=None):
+def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, dtype=None, fp32_sums: bool = False,
+                           stream=None):
     """C[e] = sum over expert e's rows r of A[:, r].B[:, r]^T + beta*C[e].
 
     A (M x P) and B (N x P) as quantize_fp8_cols makes them with these
     ``offsets``; C is experts x M x N, allocated with ``dtype`` (float32 unless
-    given) when omitted.
+    given) when omitted; ``fp32_sums`` as in gemm_fp8.
     """
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
@@ -316,6 +324,6 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
     if C.dim() != 3:
         raise ValueError("C must be experts x M x N")
     ldc = _ld(C[0], "C")
-    _check(_c.fp8_gemm_experts_wgrad(_type_of(C.dtype, "C"), rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
+    _check(_c.fp8_gemm_experts_wgrad(_type_and_sums(C, fp32_sums), rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
                                      C.stride(0), _stream_of(A, stream)), "fp8_gemm_experts_wgrad")
     return C

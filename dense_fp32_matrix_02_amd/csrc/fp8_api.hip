@@ -45,6 +45,10 @@ QuantArgs args_of(const Quantize& q, const int* offsets, int experts) {
   return QuantArgs{q.X, q.ldx, q.rows, q.cols, q.index, q.n, offsets, experts, q.Q, q.ldq, q.S, q.s_row, q.s_block};
 }
 
+// The type of C, and whether block sums have to be FP32, of a product's `type` argument.
+int type_of_c(int type) { return type & ~SGEMM_MI355_FP32_SUMS; }
+bool fp32_sums(int type) { return type_of_c(type) == SGEMM_MI355_F32 || (type & SGEMM_MI355_FP32_SUMS) != 0; }
+
 int check_product(const Fp8Args& g, Fp8Form form, int64_t p, int64_t groups) {
   if (!known_type(g.type)) return SGEMM_MI355_ERR_TYPE;
   if (g.sb_rows != 1 && g.sb_rows != 128) return SGEMM_MI355_ERR_OP;
@@ -117,8 +121,8 @@ int sgemm_mi355_fp8_gemm(int type, int M, int N, int K, const unsigned char* A, 
                          long long sa_row, long long sa_block, const unsigned char* B, int ldb, const float* SB,
                          long long sb_row, long long sb_block, int sb_rows, float beta, void* C, int ldc,
                          hipStream_t stream) {
-  const Fp8Args g{type, M, N, K, A, lda, SA, sa_row, sa_block, B, ldb, 0, SB, sb_row, sb_block, 0, sb_rows,
-                  nullptr, 0, beta, C, ldc, 0};
+  const Fp8Args g{type_of_c(type), M, N, K, A, lda, SA, sa_row, sa_block, B, ldb, 0, SB, sb_row, sb_block, 0, sb_rows,
+                  nullptr, 0, beta, C, ldc, 0, fp32_sums(type)};
   const int v = check_product(g, FP8_DENSE, K, 1);
   if (v != SGEMM_MI355_OK || M == 0 || N == 0) return v;
   if (!fp8_launchable(FP8_DENSE, g)) return SGEMM_MI355_ERR_EXTENT;
@@ -130,8 +134,8 @@ int sgemm_mi355_fp8_gemm_experts(int type, int rows, int N, int K, int experts, 
                                  int ldb, long long strideB, const float* SB, long long sb_row, long long sb_block,
                                  long long stride_sb, int sb_rows, const int* offsets, void* C, int ldc,
                                  hipStream_t stream) {
-  const Fp8Args g{type, rows, N, K, A, lda, SA, sa_row, sa_block, B, ldb, strideB, SB, sb_row, sb_block, stride_sb,
-                  sb_rows, offsets, experts, 0.0f, C, ldc, 0};
+  const Fp8Args g{type_of_c(type), rows, N, K, A, lda, SA, sa_row, sa_block, B, ldb, strideB, SB, sb_row, sb_block,
+                  stride_sb, sb_rows, offsets, experts, 0.0f, C, ldc, 0, fp32_sums(type)};
   const int v = check_product(g, FP8_EXPERTS, K, experts);
   if (v != SGEMM_MI355_OK || rows == 0 || N == 0) return v;
   if (!fp8_launchable(FP8_EXPERTS, g)) return SGEMM_MI355_ERR_EXTENT;
@@ -143,8 +147,8 @@ int sgemm_mi355_fp8_gemm_experts_wgrad(int type, int rows, int M, int N, int exp
                                        const unsigned char* B, int ldb, const float* SB, long long sb_row,
                                        long long sb_block, const int* offsets, float beta, void* C, int ldc,
                                        long long strideC, hipStream_t stream) {
-  const Fp8Args g{type, M, N, rows, A, lda, SA, sa_row, sa_block, B, ldb, 0, SB, sb_row, sb_block, 0, 1,
-                  offsets, experts, beta, C, ldc, strideC};
+  const Fp8Args g{type_of_c(type), M, N, rows, A, lda, SA, sa_row, sa_block, B, ldb, 0, SB, sb_row, sb_block, 0, 1,
+                  offsets, experts, beta, C, ldc, strideC, fp32_sums(type)};
   const int64_t p = rows < 0 || experts < 0 ? 0 : 128 * ((int64_t)rows / 128 + experts);
   const int v = check_product(g, FP8_WGRAD, p, experts);
   if (v != SGEMM_MI355_OK || M == 0 || N == 0) return v;
@@ -154,10 +158,11 @@ int sgemm_mi355_fp8_gemm_experts_wgrad(int type, int rows, int M, int N, int exp
 
 const char* sgemm_mi355_fp8_kernel_name(int form, int type, int M, int N, int K, int experts, const unsigned char* A,
                                         int lda, const unsigned char* B, int ldb, long long strideB) {
-  if (form < FP8_DENSE || form > FP8_WGRAD || !known_type(type) || M < 1 || N < 1 || K < 0) return nullptr;
+  if (form < FP8_DENSE || form > FP8_WGRAD || !known_type(type_of_c(type)) || M < 1 || N < 1 || K < 0) return nullptr;
   if ((form != FP8_DENSE && experts < 1) || lda < 1 || ldb < 1 || strideB < 0) return nullptr;
   Fp8Args g{};
-  g.type = type, g.M = M, g.N = N, g.K = K, g.experts = experts, g.A = A, g.lda = lda, g.B = B, g.ldb = ldb;
+  g.type = type_of_c(type), g.wide = fp32_sums(type), g.M = M, g.N = N, g.K = K, g.experts = experts;
+  g.A = A, g.lda = lda, g.B = B, g.ldb = ldb;
   if (form == FP8_EXPERTS) g.strideB = strideB;
   return fp8_kernel_name((Fp8Form)form, g);
 }

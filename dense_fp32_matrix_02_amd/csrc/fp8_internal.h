@@ -52,13 +52,14 @@ struct Fp8Args {
   float beta;
   void* C;
   int64_t ldc, strideC;
+  bool wide;  // block sums have to be FP32 sums: C is FP32, or the caller asks for it
 };
 
 hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s);
 // Kernels for aligned operands (kernels_fp8_tile.hip, kernels_fp8_skinny.hip). wide: the values are widened to bf16.
 // tall: B has a scale for each 128 rows; bm: rows of A in a workgroup's tile.
 const void* fp8_tile_kernel_for(Fp8Form form, bool wide, bool tall, int bm);
-const void* fp8_skinny_kernel_for(Fp8Form form, bool wide, bool tall, int bm);
+const void* fp8_skinny_kernel_for(Fp8Form form, bool tall, int bm);
 // Whether the grids launch_fp8_gemm would use for g fit a launch.
 bool fp8_launchable(Fp8Form form, const Fp8Args& g);
 // The name of the kernel that launch_fp8_gemm would run for g.

@@ -16,9 +16,11 @@ constexpr int kSkinnyWaves = 8;
 // are added in wave order through LDS. Bound by B's bytes as long as enough
 // workgroups share a CU: the loads of one then fill the pauses of another (its
 // start, its sums' way through LDS). 16 tokens of 4 of 32 experts, N 2048, K
-// 4096: 42 us (5.5 TB/s) with six waves a SIMD and two blocks of each in
-// flight, 51 with four and four.
-template <int FORM, bool WIDE, bool TALL, int MF>
+// 4096: 45 us (5.2 TB/s) with six waves a SIMD and two blocks of each in
+// flight, 51 with four and four. Values are widened whatever C's type: the
+// matrix unit waits for memory here, and FP32 block sums cost 45.3 us against
+// 44.0 with the FP8 unit's (8 x 4096 x 4096: 5.4 and 5.2; 64 rows: 12.7 and 11.9).
+template <int FORM, bool TALL, int MF>
 __global__ void __launch_bounds__(64 * kSkinnyWaves, MF == 4 ? 2 : MF == 1 ? 6 : 4) fp8_skinny_kernel(Fp8Args g) {
   constexpr int BM = 16 * MF, BN = 16, NW = kSkinnyWaves;
   constexpr int AHEAD = 2;  // blocks that a wave has in flight
@@ -65,7 +67,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves, MF == 4 ? 2 : MF == 1 ? 6 :
     }
   };
   auto multiply = [&](const Held& h) __attribute__((always_inline)) {
-    Frag<WIDE> fb, fa;
+    Frag<true> fb, fa;
     fb.set(h.b[0], h.b[1]);
     f32x4 rows_sb;  // of the four rows of B that a lane has results of
 #pragma unroll
@@ -111,21 +113,17 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves, MF == 4 ? 2 : MF == 1 ? 6 :
   }
 }
 
-template <bool WIDE, int MF>
+template <int MF>
 const void* of_width(Fp8Form form, bool tall) {
   if (form == FP8_EXPERTS)
-    return tall ? (const void*)&fp8_skinny_kernel<FP8_EXPERTS, WIDE, true, MF>
-                : (const void*)&fp8_skinny_kernel<FP8_EXPERTS, WIDE, false, MF>;
-  return tall ? (const void*)&fp8_skinny_kernel<FP8_DENSE, WIDE, true, MF>
-              : (const void*)&fp8_skinny_kernel<FP8_DENSE, WIDE, false, MF>;
+    return tall ? (const void*)&fp8_skinny_kernel<FP8_EXPERTS, true, MF> : (const void*)&fp8_skinny_kernel<FP8_EXPERTS, false, MF>;
+  return tall ? (const void*)&fp8_skinny_kernel<FP8_DENSE, true, MF> : (const void*)&fp8_skinny_kernel<FP8_DENSE, false, MF>;
 }
 
 }  // namespace
 
-const void* fp8_skinny_kernel_for(Fp8Form form, bool wide, bool tall, int bm) {
-  if (bm == 16) return wide ? of_width<true, 1>(form, tall) : of_width<false, 1>(form, tall);
-  if (bm == 32) return wide ? of_width<true, 2>(form, tall) : of_width<false, 2>(form, tall);
-  return wide ? of_width<true, 4>(form, tall) : of_width<false, 4>(form, tall);
+const void* fp8_skinny_kernel_for(Fp8Form form, bool tall, int bm) {
+  return bm == 16 ? of_width<1>(form, tall) : bm == 32 ? of_width<2>(form, tall) : of_width<4>(form, tall);
 }
 
 }  // namespace sgemm_impl

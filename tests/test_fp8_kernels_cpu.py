@@ -23,7 +23,7 @@ def built_library():
 GOOD = dict(form=0, type=1, M=4096, N=4096, K=4096, experts=0, A=X, lda=4096, B=X, ldb=4096, strideB=0)
 
 
-@pytest.mark.parametrize("bad", [dict(form=3), dict(form=-1), dict(type=3), dict(M=0), dict(N=0), dict(K=-1), dict(form=1),
+@pytest.mark.parametrize("bad", [dict(form=3), dict(form=-1), dict(type=3), dict(type=3 | sg.FP32_SUMS), dict(M=0), dict(N=0), dict(K=-1), dict(form=1),
                                  dict(form=2, experts=0), dict(lda=0), dict(ldb=0), dict(form=1, experts=4, strideB=-16)])
 def test_no_name_where_nothing_runs(bad):
     assert sg.sgemm_mi355_fp8_kernel_name(**GOOD) == "tile_256x256_fp8"
@@ -31,9 +31,10 @@ def test_no_name_where_nothing_runs(bad):
 
 
 @pytest.mark.parametrize("change,name", [
-    (dict(M=8), "rows_16_fp8"), (dict(M=8, type=0), "rows_16_bf16"), (dict(type=0), "tile_128x128_bf16"),
+    (dict(M=8), "rows_16_bf16"), (dict(M=8, type=0), "rows_16_bf16"), (dict(type=0), "tile_128x128_bf16"),
     (dict(A=X + 1), "staged_128x128_bf16"), (dict(ldb=4097), "staged_128x128_bf16"), (dict(K=15), "staged_128x128_bf16"),
-    (dict(form=1, experts=4, strideB=8), "staged_128x128_bf16"), (dict(strideB=8), "tile_256x256_fp8")])
+    (dict(form=1, experts=4, strideB=8), "staged_128x128_bf16"), (dict(strideB=8), "tile_256x256_fp8"),
+    (dict(type=1 | sg.FP32_SUMS), "tile_128x128_bf16"), (dict(type=0 | sg.FP32_SUMS), "tile_128x128_bf16")])
 def test_names(change, name):
     assert sg.sgemm_mi355_fp8_kernel_name(**dict(GOOD, **change)) == name
 

@@ -60,7 +60,7 @@ DENSE = [  # kernel, kind, M, N, K
     ("tile_128x128_bf16", "fp32", 1300, 2100, 260), ("tile_128x128_bf16", "fp32", 700, 3001, 640),
     ("tile_128x128_bf16", "fp32", 257, 8200, 900), ("tile_192x128_bf16", "fp32", 2100, 2200, 400),
     ("rows_64_bf16", "fp32", 450, 1030, 2000), ("rows_64_bf16", "fp32", 400, 2050, 1000),
-    ("rows_64_fp8", "bf16", 520, 640, 3990), ("rows_32_fp8", "fp16", 300, 300, 8100),
+    ("rows_64_bf16", "bf16", 520, 640, 3990), ("rows_32_bf16", "fp16", 300, 300, 8100),
     ("staged_128x128_bf16", "bf16", 300, 260, 10), ("staged_128x128_bf16", "fp16", 129, 257, 15)]
 
 
@@ -122,7 +122,7 @@ EXPERTS = [  # kernel, kind, rows, N, K, experts
     ("tile_256x256_fp8", "bf16", 5000, 2050, 1000, 4), ("tile_128x128_fp8", "fp16", 1500, 1000, 400, 4),
     ("tile_128x128_fp8", "bf16", 900, 2050, 260, 3), ("tile_128x128_fp8", "bf16", 2000, 500, 384, 5),
     ("tile_128x128_bf16", "fp32", 1500, 1000, 400, 4), ("tile_128x128_bf16", "fp32", 5000, 1030, 512, 3),
-    ("rows_64_fp8", "fp16", 600, 1030, 600, 2), ("rows_64_bf16", "fp32", 600, 1030, 600, 2)]
+    ("rows_64_bf16", "fp16", 600, 1030, 600, 2), ("rows_64_bf16", "fp32", 600, 1030, 600, 2)]
 
 
 @pytest.mark.parametrize("tall", [1, 128])
@@ -237,3 +237,61 @@ def test_tiles_captured_and_replayed():
         torch.cuda.synchronize()
         for g, w in zip(got, work()):
             assert torch.equal(g, w)
+
+
+def cancelling(K, seed):
+    """(a, b): whose products are 2^16, -2^16 and six of 4 in every eight, in random places; their sum is 3 K."""
+    g = torch.Generator().manual_seed(seed)
+    b = torch.full((K // 8, 8), 2.0)
+    at = torch.rand(K // 8, 8, generator=g).argsort(-1)
+    b.scatter_(1, at[:, :2], 256.0)
+    a = b.clone().scatter_(1, at[:, :1], -256.0)
+    return a.flatten(), b.flatten()
+
+
+def stored(x):
+    return x.to(torch.float8_e4m3fn).to("cuda")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,K,asked", [
+    (1, 100, 640, False), (8, 1000, 1040, False), (30, 700, 640, False), (64, 1100, 512, False), (450, 1030, 640, True),
+    (1100, 2050, 400, True), (2304, 2560, 384, True)])
+def test_sums_into_16_bits_are_fp32(kind, M, N, K, asked):
+    """Products of 2^16 that cancel leave the small ones whole: partial sums are whole numbers below 2^24, which FP32
+    holds in any order. Few rows keep them always, larger products where the caller asks."""
+    print(f"[gpu] cancelling products {M}x{N}x{K} {kind}", flush=True)
+    a, b = cancelling(K, 1)
+    g = torch.Generator().manual_seed(2)
+    sign = torch.randint(0, 2, (M, 1), generator=g) * 2.0 - 1.0
+    A, B = stored(sign * a), stored(b.repeat(N, 1))
+    sb = torch.exp2(torch.randint(-3, 4, (N, 1), generator=g).float())
+    name = sg.sgemm_mi355_fp8_kernel_name(sg.FP8_DENSE, CODE[kind] | (sg.FP32_SUMS if asked else 0), M, N, K, 0,
+                                          A.data_ptr(), K, B.data_ptr(), K)
+    assert name.endswith("bf16")
+    C = sg.gemm_fp8(A, torch.ones(M, -(-K // 128), device="cuda"), B, sb.to("cuda").expand(N, -(-K // 128)),
+                    dtype=R.TYPES[kind], fp32_sums=asked)
+    assert torch.equal(C.cpu(), (sign * sb.t() * 3 * K).to(R.TYPES[kind]))
+
+
+def test_experts_sums_are_fp32_where_asked():
+    rows, N, K, E = 3000, 1030, 640, 3
+    offsets = torch.tensor([0, 1500, 1501, 2990], dtype=torch.int32, device="cuda")
+    a, b = cancelling(K, 1)
+    factor = torch.tensor([1.0, 0.25, 4.0])
+    got = sg.gemm_fp8_experts(stored(a.repeat(rows, 1)), torch.ones(rows, 5, device="cuda"), stored(b.repeat(E, N, 1)),
+                              factor.to("cuda").view(E, 1, 1).expand(E, N, 5), offsets, fp32_sums=True)
+    want = torch.zeros(rows, N)
+    for e, (at, to) in enumerate([(0, 1500), (1500, 1501), (1501, 2990)]):
+        want[at:to] = 3 * K * factor[e]
+    assert torch.equal(got.cpu(), want.bfloat16())
+    # as the summed axis: 128 rows of one expert in the first block, 512 of the other in blocks 2 to 5
+    offsets = torch.tensor([0, 128, 640], dtype=torch.int32, device="cuda")
+    (a, b), used = cancelling(128 * 7, 3), torch.ones(7, 128)
+    used[1], used[6] = 0.0, 0.0
+    a, b = (x.view(7, 128) * used for x in (a, b))
+    got = sg.gemm_fp8_experts_wgrad(stored(a.flatten().repeat(300, 1)), torch.ones(300, 7, device="cuda"),
+                                    stored(b.flatten().repeat(500, 1)), torch.ones(500, 7, device="cuda"), offsets,
+                                    dtype=torch.float16, fp32_sums=True)
+    want = torch.stack([torch.full((300, 500), 3.0 * n) for n in (128, 512)]).to(torch.float16)
+    assert torch.equal(got.cpu(), want)
