@@ -96,8 +96,11 @@ struct PlanArgs {
   const int* ids;
   int *offsets, *row_token, *place;
   int* counts;  // workspace: entries of each expert in each run of kPlanRun entries
+  int runs;     // 1 for no entries: the offsets are written all the same
 };
 constexpr int kPlanRun = 2048;
+// Of up to 2^31 - 1 entries, whose number rounded up to whole runs needs 64 bits.
+inline int plan_runs(int64_t entries) { return entries > kPlanRun ? (int)((entries + kPlanRun - 1) / kPlanRun) : 1; }
 hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s);
 
 struct CombineArgs {

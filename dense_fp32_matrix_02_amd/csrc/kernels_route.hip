@@ -429,7 +429,7 @@ __device__ __forceinline__ uint64_t same_key(int key, bool active, int bits) {
   return same;
 }
 
-__global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) {
+__global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p) {
   constexpr int WAVES = 16, PER = kPlanRun / WAVES / 64;  // entries per lane
   // next[w][e]: first the wave's entries of expert e, then the row of its next one.
   __shared__ int next[WAVES * (SGEMM_MI355_MAX_EXPERTS + 1)];
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) 
   for (int i = 0; i < PER; ++i)
     if (expert[i] >= 0) atomicAdd(&next[wave * width + expert[i]], 1);
   __syncthreads();
-  if (runs > 1) {
+  if (p.runs > 1) {
     // Of each expert, the entries in all runs and those in the runs before this
     // one: the threads share the runs, and add up their parts in LDS (65536
     // tokens of 8 choices: 18 us, 42 with a thread for each expert).
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) 
       const int part = i / width, e = i - part * width;
       int here = 0, all = 0;
 #pragma unroll 8
-      for (int r = part; r < runs; r += parts) {
+      for (int r = part; r < p.runs; r += parts) {
         const int c = p.counts[(int64_t)r * width + e];
         all += c;
         if (r < (int)blockIdx.x) here += c;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p, int runs) 
     const int e = e0 + t;
     int here = 0, all = 0;
     if (e < width) {
-      if (runs == 1) {
+      if (p.runs == 1) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) all += next[w * width + e];
       } else {
@@ -633,15 +633,11 @@ hipError_t launch_route_backward(int type, int score, const RouteArgs& r, hipStr
 }
 
 hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s) {
-  int runs = (p.entries + kPlanRun - 1) / kPlanRun;
-  if (runs < 1) runs = 1;  // offsets are written all the same
-  if (runs > 1) {
-    const hipError_t err = launch_with((const void*)&plan_count_kernel, dim3((unsigned)runs), dim3(1024), p, s);
+  if (p.runs > 1) {
+    const hipError_t err = launch_with((const void*)&plan_count_kernel, dim3((unsigned)p.runs), dim3(1024), p, s);
     if (err != hipSuccess) return err;
   }
-  PlanArgs copy = p;
-  void* args[] = {&copy, &runs};
-  return hipLaunchKernel((const void*)&plan_place_kernel, dim3((unsigned)runs), dim3(1024), args, 0, s);
+  return launch_with((const void*)&plan_place_kernel, dim3((unsigned)p.runs), dim3(1024), p, s);
 }
 
 hipError_t launch_combine(int type, const CombineArgs& c, hipStream_t s) {

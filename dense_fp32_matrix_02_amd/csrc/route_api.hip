@@ -18,11 +18,6 @@ int check_route(int type, int tokens, int experts, int ld, int score, int choice
   return SGEMM_MI355_OK;
 }
 
-int plan_runs(int64_t entries) {
-  const int64_t runs = (entries + kPlanRun - 1) / kPlanRun;
-  return (int)(runs > 1 ? runs : 1);
-}
-
 int check_combine(int type, int tokens, int choices, int rows, int cols) {
   if (!known_type(type)) return SGEMM_MI355_ERR_TYPE;
   if (tokens < 0 || choices < 0 || rows < 0 || cols < 0) return SGEMM_MI355_ERR_DIM;
@@ -82,7 +77,9 @@ int sgemm_mi355_route_backward(int type, int tokens, int experts, const void* lo
 
 size_t sgemm_mi355_route_plan_workspace_size(int tokens, int choices, int experts) {
   if (tokens < 0 || choices < 0 || experts < 1 || experts > SGEMM_MI355_MAX_EXPERTS) return 0;
-  const int runs = plan_runs((int64_t)tokens * choices);
+  const int64_t entries = (int64_t)tokens * choices;
+  if (entries > kMostRows) return 0;
+  const int runs = plan_runs(entries);
   return runs == 1 ? 0 : (size_t)runs * ((size_t)experts + 1) * 4;
 }
 
@@ -102,7 +99,8 @@ int sgemm_mi355_route_plan(int tokens, int choices, int experts, const int* ids,
   const int c = m.check();
   if (c != SGEMM_MI355_OK) return c;
   if (workspace_bytes < need) return SGEMM_MI355_ERR_WORKSPACE;
-  const PlanArgs p{(int)entries, choices, experts, ids, offsets, row_token, place, (int*)workspace};
+  const PlanArgs p{(int)entries, choices, experts, ids, offsets, row_token, place, (int*)workspace,
+                   plan_runs(entries)};
   return done(launch_route_plan(p, stream));
 }
 

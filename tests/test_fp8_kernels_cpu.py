@@ -46,3 +46,9 @@ def test_a_wrong_choice_of_ties_is_seen():
     planted = logits.shape[1] - 1 - R.route(logits[:, ::-1], 2)[1]
     assert right.tolist() == [[1, 2]] and planted.tolist() == [[4, 2]]
     assert (right != planted).any()
+
+
+def test_workspace_of_the_largest_plans():
+    n = 268435315 * 8
+    assert sg.sgemm_mi355_route_plan_workspace_size(268435315, 8, 3) == -(-n // 2048) * 16
+    assert sg.sgemm_mi355_route_plan_workspace_size(2 ** 31 - 1, 32, 3) == 0  # more than the call takes
