@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 
 // A wave has one token, lane k its choice k. A sigmoid's gradient needs the
 // chosen experts' scores alone; a softmax's needs the whole row.
+// 1 - s of a sigmoid comes from the exponential, not from s, which may round to 1.
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
   __shared__ double rows[4][64 * V];  // scores, then the lanes of the chosen experts' choices, then their gradients
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
   if (token >= a.tokens) return;
   const T* logits = (const T*)a.logits + (int64_t)token * a.ld;
   int id = -1;
-  double dw = 0.0, w = 0.0;
+  double dw = 0.0, w = 0.0, rest = 0.0;  // rest: 1 - w of a sigmoid
   if (lane < a.choices) {
     id = a.ids_in[(int64_t)token * a.choices + lane];
     if ((unsigned)id >= (unsigned)a.experts) id = -1;
@@ -336,13 +337,15 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     wave_sync();
     if (id >= 0) w = row[id];
   } else if (id >= 0) {
-    w = 1.0 / (1.0 + exp(-to_f64(logits[id])));
+    const double x = to_f64(logits[id]), t = exp(-fabs(x)), one = 1.0 / (1.0 + t);
+    w = x < 0.0 ? t * one : one;
+    rest = x < 0.0 ? one : t * one;
   }
   // total = S, dot = sum of dw_m s_m over the chosen
   double total = 1.0, dot = 0.0;
   if (a.renorm) total = sum_of(w), dot = sum_of(w * dw);
   double d = id < 0 || total == 0.0 ? 0.0 : (double)a.scale * (dw - dot / total) / total;
-  if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * (1.0 - w);
+  if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * rest;
   // Through LDS to the lanes that hold the experts (8192 tokens, 8 of 256: 6.1 us;
   // 8.5 with every choice compared with all experts). Experts that are chosen
   // more than once are found first, and added up in the choices' order.
