@@ -313,7 +313,11 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 
 // A wave has one token, lane k its choice k. A sigmoid's gradient needs the
 // chosen experts' scores alone; a softmax's needs the whole row.
-// 1 - s of a sigmoid comes from the exponential, not from s, which may round to 1.
+// Nothing is computed as a difference of nearly equal numbers that is small by
+// the formula: 1 - s of a sigmoid comes from the exponential, and a weighted
+// mean is taken of the differences from the value of the largest score, which
+// may be nearly the whole weight (dw_j - sum_m dw_m s_m / S with S nearly one
+// s_m, and ds_i - sum_m ds_m s_m with one s_m nearly 1).
 template <class T, int SCORE, int V>
 __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
   __shared__ double rows[4][64 * V];  // scores, then the lanes of the chosen experts' choices, then their gradients
@@ -341,9 +345,19 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     w = x < 0.0 ? t * one : one;
     rest = x < 0.0 ? one : t * one;
   }
+  double most = 0.0;  // the largest of the chosen scores, and a choice that has it
+  int first = 0;
+  if (SCORE == SGEMM_MI355_SOFTMAX || a.renorm) {
+    most = max_of(w);
+    const uint64_t lanes = __ballot(w == most);
+    if (lanes != 0) first = __builtin_ctzll(lanes);  // none: NaN
+  }
   // total = S, dot = sum of dw_m s_m over the chosen
   double total = 1.0, dot = 0.0;
-  if (a.renorm) total = sum_of(w), dot = sum_of(w * dw);
+  if (a.renorm) {
+    dw -= lane_value(dw, first);
+    total = sum_of(w), dot = sum_of(w * dw);
+  }
   double d = id < 0 || total == 0.0 ? 0.0 : (double)a.scale * (dw - dot / total) / total;
   if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * rest;
   // Through LDS to the lanes that hold the experts (8192 tokens, 8 of 256: 6.1 us;
@@ -373,6 +387,15 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
     }
   }
   if constexpr (SCORE == SGEMM_MI355_SOFTMAX) {
+    if (most > 0.5) {  // else no score is nearly 1, or one that was not chosen, whose ds is 0
+      const int e = (int)lane_value((uint32_t)id, first);
+      double base = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (e % V == v) base = lane_value(ds[v], e / V);
+#pragma unroll
+      for (int v = 0; v < V; ++v) ds[v] -= base;
+    }
     double inner = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) inner += ds[v] * s[v];
