@@ -95,12 +95,27 @@ struct PlanArgs {
   int entries, choices, experts;
   const int* ids;
   int *offsets, *row_token, *place;
-  int* counts;  // workspace: entries of each expert in each run of kPlanRun entries
-  int runs;     // 1 for no entries: the offsets are written all the same
+  int* counts;  // workspace: entries of each expert in each run, then (with groups) in each group of runs
+  int runs;     // runs of kPlanRun entries; 1 for no entries: the offsets are written all the same
+  int per;      // runs in a group; 0 where they are not grouped
+  int groups;   // groups of runs, the last one shorter
 };
 constexpr int kPlanRun = 2048;
-// Of up to 2^31 - 1 entries, whose number rounded up to whole runs needs 64 bits.
-inline int plan_runs(int64_t entries) { return entries > kPlanRun ? (int)((entries + kPlanRun - 1) / kPlanRun) : 1; }
+constexpr int kPlanGroups = 512;  // groups at most
+// The division of up to 2^31 - 1 entries, whose number rounded up to whole runs needs 64 bits.
+// Runs are grouped where every run reading the counts of all costs more than the
+// groups' kernel (us, without and with groups, 8 choices of
+//   8 experts, 512 / 1024 / 4096 runs      15.9, 20.6 / 28.8, 31.4 / 130, 87
+//   64 experts, 256 / 512 / 1024 runs      11.4, 15.1 / 20.9, 22.6 / 47.8, 35.5
+//   256 experts, 128 / 256 / 4096 runs     12.3, 14.1 / 17.2, 16.7 / 1363, 107
+//   1024 experts, 32 / 64 / 128 runs       13.3, 15.2 / 16.4, 15.8 / 22.5, 17.3).
+inline void plan_division(int64_t entries, int experts, PlanArgs& p) {
+  p.runs = entries > kPlanRun ? (int)((entries + kPlanRun - 1) / kPlanRun) : 1;
+  const int64_t numbers = (int64_t)p.runs * (experts + 1);  // that each run reads
+  const bool grouped = numbers > 1 << 16 || numbers * p.runs > 1 << 25;
+  p.per = grouped ? (p.runs + kPlanGroups - 1) / kPlanGroups : 0;
+  p.groups = grouped ? (p.runs + p.per - 1) / p.per : 0;
+}
 hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s);
 
 struct CombineArgs {

@@ -425,6 +425,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
 // having counted its own entries, knows where its first of each expert goes;
 // then the waves place theirs without waiting for each other. Ids outside the
 // experts count as expert number `experts`, the last.
+//
+// Every run reading the counts of all runs is work of their square. Where there
+// are many, the first kernel takes a group of neighbouring runs to a workgroup,
+// one after the other, and writes for each run what its group has before it; a
+// kernel between the two adds up the groups; and a run reads three numbers of
+// each expert (1048576 tokens of 8 of 256 experts: 107 us, 1363 without groups).
 
 __device__ __forceinline__ int expert_of(const PlanArgs& p, int entry) {
   const int id = p.ids[entry];
@@ -443,6 +449,65 @@ __global__ void __launch_bounds__(1024) plan_count_kernel(PlanArgs p) {
   }
   __syncthreads();
   for (int e = threadIdx.x; e <= p.experts; e += 1024) p.counts[(int64_t)blockIdx.x * (p.experts + 1) + e] = count[e];
+}
+
+// Rows of counts after those of the runs: the entries before each group, and all.
+__device__ __forceinline__ int* group_counts(const PlanArgs& p, int group) {
+  return p.counts + ((int64_t)p.runs + group) * (p.experts + 1);
+}
+
+__global__ void __launch_bounds__(1024) plan_group_kernel(PlanArgs p) {
+  constexpr int PER = kPlanRun / 1024;
+  __shared__ int count[SGEMM_MI355_MAX_EXPERTS + 1];
+  const int t = threadIdx.x, width = p.experts + 1;
+  const int from = blockIdx.x * p.per, to = min(from + p.per, p.runs);
+  for (int e = t; e < width; e += 1024) count[e] = 0;
+  int expert[PER];
+  auto load = [&](int run) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int entry = run * kPlanRun + i * 1024 + t;
+      expert[i] = entry < p.entries ? expert_of(p, entry) : -1;
+    }
+  };
+  load(from);
+  for (int run = from; run < to; ++run) {
+    __syncthreads();
+    for (int e = t; e < width; e += 1024) p.counts[(int64_t)run * width + e] = count[e];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (expert[i] >= 0) atomicAdd(&count[expert[i]], 1);
+    if (run + 1 < to) load(run + 1);
+  }
+  __syncthreads();
+  for (int e = t; e < width; e += 1024) group_counts(p, blockIdx.x)[e] = count[e];
+}
+
+// A lane has an expert and a wave 1/16 of the groups: their entries become those
+// before them.
+__global__ void __launch_bounds__(1024) plan_sum_kernel(PlanArgs p) {
+  constexpr int WAVES = 16, MOST = kPlanGroups / WAVES;
+  __shared__ int part[WAVES][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, e = blockIdx.x * 64 + lane;
+  const bool there = e <= p.experts;
+  const int each = (p.groups + WAVES - 1) / WAVES, from = wave * each;
+  int c[MOST], own = 0;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    c[i] = there && i < each && from + i < p.groups ? group_counts(p, from + i)[e] : 0;
+    own += c[i];
+  }
+  part[wave][lane] = own;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += part[w][lane];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    if (there && i < each && from + i < p.groups) group_counts(p, from + i)[e] = before;
+    before += c[i];
+  }
+  if (there && wave == WAVES - 1) group_counts(p, p.groups)[e] = before;
 }
 
 // Lanes of the wave that have the same key (of `bits` bits).
@@ -475,7 +540,15 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p) {
   for (int i = 0; i < PER; ++i)
     if (expert[i] >= 0) atomicAdd(&next[wave * width + expert[i]], 1);
   __syncthreads();
-  if (p.runs > 1) {
+  if (p.per > 0) {
+    const int* group = group_counts(p, blockIdx.x / p.per);
+    const int* all = group_counts(p, p.groups);
+    for (int e = t; e < width; e += 1024) {
+      in_all[e] = all[e];
+      in_earlier[e] = group[e] + p.counts[(int64_t)blockIdx.x * width + e];
+    }
+    __syncthreads();
+  } else if (p.runs > 1) {
     // Of each expert, the entries in all runs and those in the runs before this
     // one: the threads share the runs, and add up their parts in LDS (65536
     // tokens of 8 choices: 18 us, 42 with a thread for each expert).
@@ -659,10 +732,15 @@ hipError_t launch_route_backward(int type, int score, const RouteArgs& r, hipStr
 }
 
 hipError_t launch_route_plan(const PlanArgs& p, hipStream_t s) {
-  if (p.runs > 1) {
-    const hipError_t err = launch_with((const void*)&plan_count_kernel, dim3((unsigned)p.runs), dim3(1024), p, s);
-    if (err != hipSuccess) return err;
+  hipError_t err = hipSuccess;
+  if (p.per > 0) {
+    err = launch_with((const void*)&plan_group_kernel, dim3((unsigned)p.groups), dim3(1024), p, s);
+    if (err == hipSuccess)
+      err = launch_with((const void*)&plan_sum_kernel, dim3((unsigned)(p.experts / 64 + 1)), dim3(1024), p, s);
+  } else if (p.runs > 1) {
+    err = launch_with((const void*)&plan_count_kernel, dim3((unsigned)p.runs), dim3(1024), p, s);
   }
+  if (err != hipSuccess) return err;
   return launch_with((const void*)&plan_place_kernel, dim3((unsigned)p.runs), dim3(1024), p, s);
 }
 

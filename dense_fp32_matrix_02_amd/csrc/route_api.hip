@@ -79,8 +79,10 @@ size_t sgemm_mi355_route_plan_workspace_size(int tokens, int choices, int expert
   if (tokens < 0 || choices < 0 || experts < 1 || experts > SGEMM_MI355_MAX_EXPERTS) return 0;
   const int64_t entries = (int64_t)tokens * choices;
   if (entries > kMostRows) return 0;
-  const int runs = plan_runs(entries);
-  return runs == 1 ? 0 : (size_t)runs * ((size_t)experts + 1) * 4;
+  PlanArgs p{};
+  plan_division(entries, experts, p);
+  const size_t rows = p.runs == 1 ? 0 : (size_t)p.runs + (p.per > 0 ? p.groups + 1 : 0);
+  return rows * ((size_t)experts + 1) * 4;
 }
 
 int sgemm_mi355_route_plan(int tokens, int choices, int experts, const int* ids, int* offsets, int* row_token,
@@ -99,8 +101,8 @@ int sgemm_mi355_route_plan(int tokens, int choices, int experts, const int* ids,
   const int c = m.check();
   if (c != SGEMM_MI355_OK) return c;
   if (workspace_bytes < need) return SGEMM_MI355_ERR_WORKSPACE;
-  const PlanArgs p{(int)entries, choices, experts, ids, offsets, row_token, place, (int*)workspace,
-                   plan_runs(entries)};
+  PlanArgs p{(int)entries, choices, experts, ids, offsets, row_token, place, (int*)workspace, 0, 0, 0};
+  plan_division(entries, experts, p);
   return done(launch_route_plan(p, stream));
 }
 

@@ -49,6 +49,6 @@ def test_a_wrong_choice_of_ties_is_seen():
 
 
 def test_workspace_of_the_largest_plans():
-    n = 268435315 * 8
-    assert sg.sgemm_mi355_route_plan_workspace_size(268435315, 8, 3) == -(-n // 2048) * 16
+    runs = -(-268435315 * 8 // 2048)  # in 512 groups, and a row for all
+    assert sg.sgemm_mi355_route_plan_workspace_size(268435315, 8, 3) == (runs + 512 + 1) * 16
     assert sg.sgemm_mi355_route_plan_workspace_size(2 ** 31 - 1, 32, 3) == 0  # more than the call takes

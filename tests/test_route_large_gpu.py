@@ -46,3 +46,43 @@ def test_plan_of_nearly_2_to_the_31_entries():
             token[-1] = (n - 1) // k
         assert torch.equal(rows[at:at + step], token)
         del entry, want, token
+
+
+@pytest.mark.parametrize("tokens,k,experts", [
+    (16384, 8, 1024), (17001, 8, 1023), (65536, 8, 256), (70001, 8, 255), (262144, 8, 64), (600011, 8, 7), (200003, 1, 1000),
+    (1 << 20, 8, 256)])
+def test_plan_of_many_runs(tokens, k, experts):
+    """Runs in groups, of one run and of more, the last run and the last group shorter; some ids outside the experts."""
+    n = tokens * k
+    print(f"[gpu] plan {tokens} {k} {experts}", flush=True)
+    size = sg.sgemm_mi355_route_plan_workspace_size(tokens, k, experts)
+    assert size > 4 * -(-n // 2048) * (experts + 1)  # room for groups: they are taken
+    g = torch.Generator(device="cuda").manual_seed(n)
+    for ids in (torch.randint(0, experts, (tokens, k), generator=g, device="cuda", dtype=torch.int32),
+                torch.randint(-3, experts + 5, (tokens, k), generator=g, device="cuda", dtype=torch.int32),
+                torch.full((tokens, k), experts - 1, dtype=torch.int32, device="cuda")):
+        offsets, rows, place = sg.route_plan(ids, experts)
+        flat = torch.where((ids < 0) | (ids >= experts), experts, ids).flatten().long()
+        counts = torch.zeros(experts + 1, dtype=torch.long, device="cuda").index_add_(0, flat, torch.ones_like(flat))
+        assert torch.equal(offsets.long(), torch.cat([counts.new_zeros(1), counts.cumsum(0)[:-1]]))
+        order = (flat * n + torch.arange(n, device="cuda")).sort().indices  # by expert, then by place in ids
+        assert torch.equal(rows.long(), order // k)
+        assert torch.equal(place.flatten()[order].long(), torch.arange(n, device="cuda"))
+
+
+def test_plan_of_many_runs_captured_and_replayed():
+    ids = torch.zeros(70001, 8, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sg.route_plan(ids, 256)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = sg.route_plan(ids, 256)
+    for i in range(4):
+        ids.copy_(torch.randint(0, 256, (70001, 8), generator=torch.Generator().manual_seed(i), dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, sg.route_plan(ids, 256)):
+            assert torch.equal(a, b)
