@@ -22,6 +22,7 @@ ERR_DIM, ERR_LD, ERR_NULL, ERR_ALIAS, ERR_EXTENT, ERR_LAUNCH, ERR_CONFIG, ERR_AL
 ERR_STRIDE, ERR_OP, ERR_WORKSPACE, ERR_SCRATCH = -9, -10, -11, -12
 SCRATCH_BYTES = 32 << 20
 OP_N, OP_T = 0, 1
+MOST = 2 ** 31 - 1  # sizes and row strides are ints in the C calls; ctypes would cut larger ones without a word
 
 _lib = None
 _P = ctypes.c_void_p
@@ -319,6 +320,8 @@ def _ld(x, name):
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = x.shape
+    if rows > MOST or cols > MOST or (rows > 1 and x.stride(0) > MOST):
+        raise ValueError(f"{name} has a size or row stride over 2^31 - 1")
     if rows and cols > 1 and x.stride(1) != 1:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
     if rows > 1:
@@ -415,6 +418,8 @@ def gemm_strided_batched(A, B, C=None, *, opA: int = OP_N, opB: int = OP_N, alph
     import torch
 
     batch = C.shape[0] if C is not None else max(A.shape[0], B.shape[0])
+    if batch > MOST:
+        raise ValueError("the batch has a size over 2^31 - 1")
     M, K = _op_dims(A[0], opA)
     K2, N = _op_dims(B[0], opB)
     if K != K2:

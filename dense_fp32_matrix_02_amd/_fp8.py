@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import OK, SgemmError, load
+from ._binding import MOST, OK, SgemmError, load
 from ._binding import _ld as _any_ld
 
 ERR_TYPE, ERR_ROUTE = -13, -14
@@ -100,7 +100,7 @@ torch = _Torch()
 def _ld(x, name):
     """Row stride of a 2-D tensor with contiguous rows."""
     strides, shape = x.stride(), x.shape
-    if len(strides) == 2 and strides[1] == 1 and shape[0] > 1 and strides[0] >= shape[1] > 0:
+    if len(strides) == 2 and strides[1] == 1 and 1 < shape[0] <= MOST >= strides[0] >= shape[1] > 0:
         return strides[0]
     return _any_ld(x, name)
 
@@ -143,6 +143,8 @@ def _ints(x, name, length=None):
     _gpu(x, name, torch.int32)
     if x.dim() != 1 or (x.numel() > 1 and x.stride(0) != 1) or (length is not None and x.numel() != length):
         raise ValueError(f"{name} must be a dense 1-D tensor" + ("" if length is None else f" of {length} values"))
+    if x.numel() > MOST:
+        raise ValueError(f"{name} has more than 2^31 - 1 values")
     return x.data_ptr()
 
 
@@ -234,7 +236,7 @@ def _operand(Q, S, name, rows, cols, either=False):
         raise ValueError(f"the scales of {name} must be {rows}{f' or {_blocks(rows)}' if either else ''} x {_blocks(cols)}, "
                          f"not {per} x {blocks}")
     ld, step = Q.stride()[-2:]
-    if rows <= 1 or step != 1 or ld < cols:
+    if step != 1 or not 1 < rows <= MOST >= ld >= cols:
         ld = _ld(Q if Q.dim() == 2 else Q[0], name)
     by_row, by_block = S.stride()[-2:]
     return Q.data_ptr(), max(ld, 1), S.data_ptr(), by_row, by_block, 1 if per == rows else 128

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
+from ._binding import MOST
 from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _ld, _Library, _P, _stream_of, _type_of, torch
 
 SOFTMAX, SIGMOID = 0, 1
@@ -40,7 +41,14 @@ def _dense(x, name, dtype, shape):
     _gpu(x, name, dtype)
     if x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be a dense {' x '.join(map(str, shape))} tensor")
+    if shape[0] > MOST or shape[-1] > MOST:
+        raise ValueError(f"{name} has a size over 2^31 - 1")
     return x.data_ptr()
+
+
+def _bounded(x):
+    """A count that the C calls refuse, inside an int's range."""
+    return max(-1, min(x, MAX_EXPERTS + 1))
 
 
 def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
@@ -58,6 +66,8 @@ def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1,
     _gpu(logits, "logits")
     kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
     tokens, experts = logits.shape
+    if not (0 <= k <= MAX_CHOICES and 1 <= top_groups <= groups <= MAX_EXPERTS):
+        k, groups, top_groups = _bounded(k), _bounded(groups), _bounded(top_groups)
     at = None if bias is None else _dense(bias, "bias", torch.float32, (experts,))
     weights = _empty((tokens, max(k, 0)), torch.float32, logits.device, stream)
     ids = _empty((tokens, max(k, 0)), torch.int32, logits.device, stream)
@@ -96,6 +106,8 @@ def route_plan(experts, num_experts: int, *, stream=None):
         raise ValueError("experts must be tokens x k")
     tokens, k = experts.shape
     ids = _dense(experts, "experts", torch.int32, (tokens, k))
+    if not 1 <= num_experts <= MAX_EXPERTS:
+        num_experts = _bounded(num_experts)
     need = _c.route_plan_workspace_size(tokens, k, num_experts)
     offsets = _empty((max(num_experts, 0) + 1,), torch.int32, experts.device, stream)
     rows = _empty((tokens * k,), torch.int32, experts.device, stream)

@@ -1,0 +1,119 @@
+"""What the torch wrappers refuse before any HIP call, with tensors that say they are on a GPU (no GPU needed)."""
+from __future__ import annotations
+
+import os
+
+import pytest
+import torch
+
+import dense_fp32_matrix_02_amd as sg
+from dense_fp32_matrix_02_amd import _binding, _fp8
+
+FAR = 2 ** 32 + 304  # cut to 32 bits this is 304
+E4M3 = torch.float8_e4m3fn
+
+
+class OnGpu(torch.Tensor):
+    """A tensor without memory that says it is on a GPU."""
+
+    is_cuda = True
+    at = 0
+
+    def get_device(self):
+        return self.at
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.at)
+
+
+def gpu(shape, dtype=torch.float32, strides=None, at=0):
+    x = torch.empty(shape, dtype=dtype, device="meta") if strides is None else \
+        torch.empty_strided(shape, strides, dtype=dtype, device="meta")
+    x = x.as_subclass(OnGpu)
+    x.at = at
+    return x
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    if not os.path.exists(sg.LIB_PATH):
+        from dense_fp32_matrix_02_amd import build
+        build.build()
+    return sg.load()
+
+
+@pytest.fixture(autouse=True)
+def no_allocation(monkeypatch):
+    """Outputs without memory, on no stream."""
+    monkeypatch.setattr(_fp8, "_stream_of", lambda x, stream: 0)
+    for module in (_fp8, __import__("dense_fp32_matrix_02_amd._route", fromlist=["x"])):
+        monkeypatch.setattr(module, "_empty", lambda shape, dtype, device, stream, strides=None: gpu(shape, dtype, strides))
+        monkeypatch.setattr(module, "_stream_of", lambda x, stream: 0)
+
+
+def q(rows, cols, strides=None):
+    return gpu((rows, cols), E4M3, strides)
+
+
+def s(rows, blocks):
+    return gpu((rows, blocks))
+
+
+def ints(*shape):
+    return gpu(shape, torch.int32)
+
+
+WIDE = [
+    lambda: sg.quantize_fp8(gpu((2, 300), strides=(FAR, 1))),
+    lambda: sg.quantize_fp8(gpu((2 ** 32 + 5, 1))),
+    lambda: sg.quantize_fp8(gpu((5, 8)), index=ints(2 ** 32 + 5)),
+    lambda: sg.quantize_fp8(gpu((2, 300), strides=(FAR, 1)), blocks=True),
+    lambda: sg.quantize_fp8_cols(gpu((2, 300), strides=(FAR, 1))),
+    lambda: sg.quantize_fp8_cols(gpu((5, 8)), offsets=ints(2 ** 32 + 5)),
+    lambda: sg.gemm_fp8(q(2, 300, (FAR, 1)), s(2, 3), q(4, 300), s(4, 3)),
+    lambda: sg.gemm_fp8(q(2, 300), s(2, 3), q(4, 300, (FAR, 1)), s(4, 3)),
+    lambda: sg.gemm_fp8(q(2 ** 32 + 2, 8), s(2 ** 32 + 2, 1), q(4, 8), s(4, 1)),
+    lambda: sg.gemm_fp8(q(2, 300), s(2, 3), q(4, 300), s(4, 3), gpu((2, 4), strides=(FAR, 1))),
+    lambda: sg.gemm_fp8_experts(q(2, 300, (FAR, 1)), s(2, 3), gpu((1, 4, 300), E4M3), gpu((1, 4, 3)), ints(2)),
+    lambda: sg.gemm_fp8_experts(q(2, 300), s(2, 3), gpu((1, 4, 300), E4M3, (0, FAR, 1)), gpu((1, 4, 3)), ints(2)),
+    lambda: sg.gemm_fp8_experts_wgrad(q(2, 256, (FAR, 1)), s(2, 2), q(4, 256), s(4, 2), ints(2)),
+    lambda: sg.route(gpu((2, 8), strides=(FAR, 1)), 2),
+    lambda: sg.route(gpu((2 ** 32 + 2, 8)), 2),
+    lambda: sg.route_backward(gpu((2, 8), strides=(FAR, 1)), ints(2, 2), gpu((2, 2))),
+    lambda: sg.route_plan(ints(2 ** 32 + 2, 2), 4),
+    lambda: sg.route_plan(ints(2, 2 ** 32 + 2), 4),
+    lambda: sg.route_combine(gpu((4, 8), strides=(FAR, 1)), ints(2, 2), gpu((2, 2))),
+    lambda: sg.route_combine(gpu((4, 8)), ints(2 ** 32 + 2, 1), gpu((2 ** 32 + 2, 1))),
+    lambda: sg.route_combine_backward(gpu((2, 8), strides=(FAR, 1)), gpu((4, 8)), ints(2, 2), gpu((2, 2))),
+    lambda: _binding._ld(gpu((2, 300), strides=(FAR, 1)), "A"),
+    lambda: _binding._ld(gpu((1, 2 ** 32 + 300)), "A"),
+    lambda: sg.gemm(gpu((2, 300), strides=(FAR, 1)), gpu((300, 4)), gpu((2, 4)), stream=_Stream()),
+    lambda: sg.matmul(gpu((2, 300)), gpu((300, 4), strides=(FAR, 1)), gpu((2, 4)), stream=_Stream()),
+    lambda: sg.gemm_strided_batched(gpu((2 ** 32 + 1, 1, 1)), gpu((1, 1, 1)), gpu((2 ** 32 + 1, 1, 1)), stream=_Stream()),
+]
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("call", WIDE, ids=range(len(WIDE)))
+def test_sizes_and_strides_past_32_bits_are_refused(call):
+    with pytest.raises(ValueError):
+        call()
+
+
+@pytest.mark.parametrize("k,groups,top", [(2 ** 32 + 2, 1, 1), (-2 ** 32 + 2, 1, 1), (2, 2 ** 32 + 1, 1), (2, 1, 2 ** 32 + 1),
+                                          (2, -2 ** 32 + 1, 1), (2, 1, -2 ** 32 + 1), (2, 2, 3)])
+def test_counts_past_32_bits_are_refused(k, groups, top):
+    with pytest.raises(sg.SgemmError) as e:
+        sg.route(gpu((2, 8)), k, groups=groups, top_groups=top)
+    assert e.value.code in (sg.ERR_ROUTE, sg.ERR_DIM)
+
+
+@pytest.mark.parametrize("experts", [2 ** 32 + 4, -2 ** 32 + 4, 0, 1025])
+def test_experts_past_32_bits_are_refused(experts):
+    with pytest.raises(sg.SgemmError) as e:
+        sg.route_plan(ints(2, 2), experts)
+    assert e.value.code in (sg.ERR_ROUTE, sg.ERR_DIM)
