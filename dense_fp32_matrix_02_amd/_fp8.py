@@ -115,9 +115,12 @@ def _type_of(dtype, name):
     return code
 
 
-def _stream_of(x, stream):
-    # The handle of torch.cuda.current_stream without a Stream object.
-    return torch._C._cuda_getCurrentRawStream(x.get_device()) if stream is None else stream.cuda_stream
+def _stream_of(device, stream):
+    if stream is None:  # the handle of torch.cuda.current_stream without a Stream object
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on GPU {stream.device_index}, the call's tensors on GPU {device}")
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream, strides=None):
@@ -132,15 +135,19 @@ def _empty(shape, dtype, device, stream, strides=None):
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
-def _gpu(x, name, dtype=None):
-    if x.is_cuda and (dtype is None or x.dtype == dtype):
-        return x
-    raise TypeError(f"{name} must be a {'' if dtype is None else str(dtype).replace('torch.', '') + ' '}GPU tensor")
+def _gpu(x, name, dtype=None, device=None):
+    """The number of x's GPU, which has to be `device` where that is given."""
+    at = x.get_device()  # -1: on the host
+    if at < 0 or (dtype is not None and x.dtype != dtype):
+        raise TypeError(f"{name} must be a {'' if dtype is None else str(dtype).replace('torch.', '') + ' '}GPU tensor")
+    if device is not None and at != device:
+        raise ValueError(f"{name} is on GPU {at}, other tensors of the call on GPU {device}")
+    return at
 
 
-def _ints(x, name, length=None):
-    """Address of a dense 1-D int32 GPU tensor."""
-    _gpu(x, name, torch.int32)
+def _ints(x, name, device, length=None):
+    """Address of a dense 1-D int32 tensor on this GPU."""
+    _gpu(x, name, torch.int32, device)
     if x.dim() != 1 or (x.numel() > 1 and x.stride(0) != 1) or (length is not None and x.numel() != length):
         raise ValueError(f"{name} must be a dense 1-D tensor" + ("" if length is None else f" of {length} values"))
     if x.numel() > MOST:
@@ -171,10 +178,10 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
     gives zeros. ``blocks``: one scale for each 128 x 128 tile instead, for
     weights; S then has a row for each 128 rows of X.
     """
-    _gpu(X, "X")
+    on = _gpu(X, "X")
     kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
     rows, cols = X.shape
-    s = _stream_of(X, stream)
+    s = _stream_of(on, stream)
     if blocks:
         if index is not None:
             raise ValueError("tiles are quantised without an index")
@@ -185,7 +192,7 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
                "fp8_quantize_tiles")
         return Q, S
     n = rows if index is None else index.numel()
-    at = None if index is None else _ints(index, "index")
+    at = None if index is None else _ints(index, "index", on)
     Q, ldq = _bytes_out(n, cols, X.device, stream)
     S = _empty((n, _blocks(cols)), torch.float32, X.device, stream, (1, max(n, 1)))  # block by block
     if at is not None and n == 0:
@@ -205,32 +212,30 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
     begin a block, expert e's block offsets[e] // 128 + e; Q then has
     128 * (n // 128 + experts) columns, zero where no row is.
     """
-    _gpu(X, "X")
+    on = _gpu(X, "X")
     kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
     rows, cols = X.shape
     n = rows if index is None else index.numel()
-    at = None if index is None else _ints(index, "index")
+    at = None if index is None else _ints(index, "index", on)
     experts = 0 if offsets is None else offsets.numel() - 1
     if offsets is not None and experts < 1:
         raise ValueError("offsets must have experts + 1 values")
-    off = None if offsets is None else _ints(offsets, "offsets")
+    off = None if offsets is None else _ints(offsets, "offsets", on)
     width = n if offsets is None else 128 * (n // 128 + experts)
     Q, ldq = _bytes_out(cols, width, X.device, stream)
     S = _empty((cols, _blocks(width)), torch.float32, X.device, stream, (1, max(cols, 1)))
     if at is not None and n == 0:
         at, rows = None, 0
     _check(_c.fp8_quantize_cols(kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts, Q.data_ptr(), ldq, S.data_ptr(), 1,
-                                max(cols, 1), _stream_of(X, stream)), "fp8_quantize_cols")
+                                max(cols, 1), _stream_of(on, stream)), "fp8_quantize_cols")
     return Q, S
 
 
-def _operand(Q, S, name, rows, cols, either=False):
+def _operand(Q, S, name, rows, cols, device, either=False):
     """Address, row stride, scales' address and strides, and rows that share a
     scale, of a quantised matrix (2-D, or the last two axes of a 3-D one)."""
-    if Q.dtype != torch.float8_e4m3fn or not Q.is_cuda:
-        raise TypeError(f"{name} must be a float8_e4m3fn GPU tensor")
-    if S.dtype != torch.float32 or not S.is_cuda:
-        raise TypeError(f"the scales of {name} must be a float32 GPU tensor")
+    _gpu(Q, name, torch.float8_e4m3fn, device)
+    _gpu(S, f"the scales of {name}", torch.float32, device)
     per, blocks = S.shape[-2:]
     if blocks != _blocks(cols) or not (per == rows or (either and per == _blocks(rows))):
         raise ValueError(f"the scales of {name} must be {rows}{f' or {_blocks(rows)}' if either else ''} x {_blocks(cols)}, "
@@ -246,14 +251,15 @@ def _type_and_sums(C, fp32_sums):
     return _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
 
 
-def _result(C, shape, dtype, device, beta, stream):
+def _result(C, shape, dtype, A, on, beta, stream):
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs an input C")
-        return _empty(shape, dtype, device, stream)
+        return _empty(shape, dtype, A.device, stream)
     if C.shape != shape:
         raise ValueError(f"C must be {' x '.join(map(str, shape))}")
-    return _gpu(C, "C")
+    _gpu(C, "C", None, on)
+    return C
 
 
 def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, fp32_sums: bool = False, stream=None):
@@ -270,10 +276,11 @@ def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, fp32_sums: 
     (M, K), (N, K2) = A.shape, B.shape
     if K != K2:
         raise ValueError("inner dimensions differ")
-    a = _operand(A, SA, "A", M, K)
-    b = _operand(B, SB, "B", N, K, either=True)
-    C = _result(C, (M, N), dtype or torch.bfloat16, A.device, beta, stream)
-    _check(_c.fp8_gemm(_type_and_sums(C, fp32_sums), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)),
+    on = _gpu(A, "A")
+    a = _operand(A, SA, "A", M, K, on)
+    b = _operand(B, SB, "B", N, K, on, either=True)
+    C = _result(C, (M, N), dtype or torch.bfloat16, A, on, beta, stream)
+    _check(_c.fp8_gemm(_type_and_sums(C, fp32_sums), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)),
            "fp8_gemm")
     return C
 
@@ -291,12 +298,13 @@ def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, fp32_sums: bo
     (R, K), (E, N, K2) = A.shape, B.shape
     if K != K2:
         raise ValueError("inner dimensions differ")
-    off = _ints(offsets, "offsets", E + 1)
-    a = _operand(A, SA, "A", R, K)
-    b = _operand(B, SB, "B", N, K, either=True)
-    C = _result(C, (R, N), dtype or torch.bfloat16, A.device, 0.0, stream)
+    on = _gpu(A, "A")
+    off = _ints(offsets, "offsets", on, E + 1)
+    a = _operand(A, SA, "A", R, K, on)
+    b = _operand(B, SB, "B", N, K, on, either=True)
+    C = _result(C, (R, N), dtype or torch.bfloat16, A, on, 0.0, stream)
     _check(_c.fp8_gemm_experts(_type_and_sums(C, fp32_sums), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5],
-                               off, C.data_ptr(), _ld(C, "C"), _stream_of(A, stream)), "fp8_gemm_experts")
+                               off, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)), "fp8_gemm_experts")
     return C
 
 
@@ -312,7 +320,8 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
         raise ValueError("A and B must be 2-D")
     (M, P), (N, P2) = A.shape, B.shape
     E = offsets.numel() - 1
-    off = _ints(offsets, "offsets")
+    on = _gpu(A, "A")
+    off = _ints(offsets, "offsets", on)
     if P != P2:
         raise ValueError("inner dimensions differ")
     if E < 1 or P % 128 != 0 or P < 128 * E:
@@ -320,12 +329,12 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
     # P counts the blocks of rows, so the rows are known to a block: the most
     # that P has room for. The offsets end before that.
     rows = P - 128 * E + 127
-    a = _operand(A, SA, "A", M, P)
-    b = _operand(B, SB, "B", N, P)
-    C = _result(C, (E, M, N), dtype or torch.float32, A.device, beta, stream)
+    a = _operand(A, SA, "A", M, P, on)
+    b = _operand(B, SB, "B", N, P, on)
+    C = _result(C, (E, M, N), dtype or torch.float32, A, on, beta, stream)
     if C.dim() != 3:
         raise ValueError("C must be experts x M x N")
     ldc = _ld(C[0], "C")
     _check(_c.fp8_gemm_experts_wgrad(_type_and_sums(C, fp32_sums), rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
-                                     C.stride(0), _stream_of(A, stream)), "fp8_gemm_experts_wgrad")
+                                     C.stride(0), _stream_of(on, stream)), "fp8_gemm_experts_wgrad")
     return C

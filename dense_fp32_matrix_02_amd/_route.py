@@ -36,9 +36,9 @@ def _score(score):
     return code
 
 
-def _dense(x, name, dtype, shape):
-    """Address of a dense GPU tensor of this dtype and shape."""
-    _gpu(x, name, dtype)
+def _dense(x, name, dtype, shape, device):
+    """Address of a dense tensor of this dtype and shape on this GPU."""
+    _gpu(x, name, dtype, device)
     if x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be a dense {' x '.join(map(str, shape))} tensor")
     if shape[0] > MOST or shape[-1] > MOST:
@@ -63,16 +63,16 @@ def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1,
     groups with the largest sum of their two largest choice values take part;
     ``renorm`` divides the weights by their sum; ``scale`` multiplies them.
     """
-    _gpu(logits, "logits")
+    on = _gpu(logits, "logits")
     kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
     tokens, experts = logits.shape
     if not (0 <= k <= MAX_CHOICES and 1 <= top_groups <= groups <= MAX_EXPERTS):
         k, groups, top_groups = _bounded(k), _bounded(groups), _bounded(top_groups)
-    at = None if bias is None else _dense(bias, "bias", torch.float32, (experts,))
+    at = None if bias is None else _dense(bias, "bias", torch.float32, (experts,), on)
     weights = _empty((tokens, max(k, 0)), torch.float32, logits.device, stream)
     ids = _empty((tokens, max(k, 0)), torch.int32, logits.device, stream)
     _check(_c.route(kind, tokens, experts, logits.data_ptr(), ld, at, how, groups, top_groups, k,
-                             int(bool(renorm)), scale, weights.data_ptr(), ids.data_ptr(), _stream_of(logits, stream)),
+                             int(bool(renorm)), scale, weights.data_ptr(), ids.data_ptr(), _stream_of(on, stream)),
            "route")
     return weights, ids
 
@@ -81,15 +81,15 @@ def route_backward(logits, experts, dweights, *, score: str = "softmax", renorm:
                    stream=None):
     """The gradient of the logits (float32) for given gradients of route's
     weights; ``experts`` are the ones it chose."""
-    _gpu(logits, "logits")
+    on = _gpu(logits, "logits")
     kind, ld, how = _type_of(logits.dtype, "logits"), _ld(logits, "logits"), _score(score)
     tokens, count = logits.shape
     k = experts.shape[-1]
-    ids = _dense(experts, "experts", torch.int32, (tokens, k))
-    dw = _dense(dweights, "dweights", torch.float32, (tokens, k))
+    ids = _dense(experts, "experts", torch.int32, (tokens, k), on)
+    dw = _dense(dweights, "dweights", torch.float32, (tokens, k), on)
     out = _empty((tokens, count), torch.float32, logits.device, stream)
     _check(_c.route_backward(kind, tokens, count, logits.data_ptr(), ld, ids, dw, how, k,
-                                      int(bool(renorm)), scale, out.data_ptr(), max(count, 1), _stream_of(logits, stream)),
+                                      int(bool(renorm)), scale, out.data_ptr(), max(count, 1), _stream_of(on, stream)),
            "route_backward")
     return out
 
@@ -105,7 +105,8 @@ def route_plan(experts, num_experts: int, *, stream=None):
     if experts.dim() != 2:
         raise ValueError("experts must be tokens x k")
     tokens, k = experts.shape
-    ids = _dense(experts, "experts", torch.int32, (tokens, k))
+    on = _gpu(experts, "experts", torch.int32)
+    ids = _dense(experts, "experts", torch.int32, (tokens, k), on)
     if not 1 <= num_experts <= MAX_EXPERTS:
         num_experts = _bounded(num_experts)
     need = _c.route_plan_workspace_size(tokens, k, num_experts)
@@ -114,7 +115,7 @@ def route_plan(experts, num_experts: int, *, stream=None):
     place = _empty((tokens, k), torch.int32, experts.device, stream)
     room = _empty((need // 4,), torch.int32, experts.device, stream) if need else None
     _check(_c.route_plan(tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),
-                                  place.data_ptr(), None if room is None else room.data_ptr(), need, _stream_of(experts, stream)),
+                                  place.data_ptr(), None if room is None else room.data_ptr(), need, _stream_of(on, stream)),
            "route_plan")
     return offsets, rows, place
 
@@ -122,18 +123,18 @@ def route_plan(experts, num_experts: int, *, stream=None):
 def route_combine(Z, place, weights, Y=None, *, stream=None):
     """Y[t] = sum_j weights[t, j] * Z[place[t, j]], of Z's dtype; a place
     outside Z's rows adds nothing."""
-    _gpu(Z, "Z")
+    on = _gpu(Z, "Z")
     kind, ldz = _type_of(Z.dtype, "Z"), _ld(Z, "Z")
     rows, cols = Z.shape
     tokens, k = place.shape
-    at, w = _dense(place, "place", torch.int32, (tokens, k)), _dense(weights, "weights", torch.float32, (tokens, k))
+    at, w = _dense(place, "place", torch.int32, (tokens, k), on), _dense(weights, "weights", torch.float32, (tokens, k), on)
     if Y is None:
         Y = _empty((tokens, cols), Z.dtype, Z.device, stream)
-    _gpu(Y, "Y", Z.dtype)
+    _gpu(Y, "Y", Z.dtype, on)
     if tuple(Y.shape) != (tokens, cols):
         raise ValueError("Y must be tokens x cols")
     _check(_c.route_combine(kind, tokens, k, rows, cols, Z.data_ptr(), ldz, at, w, Y.data_ptr(), _ld(Y, "Y"),
-                                     _stream_of(Z, stream)), "route_combine")
+                                     _stream_of(on, stream)), "route_combine")
     return Y
 
 
@@ -143,17 +144,17 @@ def route_combine_backward(dY, Z, place, weights, *, stream=None):
     place must name each row of Z once, as route_plan's does: rows that it does
     not name are not written.
     """
-    _gpu(Z, "Z")
-    _gpu(dY, "dY", Z.dtype)
+    on = _gpu(Z, "Z")
+    _gpu(dY, "dY", Z.dtype, on)
     kind, ldz, ldy = _type_of(Z.dtype, "Z"), _ld(Z, "Z"), _ld(dY, "dY")
     rows, cols = Z.shape
     tokens, k = place.shape
     if tuple(dY.shape) != (tokens, cols):
         raise ValueError("dY must be tokens x cols")
-    at, w = _dense(place, "place", torch.int32, (tokens, k)), _dense(weights, "weights", torch.float32, (tokens, k))
+    at, w = _dense(place, "place", torch.int32, (tokens, k), on), _dense(weights, "weights", torch.float32, (tokens, k), on)
     dZ = _empty((rows, cols), Z.dtype, Z.device, stream)
     dw = _empty((tokens, k), torch.float32, Z.device, stream)
     _check(_c.route_combine_backward(kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,
-                                              dZ.data_ptr(), max(cols, 1), dw.data_ptr(), _stream_of(Z, stream)),
+                                              dZ.data_ptr(), max(cols, 1), dw.data_ptr(), _stream_of(on, stream)),
            "route_combine_backward")
     return dZ, dw

@@ -7,10 +7,15 @@ import pytest
 import torch
 
 import dense_fp32_matrix_02_amd as sg
-from dense_fp32_matrix_02_amd import _binding, _fp8
+from dense_fp32_matrix_02_amd import _binding, _fp8, _route
 
 FAR = 2 ** 32 + 304  # cut to 32 bits this is 304
 E4M3 = torch.float8_e4m3fn
+
+
+class _Stream:
+    cuda_stream = 0
+    device_index = 0
 
 
 class OnGpu(torch.Tensor):
@@ -46,10 +51,8 @@ def built_library():
 @pytest.fixture(autouse=True)
 def no_allocation(monkeypatch):
     """Outputs without memory, on no stream."""
-    monkeypatch.setattr(_fp8, "_stream_of", lambda x, stream: 0)
-    for module in (_fp8, __import__("dense_fp32_matrix_02_amd._route", fromlist=["x"])):
+    for module in (_fp8, _route):
         monkeypatch.setattr(module, "_empty", lambda shape, dtype, device, stream, strides=None: gpu(shape, dtype, strides))
-        monkeypatch.setattr(module, "_stream_of", lambda x, stream: 0)
 
 
 def q(rows, cols, strides=None):
@@ -67,7 +70,7 @@ def ints(*shape):
 WIDE = [
     lambda: sg.quantize_fp8(gpu((2, 300), strides=(FAR, 1))),
     lambda: sg.quantize_fp8(gpu((2 ** 32 + 5, 1))),
-    lambda: sg.quantize_fp8(gpu((5, 8)), index=ints(2 ** 32 + 5)),
+    lambda: sg.quantize_fp8(gpu((5, 8)), index=ints(2 ** 32 + 5), stream=_Stream()),
     lambda: sg.quantize_fp8(gpu((2, 300), strides=(FAR, 1)), blocks=True),
     lambda: sg.quantize_fp8_cols(gpu((2, 300), strides=(FAR, 1))),
     lambda: sg.quantize_fp8_cols(gpu((5, 8)), offsets=ints(2 ** 32 + 5)),
@@ -94,10 +97,6 @@ WIDE = [
 ]
 
 
-class _Stream:
-    cuda_stream = 0
-
-
 @pytest.mark.parametrize("call", WIDE, ids=range(len(WIDE)))
 def test_sizes_and_strides_past_32_bits_are_refused(call):
     with pytest.raises(ValueError):
@@ -108,12 +107,48 @@ def test_sizes_and_strides_past_32_bits_are_refused(call):
                                           (2, -2 ** 32 + 1, 1), (2, 1, -2 ** 32 + 1), (2, 2, 3)])
 def test_counts_past_32_bits_are_refused(k, groups, top):
     with pytest.raises(sg.SgemmError) as e:
-        sg.route(gpu((2, 8)), k, groups=groups, top_groups=top)
+        sg.route(gpu((2, 8)), k, groups=groups, top_groups=top, stream=_Stream())
     assert e.value.code in (sg.ERR_ROUTE, sg.ERR_DIM)
 
 
 @pytest.mark.parametrize("experts", [2 ** 32 + 4, -2 ** 32 + 4, 0, 1025])
 def test_experts_past_32_bits_are_refused(experts):
     with pytest.raises(sg.SgemmError) as e:
-        sg.route_plan(ints(2, 2), experts)
+        sg.route_plan(ints(2, 2), experts, stream=_Stream())
     assert e.value.code in (sg.ERR_ROUTE, sg.ERR_DIM)
+
+
+def call_with(fn, far):
+    """The call with tensor number `far` of `fn`'s list on another GPU."""
+    made = []
+
+    def on(shape, dtype=torch.float32):
+        made.append(gpu(shape, dtype, at=1 if len(made) == far else 0))
+        return made[-1]
+
+    return fn(on)
+
+
+TOGETHER = [  # the call and the number of its tensors
+    (lambda t: sg.quantize_fp8(t((5, 8)), index=t((4,), torch.int32), stream=_Stream()), 2),
+    (lambda t: sg.quantize_fp8_cols(t((5, 8)), index=t((4,), torch.int32), offsets=t((3,), torch.int32), stream=_Stream()), 3),
+    (lambda t: sg.gemm_fp8(t((2, 300), E4M3), t((2, 3)), t((4, 300), E4M3), t((4, 3)), t((2, 4)), stream=_Stream()), 5),
+    (lambda t: sg.gemm_fp8_experts(t((2, 300), E4M3), t((2, 3)), t((2, 4, 300), E4M3), t((2, 4, 3)), t((3,), torch.int32),
+                                   t((2, 4)), stream=_Stream()), 6),
+    (lambda t: sg.gemm_fp8_experts_wgrad(t((2, 256), E4M3), t((2, 2)), t((4, 256), E4M3), t((4, 2)), t((3,), torch.int32),
+                                         t((2, 2, 4)), stream=_Stream()), 6),
+    (lambda t: sg.route(t((2, 8)), 2, bias=t((8,)), stream=_Stream()), 2),
+    (lambda t: sg.route_backward(t((2, 8)), t((2, 2), torch.int32), t((2, 2)), stream=_Stream()), 3),
+    (lambda t: sg.route_plan(t((2, 2), torch.int32), 4, stream=_Stream()), 1),
+    (lambda t: sg.route_combine(t((4, 8)), t((2, 2), torch.int32), t((2, 2)), t((2, 8)), stream=_Stream()), 4),
+    (lambda t: sg.route_combine_backward(t((2, 8)), t((4, 8)), t((2, 2), torch.int32), t((2, 2)), stream=_Stream()), 4),
+]
+
+
+@pytest.mark.parametrize("fn,far", [(fn, far) for fn, count in TOGETHER for far in range(count)],
+                         ids=[f"{i}-{far}" for i, (fn, count) in enumerate(TOGETHER) for far in range(count)])
+def test_tensors_and_stream_have_to_be_on_one_gpu(fn, far):
+    with pytest.raises(ValueError, match="GPU 1"):
+        call_with(fn, far)
+    with pytest.raises(sg.SgemmError):  # all together: the C call is reached, and refuses tensors without memory
+        call_with(fn, None)
