@@ -236,6 +236,8 @@ def _operand(Q, S, name, rows, cols, device, either=False):
     scale, of a quantised matrix (2-D, or the last two axes of a 3-D one)."""
     _gpu(Q, name, torch.float8_e4m3fn, device)
     _gpu(S, f"the scales of {name}", torch.float32, device)
+    if S.dim() != Q.dim():
+        raise ValueError(f"{name} and its scales must have as many axes")
     per, blocks = S.shape[-2:]
     if blocks != _blocks(cols) or not (per == rows or (either and per == _blocks(rows))):
         raise ValueError(f"the scales of {name} must be {rows}{f' or {_blocks(rows)}' if either else ''} x {_blocks(cols)}, "

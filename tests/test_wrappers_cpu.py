@@ -152,3 +152,15 @@ def test_tensors_and_stream_have_to_be_on_one_gpu(fn, far):
         call_with(fn, far)
     with pytest.raises(sg.SgemmError):  # all together: the C call is reached, and refuses tensors without memory
         call_with(fn, None)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: sg.gemm_fp8(q(2, 300), gpu((5, 2, 3)), q(4, 300), s(4, 3), stream=_Stream()),
+    lambda: sg.gemm_fp8(q(2, 300), s(2, 3), q(4, 300), gpu((5, 4, 3)), stream=_Stream()),
+    lambda: sg.gemm_fp8(q(2, 300), gpu((6,)), q(4, 300), s(4, 3), stream=_Stream()),
+    lambda: sg.gemm_fp8_experts(q(2, 300), gpu((5, 2, 3)), gpu((2, 4, 300), E4M3), gpu((2, 4, 3)), ints(3), stream=_Stream()),
+    lambda: sg.gemm_fp8_experts_wgrad(q(2, 256), gpu((5, 2, 2)), q(4, 256), s(4, 2), ints(3), stream=_Stream()),
+    lambda: sg.gemm_fp8_experts_wgrad(q(2, 256), s(2, 2), q(4, 256), gpu((5, 4, 2)), ints(3), stream=_Stream())])
+def test_scales_have_the_axes_of_their_operand(call):
+    with pytest.raises(ValueError):
+        call()
