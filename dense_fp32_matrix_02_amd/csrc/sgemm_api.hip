@@ -1026,20 +1026,22 @@ int sgemm_mi355_tile_map(int bid, int tiles_m, int tiles_n, int group_m, int* tm
 const char* sgemm_mi355_strerror(int code) {
   switch (code) {
     case SGEMM_MI355_OK: return "success";
-    case SGEMM_MI355_ERR_DIM: return "a matrix dimension or the batch count is negative";
+    case SGEMM_MI355_ERR_DIM: return "a matrix dimension or a count is negative, or a call with experts has none";
     case SGEMM_MI355_ERR_LD: return "a leading dimension is smaller than its row length";
     case SGEMM_MI355_ERR_NULL: return "null pointer for a matrix with elements";
-    case SGEMM_MI355_ERR_ALIAS: return "C overlaps A or B";
+    case SGEMM_MI355_ERR_ALIAS: return "C, or another output, overlaps another matrix of the call";
     case SGEMM_MI355_ERR_EXTENT: return "problem too large for one launch";
     case SGEMM_MI355_ERR_LAUNCH: return "the HIP runtime rejected the kernel launch";
     case SGEMM_MI355_ERR_CONFIG: return "unknown kernel configuration, or one built for other operand layouts";
-    case SGEMM_MI355_ERR_ALIGN: return "a matrix pointer is not 4-byte aligned";
-    case SGEMM_MI355_ERR_STRIDE: return "a batch stride is negative, or batch entries of C overlap";
-    case SGEMM_MI355_ERR_OP: return "an operand op is neither SGEMM_MI355_OP_N nor SGEMM_MI355_OP_T";
+    case SGEMM_MI355_ERR_ALIGN: return "a pointer is not aligned to its element type";
+    case SGEMM_MI355_ERR_STRIDE:
+      return "a stride of a batch, of experts or of scales is negative, or lets entries of an output overlap";
+    case SGEMM_MI355_ERR_OP:
+      return "an operand op is neither SGEMM_MI355_OP_N nor SGEMM_MI355_OP_T, or another option has an unknown value";
     case SGEMM_MI355_ERR_SCRATCH:
       return "the split-K partial sums exceed the library's static scratch (SGEMM_MI355_SCRATCH_BYTES per device)";
     case SGEMM_MI355_ERR_WORKSPACE:
-      return "the workspace is smaller than sgemm_mi355_splitk_workspace_size or sgemm_mi355_streamk_workspace_size";
+      return "the workspace is smaller than the call's _workspace_size function says";
     case SGEMM_MI355_ERR_TYPE: return "an element type is not one the call supports";
     case SGEMM_MI355_ERR_ROUTE: return "the experts, groups or choices are outside what routing supports";
     default: return "unknown error code";

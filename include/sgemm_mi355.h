@@ -62,7 +62,7 @@ extern "C" {
 #define SGEMM_MI355_ERR_ALIGN (-8)    /* a pointer is not 4-byte aligned */
 #define SGEMM_MI355_ERR_STRIDE (-9)   /* a batch stride is negative, or batch entries of C overlap */
 #define SGEMM_MI355_ERR_OP (-10)      /* an op argument is neither OP_N nor OP_T */
-#define SGEMM_MI355_ERR_WORKSPACE (-11) /* split-K or stream-K workspace smaller than required */
+#define SGEMM_MI355_ERR_WORKSPACE (-11) /* a workspace smaller than the call's _workspace_size function says */
 #define SGEMM_MI355_ERR_SCRATCH (-12) /* split-K partial sums larger than SGEMM_MI355_SCRATCH_BYTES */
 
 #define SGEMM_MI355_ERR_TYPE (-13)    /* an element type is not one the call supports */

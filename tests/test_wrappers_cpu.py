@@ -164,3 +164,14 @@ def test_tensors_and_stream_have_to_be_on_one_gpu(fn, far):
 def test_scales_have_the_axes_of_their_operand(call):
     with pytest.raises(ValueError):
         call()
+
+
+def test_messages_cover_the_calls_that_return_them():
+    """route_plan returns ERR_WORKSPACE, too, and 2-byte types have no 4-byte alignment."""
+    workspace = sg.strerror(sg.ERR_WORKSPACE)
+    assert "workspace" in workspace and "splitk" not in workspace and "streamk" not in workspace
+    assert "4-byte" not in sg.strerror(sg.ERR_ALIGN)
+    for code, word in ((sg.ERR_ALIAS, "output"), (sg.ERR_STRIDE, "scales"), (sg.ERR_DIM, "experts"), (sg.ERR_OP, "option")):
+        assert word in sg.strerror(code)
+    codes = range(-14, 1)
+    assert len({sg.strerror(c) for c in codes}) == len(codes)
