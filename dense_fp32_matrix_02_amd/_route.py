@@ -141,8 +141,8 @@ def route_combine(Z, place, weights, Y=None, *, stream=None):
 def route_combine_backward(dY, Z, place, weights, *, stream=None):
     """(dZ, dweights) of route_combine for the gradient dY of its result.
 
-    place must name each row of Z once, as route_plan's does: rows that it does
-    not name are not written.
+    place must name no row of Z twice (route_plan's names each once); the
+    gradient of a row that it does not name is zero.
     """
     on = _gpu(Z, "Z")
     _gpu(dY, "dY", Z.dtype, on)
@@ -157,4 +157,7 @@ def route_combine_backward(dY, Z, place, weights, *, stream=None):
     _check(_c.route_combine_backward(kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,
                                               dZ.data_ptr(), max(cols, 1), dw.data_ptr(), _stream_of(on, stream)),
            "route_combine_backward")
+    if tokens * k == 0 and dZ.numel() > 0:  # the C call writes nothing then
+        with torch.cuda.stream(stream):
+            dZ.zero_()
     return dZ, dw

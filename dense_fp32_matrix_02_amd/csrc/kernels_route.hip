@@ -666,11 +666,58 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a, int slabs) 
   store8_once((T*)a.Y + token * a.ldy + col, valid, y);
 }
 
-// A wave has one choice of a token, and so a row of Z and dZ: nothing is shared
-// between waves, and nothing waits for another row's sum.
+// Zeros in the rows of dZ that no place names, of the `each` rows of this
+// workgroup: a bit for each in LDS, and all places are read. Workgroups of the
+// gradient's own launch do it, while the others wait for memory: 4096 tokens of
+// 8 rows of 4096 126 us, 123 without; 16384 of 512 columns 60.4, 59.2; 1048576
+// of 64 columns 2.47 ms, 2.39 (as a launch of its own 128, 75, 3.3 ms). With 32 or
+// 256 such workgroups 16384 of 512 columns take 59.6 or 62.6, and with as many
+// unnamed rows more 298 or 87, 110 with these.
+constexpr int kZeroGroups = 128;
+constexpr int kMostNamed = 1 << 17;  // rows of one of them
+
 template <class T>
-__global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs a) {
-  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+__device__ __forceinline__ void zero_unnamed_rows(const CombineArgs& a, int each, uint32_t* named) {
+  typedef int ints __attribute__((ext_vector_type(4), aligned(4)));
+  const int first = (int)blockIdx.x * each, rows = min(each, a.rows - first), words = (rows + 31) / 32;
+  for (int w = threadIdx.x; w < words; w += 256) named[w] = 0;
+  __syncthreads();
+  auto name = [&](int place) {
+    const uint32_t r = (uint32_t)place - (uint32_t)first;
+    if (r < (uint32_t)rows) atomicOr(&named[r / 32], 1u << (r % 32));
+  };
+  constexpr int DEEP = 8;  // loads in flight
+  const int entries = a.tokens * a.choices, whole = entries / (1024 * DEEP) * (1024 * DEEP);
+  for (int i = 4 * threadIdx.x; i < whole; i += 1024 * DEEP) {
+    ints p[DEEP];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) p[d] = *(const ints*)(a.place + i + 1024 * d);
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) name(p[d][0]), name(p[d][1]), name(p[d][2]), name(p[d][3]);
+  }
+#pragma unroll 8
+  for (int i = whole + threadIdx.x; i < entries; i += 256) name(a.place[i]);
+  __syncthreads();
+  for (int w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64); w < words; w += 4) {
+    const uint32_t there = 32 * w + 32 <= rows ? ~0u : (1u << (rows % 32)) - 1;
+    uint32_t left = __builtin_amdgcn_readfirstlane(~named[w] & there);
+    for (; left != 0; left &= left - 1) {
+      T* to = (T*)a.dZ + (int64_t)(first + 32 * w + __builtin_ctz(left)) * a.lddz;
+      const float zeros[8] = {};
+      for (uint32_t col = 8 * (threadIdx.x % 64); col < (uint32_t)a.cols; col += 512)
+        store8_once(to + col, (int)((uint32_t)a.cols - col), zeros);
+    }
+  }
+}
+
+// A wave has one choice of a token, and so a row of Z and dZ: nothing is shared
+// between waves, and nothing waits for another row's sum. The first `zeros`
+// workgroups look for the rows without a name meanwhile.
+template <class T>
+__global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs a, int zeros, int each) {
+  __shared__ uint32_t named[kMostNamed / 32];
+  if ((int)blockIdx.x < zeros) return zero_unnamed_rows<T>(a, each, named);
+  const int64_t item = (int64_t)(blockIdx.x - zeros) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t token = item / a.choices;
   if (token >= a.tokens) return;
   const int lane = threadIdx.x % 64, row = a.place[item];
@@ -693,6 +740,16 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineArgs a) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d, 64);
   if (lane == 0) a.dweights[item] = dot;
+}
+
+// Zeros in all of dZ, before the gradient, where there are more rows than those
+// workgroups have bits for.
+template <class T>
+__global__ void __launch_bounds__(256) zero_rows_kernel(CombineArgs a) {
+  const float zeros[8] = {};
+  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; r < a.rows; r += (int64_t)gridDim.x * 4)
+    for (uint32_t col = 8 * (threadIdx.x % 64); col < (uint32_t)a.cols; col += 512)
+      store8_once((T*)a.dZ + r * a.lddz + col, (int)((uint32_t)a.cols - col), zeros);
 }
 
 // f(V) for the least V of 1, 2, 4, 8, 16 with 64 V >= experts.
@@ -755,9 +812,20 @@ hipError_t launch_combine(int type, const CombineArgs& c, hipStream_t s) {
 }
 
 hipError_t launch_combine_backward(int type, const CombineArgs& c, hipStream_t s) {
-  const int64_t items = (int64_t)c.tokens * c.choices;
+  const int64_t blocks = ((int64_t)c.tokens * c.choices + 3) / 4;
+  int each = (int)(((int64_t)c.rows + kZeroGroups - 1) / kZeroGroups);
+  int zeros = c.rows > 0 && c.cols > 0 ? (c.rows + each - 1) / each : 0;
+  // A launch counts its threads in 32 bits.
+  const bool apart = each > kMostNamed || (blocks + zeros) * 256 > (int64_t)UINT32_MAX;
+  if (apart) zeros = 0;
   return by_type(type, [&](auto t) {
-    return launch_with((const void*)&combine_backward_kernel<decltype(t)>, dim3((unsigned)((items + 3) / 4)), dim3(256), c, s);
+    if (apart) {
+      const hipError_t err = launch_with((const void*)&zero_rows_kernel<decltype(t)>, dim3(8192), dim3(256), c, s);
+      if (err != hipSuccess) return err;
+    }
+    CombineArgs copy = c;
+    void* args[] = {&copy, &zeros, &each};
+    return hipLaunchKernel((const void*)&combine_backward_kernel<decltype(t)>, dim3((unsigned)(zeros + blocks)), dim3(256), args, 0, s);
   });
 }
 

@@ -91,8 +91,10 @@ int sgemm_mi355_route_combine(int type, int tokens, int choices, int rows, int c
 /*
  * Its gradients: dZ[place[t][j]] = weights[t][j] * dY[t] and dweights[t][j] =
  * sum_n dY[t][n] * Z[place[t][j]][n] (FP32; 0 for a place outside the rows). A row that
- * no place names is not written: sgemm_mi355_route_plan names each of
- * tokens*choices rows once. dZ has Z's type and row stride lddz.
+ * no place names gets zeros (without any place, nothing is written). No row may
+ * be named twice (its gradient would be one of the two):
+ * sgemm_mi355_route_plan names each of tokens*choices rows once. dZ has Z's
+ * type and row stride lddz. One kernel; two where Z has over 16777216 rows.
  */
 int sgemm_mi355_route_combine_backward(int type, int tokens, int choices, int rows, int cols,
                                        const void *dY, int lddy, const void *Z, int ldz, const int *place,
