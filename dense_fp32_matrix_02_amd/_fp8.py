@@ -234,23 +234,21 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
 def _operand(Q, S, name, rows, cols, device, either=False):
     """Address, row stride, scales' address and strides, and rows that share a
     scale, of a quantised matrix (2-D, or the last two axes of a 3-D one)."""
-    _gpu(Q, name, torch.float8_e4m3fn, device)
-    _gpu(S, f"the scales of {name}", torch.float32, device)
-    if S.dim() != Q.dim():
+    if Q.get_device() != device or S.get_device() != device or Q.dtype != torch.float8_e4m3fn or S.dtype != torch.float32:
+        _gpu(Q, name, torch.float8_e4m3fn, device)
+        _gpu(S, f"the scales of {name}", torch.float32, device)
+    sizes, strides, apart = S.shape, Q.stride(), S.stride()
+    if len(sizes) != len(strides):
         raise ValueError(f"{name} and its scales must have as many axes")
-    per, blocks = S.shape[-2:]
+    per, blocks = sizes[-2:]
     if blocks != _blocks(cols) or not (per == rows or (either and per == _blocks(rows))):
         raise ValueError(f"the scales of {name} must be {rows}{f' or {_blocks(rows)}' if either else ''} x {_blocks(cols)}, "
                          f"not {per} x {blocks}")
-    ld, step = Q.stride()[-2:]
+    ld, step = strides[-2:]
     if step != 1 or not 1 < rows <= MOST >= ld >= cols:
-        ld = _ld(Q if Q.dim() == 2 else Q[0], name)
-    by_row, by_block = S.stride()[-2:]
-    return Q.data_ptr(), max(ld, 1), S.data_ptr(), by_row, by_block, 1 if per == rows else 128
-
-
-def _type_and_sums(C, fp32_sums):
-    return _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
+        ld = _ld(Q if len(strides) == 2 else Q[0], name)
+    by_row, by_block = apart[-2:]
+    return Q.data_ptr(), ld or 1, S.data_ptr(), by_row, by_block, 1 if per == rows else 128
 
 
 def _result(C, shape, dtype, A, on, beta, stream):
@@ -282,7 +280,8 @@ def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, fp32_sums: 
     a = _operand(A, SA, "A", M, K, on)
     b = _operand(B, SB, "B", N, K, on, either=True)
     C = _result(C, (M, N), dtype or torch.bfloat16, A, on, beta, stream)
-    _check(_c.fp8_gemm(_type_and_sums(C, fp32_sums), M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)),
+    kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
+    _check(_c.fp8_gemm(kind, M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)),
            "fp8_gemm")
     return C
 
@@ -305,7 +304,8 @@ def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, fp32_sums: bo
     a = _operand(A, SA, "A", R, K, on)
     b = _operand(B, SB, "B", N, K, on, either=True)
     C = _result(C, (R, N), dtype or torch.bfloat16, A, on, 0.0, stream)
-    _check(_c.fp8_gemm_experts(_type_and_sums(C, fp32_sums), R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5],
+    kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
+    _check(_c.fp8_gemm_experts(kind, R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5],
                                off, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)), "fp8_gemm_experts")
     return C
 
@@ -337,6 +337,7 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
     if C.dim() != 3:
         raise ValueError("C must be experts x M x N")
     ldc = _ld(C[0], "C")
-    _check(_c.fp8_gemm_experts_wgrad(_type_and_sums(C, fp32_sums), rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
+    kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
+    _check(_c.fp8_gemm_experts_wgrad(kind, rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
                                      C.stride(0), _stream_of(on, stream)), "fp8_gemm_experts_wgrad")
     return C
