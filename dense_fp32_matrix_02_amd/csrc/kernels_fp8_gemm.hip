@@ -140,8 +140,8 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
   // The least of the estimated times (us; r: rounds of 256 workgroups, one for
   // each CU; k: K/1024), fitted to times of M 8 .. 2048, N 256 .. 4096, K 256 ..
   // 8192 and 8192^3, as K 2048, N 4096, bf16, M 128 / 512 / 2048:
-  //   few-rows kernel, 16, 32, 64 rows   27.2, 18.8, 15.0 / 97, 65, 55 / -, -, 210
-  //   128 x 128 tiles, 256 x 256 tiles   13.0, 17.1 / 14.2, 24.3 / 24.5, 28.3
+  //   few-rows kernel, 16, 32, 64 rows   20.5, 15.7, 15.4 / 66, 50, 56 / 237, 182, 211
+  //   128 x 128 tiles, 256 x 256 tiles   11.8, 17.4 / 12.7, 25.3 / 23.1, 29.0
   // Widened values need more registers than the strip of a wave of a 256 x 256
   // tile leaves, so that form has smaller tiles only (24.4 us at M 512, fp32).
   const double k = g.K / 1024.0 / (form == FP8_WGRAD ? g.experts : 1);
@@ -180,7 +180,10 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
   }
   if (form != FP8_WGRAD) {
     auto rounds = [&](int bm) { return groups(bm, 16) > 1.0 ? groups(bm, 16) : 1.0; };
-    offer({Choice::SKINNY, true, 64, 16, 512}, 2.4 + rounds(64) * (1.3 + (experts ? 1.2 : 2.4) * k));
+    // A CU holds one workgroup of 64 rows at a time (N 2048, K 4096, M 192: 25.1 us
+    // in its two rounds, 19.2 in 128 x 128 tiles).
+    offer({Choice::SKINNY, true, 64, 16, 512},
+          2.4 + (experts ? rounds(64) * (1.3 + 1.2 * k) : std::ceil(rounds(64)) * (1.3 + 2.5 * k)));
     offer({Choice::SKINNY, true, 32, 16, 512}, 2.6 + rounds(32) * (0.8 + (experts ? 0.9 : 1.41) * k));
     offer({Choice::SKINNY, true, 16, 16, 512}, 2.6 + rounds(16) * (experts ? 0.6 + 0.74 * k : 0.8 + 0.98 * k));
   }

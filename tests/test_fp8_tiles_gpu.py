@@ -59,8 +59,8 @@ DENSE = [  # kernel, kind, M, N, K
     ("tile_256x256_fp8", "bf16", 2304, 2560, 384), ("tile_256x256_fp8", "fp16", 2177, 2433, 129),
     ("tile_128x128_bf16", "fp32", 1300, 2100, 260), ("tile_128x128_bf16", "fp32", 700, 3001, 640),
     ("tile_128x128_bf16", "fp32", 257, 8200, 900), ("tile_192x128_bf16", "fp32", 2100, 2200, 400),
-    ("rows_64_bf16", "fp32", 450, 1030, 2000), ("rows_64_bf16", "fp32", 400, 2050, 1000),
-    ("rows_64_bf16", "bf16", 520, 640, 3990), ("rows_32_bf16", "fp16", 300, 300, 8100),
+    ("rows_64_bf16", "fp32", 450, 500, 2000), ("rows_64_bf16", "fp32", 200, 1020, 1000),
+    ("rows_64_bf16", "bf16", 505, 500, 3990), ("rows_32_bf16", "fp16", 300, 300, 8100),
     ("staged_128x128_bf16", "bf16", 300, 260, 10), ("staged_128x128_bf16", "fp16", 129, 257, 15)]
 
 
