@@ -471,16 +471,19 @@ __global__ void __launch_bounds__(1024) plan_group_kernel(PlanArgs p) {
     }
   };
   load(from);
+  __syncthreads();
   for (int run = from; run < to; ++run) {
-    __syncthreads();
     for (int e = t; e < width; e += 1024) p.counts[(int64_t)run * width + e] = count[e];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (expert[i] >= 0) atomicAdd(&count[expert[i]], 1);
     if (run + 1 < to) load(run + 1);
+    // The additions are done before the barrier: with the barrier at the loop's
+    // head, the compiler has left out its wait for them.
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __syncthreads();
   }
-  __syncthreads();
   for (int e = t; e < width; e += 1024) group_counts(p, blockIdx.x)[e] = count[e];
 }
 

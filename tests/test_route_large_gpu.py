@@ -86,3 +86,15 @@ def test_plan_of_many_runs_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(got, sg.route_plan(ids, 256)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens,experts", [(262144, 64), (70001, 256)])
+def test_plan_of_one_experts_many_runs_repeats(tokens, experts):
+    """All additions to one counter, which take longest: every run sees those of the runs before it, each time."""
+    ids = torch.full((tokens, 8), experts - 1, dtype=torch.int32, device="cuda")
+    want = torch.arange(tokens * 8, dtype=torch.int32, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        _, rows, place = sg.route_plan(ids, experts)
+        wrong += (place.flatten() != want).sum() + (rows != want // 8).sum()
+    assert int(wrong) == 0
