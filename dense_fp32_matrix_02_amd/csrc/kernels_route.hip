@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteArgs a) {
   }
   double d = id < 0 || total == 0.0 ? 0.0 : (double)a.scale * (dw - dot / total) / total;
   if constexpr (SCORE == SGEMM_MI355_SIGMOID) d = d * w * rest;
-  // Through LDS to the lanes that hold the experts (8192 tokens, 8 of 256: 6.1 us;
+  // Through LDS to the lanes that hold the experts (8192 tokens, 8 of 256: 6.4 us;
   // 8.5 with every choice compared with all experts). Experts that are chosen
   // more than once are found first, and added up in the choices' order.
   double ds[V] = {};
@@ -633,8 +633,8 @@ __global__ void __launch_bounds__(1024) plan_place_kernel(PlanArgs p) {
 // Bound by the bytes of Z and dZ. A place and a weight are the same for a whole
 // wave, so they are scalars; forward, 4 rows of Z are asked for at once. Z is
 // read and Y and dZ are written past the caches (each once). 4096 tokens of 8
-// choices of 4096 bf16 columns: 51 us forward (5.7 TB/s) and 113 back (5.0
-// TB/s, as a copy). Back with a token to a workgroup, 2 of its rows at a time,
+// choices of 4096 bf16 columns: 51 us forward (5.7 TB/s) and 115 back (4.9
+// TB/s; 111 without the search for rows that have no name). Back with a token to a workgroup, 2 of its rows at a time,
 // 121 (512 columns, 16384 tokens: 127, here 59); with 2, 4, 8 pieces of a row at
 // once 117, 118, 151: their registers leave fewer waves. Few tokens of long
 // rows are slower this way (8 of 2 choices, 16384 columns: 16.5 us, 13.6).

@@ -70,7 +70,8 @@ int sgemm_mi355_route_backward(int type, int tokens, int experts, const void *lo
  *   place (tokens x choices ints): the row of each entry.
  * Entries whose id is outside 0 .. experts-1 come last, after
  * offsets[experts], in their order; the experts' products make their rows
- * zero. `workspace`: device memory of
+ * zero. One to three kernels, whose work grows with the entries. `workspace`:
+ * device memory of
  * sgemm_mi355_route_plan_workspace_size(tokens, choices, experts) bytes, 4-byte
  * aligned (null where that is 0), free again once the work is done.
  */
