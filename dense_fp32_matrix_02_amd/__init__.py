@@ -25,6 +25,12 @@ from ._fp8 import (  # noqa: F401
     gemm_fp8_experts, gemm_fp8_experts_wgrad, quantize_fp8, quantize_fp8_cols, sgemm_mi355_fp8_gemm,
     sgemm_mi355_fp8_gemm_experts, sgemm_mi355_fp8_gemm_experts_wgrad, sgemm_mi355_fp8_kernel_name,
     sgemm_mi355_fp8_quantize_cols, sgemm_mi355_fp8_quantize_rows, sgemm_mi355_fp8_quantize_tiles)
+from ._layer import (  # noqa: F401
+    GELU, GELU_TANH, MAX_NORM_COLS, NONE, RELU, SILU, epilogue_backward, gated, gated_backward, gated_fp8,
+    gemm_fp8_epilogue, rms_norm, rms_norm_backward, rms_norm_fp8, sgemm_mi355_epilogue_backward,
+    sgemm_mi355_epilogue_backward_workspace_size, sgemm_mi355_fp8_gemm_epilogue, sgemm_mi355_gated,
+    sgemm_mi355_gated_backward, sgemm_mi355_rms_norm, sgemm_mi355_rms_norm_backward,
+    sgemm_mi355_rms_norm_backward_workspace_size)
 from ._route import (  # noqa: F401
     MAX_CHOICES, MAX_EXPERTS, SIGMOID, SOFTMAX, route, route_backward, route_combine, route_combine_backward,
     route_plan, sgemm_mi355_route, sgemm_mi355_route_backward, sgemm_mi355_route_combine,

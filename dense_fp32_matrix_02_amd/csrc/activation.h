@@ -1,0 +1,119 @@
+// Activations and their slopes in FP32.
+#pragma once
+
+#include "fp8_internal.h"
+
+namespace sgemm_impl {
+namespace {
+
+// exp(x + lo) for x <= 0, |lo| << 1: the exponent in base 2 as a rounded product
+// and what its rounding lost, which enters as a factor 1 + r ln 2. Without it the
+// result would be off by |x| half-units in the last place. Below -104 the result is zero.
+__device__ __forceinline__ float exp_below(float x, float lo) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+  x = fmaxf(x, -104.0f);
+  const float t = x * kLog2e;
+  const float r = __builtin_fmaf(x, kLog2e, -t) + __builtin_fmaf(x, kLog2eLow, lo * kLog2e);
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * kLn2, e);
+}
+
+// s = 1 / (1 + exp(-x)) and c = 1 - s, each without a difference of like numbers.
+__device__ __forceinline__ void sigmoid(float x, float& s, float& c) {
+  const float e = exp_below(-fabsf(x), 0.0f);
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  s = x < 0.0f ? e * r : r;
+  c = x < 0.0f ? r : e * r;
+}
+
+// The normal distribution's integral up to p, and its density at p, for |p| up to 20. With
+// x = |p|: Phi(-x) = exp(-x^2/2) f(1 / (1 + 0.26 x)), f(t) t times a polynomial
+// fitted to erfc(x / sqrt 2) exp(x^2/2) / 2 on 0 <= x <= 14.5 for the least
+// relative error, 2.8e-8 (beyond, the exponential is zero).
+__device__ __forceinline__ void normal(float p, float& below, float& density) {
+  const float x = fabsf(p);
+  const float h = -0.5f * x * x;
+  const float e = exp_below(h, __builtin_fmaf(-0.5f * x, x, -h));
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.26f, x, 1.0f));
+  float f = 0.030230301335811942f;
+  f = __builtin_fmaf(f, t, -0.15149443888002528f);
+  f = __builtin_fmaf(f, t, 0.24873321057962977f);
+  f = __builtin_fmaf(f, t, -0.1477893502468334f);
+  f = __builtin_fmaf(f, t, 0.15875876440857434f);
+  f = __builtin_fmaf(f, t, 0.05196482062752984f);
+  f = __builtin_fmaf(f, t, 0.10278868211470069f);
+  f = __builtin_fmaf(f, t, 0.10305097391778659f);
+  f = __builtin_fmaf(f, t, 0.10375702210377379f);
+  const float tail = e * (f * t);
+  below = p < 0.0f ? tail : 1.0f - tail;
+  density = 0.3989422804014327f * e;
+}
+
+// p within -most .. most; a NaN stays one.
+__device__ __forceinline__ float within(float p, float most) { return p < -most ? -most : p > most ? most : p; }
+
+// Twice sqrt(2/pi), and the cubic term's share, of GELU's tanh form.
+constexpr float kTwoA = 1.5957691216057308f, kB = 0.044715f;
+
+// value = act(p) and slope = act'(p), at the infinities their limits; a NaN
+// gives NaN. Beyond the bounds below s, or Phi, is 0 or 1 to the last bit and
+// the other factor is cut, so that no infinity meets a zero.
+template <int ACT>
+__device__ __forceinline__ void activation(float p, float& value, float& slope) {
+  if constexpr (ACT == SGEMM_MI355_NONE) {
+    value = p, slope = 1.0f;
+  } else if constexpr (ACT == SGEMM_MI355_RELU) {
+    value = p <= 0.0f ? 0.0f : p;
+    slope = p <= 0.0f ? 0.0f : p > 0.0f ? 1.0f : p;
+  } else if constexpr (ACT == SGEMM_MI355_SILU) {
+    const float q = within(p, 104.0f);
+    float s, c;
+    sigmoid(q, s, c);
+    value = (p > 0.0f ? p : q) * s;
+    slope = __builtin_fmaf(q * c, s, s);  // s (1 + p (1 - s))
+  } else if constexpr (ACT == SGEMM_MI355_GELU) {
+    const float q = within(p, 20.0f);
+    float below, density;
+    normal(q, below, density);
+    value = (p > 0.0f ? p : q) * below;
+    slope = __builtin_fmaf(q, density, below);
+  } else {
+    // p s with s = sigmoid(2 u), u = sqrt(2/pi) (p + 0.044715 p^3)
+    const float q = within(p, 12.0f), q2 = q * q;
+    float s, c;
+    sigmoid(kTwoA * q * __builtin_fmaf(kB, q2, 1.0f), s, c);
+    value = (p > 0.0f ? p : q) * s;
+    slope = __builtin_fmaf(q * c * (kTwoA * __builtin_fmaf(3.0f * kB, q2, 1.0f)), s, s);
+  }
+}
+
+// The values of W arguments of an activation that the whole launch shares, in
+// little code: it is fetched once for each tile of a product. SiLU and the tanh
+// form of GELU are one expression, p sigmoid(a p + b p^3), with other numbers.
+template <int W>
+__device__ __forceinline__ void activate(int act, float (&v)[W]) {
+  if (act == SGEMM_MI355_SILU || act == SGEMM_MI355_GELU_TANH) {
+    const bool tanh = act == SGEMM_MI355_GELU_TANH;
+    const float most = tanh ? 12.0f : 104.0f, a = tanh ? kTwoA : 1.0f, b = tanh ? kB : 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float p = v[i], q = within(p, most);
+      float s, c;
+      sigmoid(a * q * __builtin_fmaf(b, q * q, 1.0f), s, c);
+      v[i] = (p > 0.0f ? p : q) * s;
+    }
+  } else if (act == SGEMM_MI355_GELU) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      float value, slope;
+      activation<SGEMM_MI355_GELU>(v[i], value, slope);
+      v[i] = value;
+    }
+  } else if (act == SGEMM_MI355_RELU) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = v[i] <= 0.0f ? 0.0f : v[i];
+  }
+}
+
+}  // namespace
+}  // namespace sgemm_impl

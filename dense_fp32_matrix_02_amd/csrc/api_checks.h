@@ -62,7 +62,7 @@ class Matrices {
     bool output;
   };
   void add(const void* p, Bytes bytes, int align, bool output) { m_[n_++] = Matrix{p, bytes, (unsigned)align, output}; }
-  Matrix m_[8];
+  Matrix m_[10];
   int n_ = 0;
 };
 

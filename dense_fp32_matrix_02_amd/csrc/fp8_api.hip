@@ -51,11 +51,14 @@ bool fp32_sums(int type) { return type_of_c(type) == SGEMM_MI355_F32 || (type & 
 
 int check_product(const Fp8Args& g, Fp8Form form, int64_t p, int64_t groups) {
   if (!known_type(g.type)) return SGEMM_MI355_ERR_TYPE;
-  if (g.sb_rows != 1 && g.sb_rows != 128) return SGEMM_MI355_ERR_OP;
-  if (g.M < 0 || g.N < 0 || g.K < 0 || (form != FP8_DENSE && g.experts < 1)) return SGEMM_MI355_ERR_DIM;
+  if ((g.sb_rows != 1 && g.sb_rows != 128) || g.act < SGEMM_MI355_NONE || g.act > SGEMM_MI355_GELU_TANH)
+    return SGEMM_MI355_ERR_OP;
+  if (g.M < 0 || g.N < 0 || g.K < 0 || ((form == FP8_EXPERTS || form == FP8_WGRAD) && g.experts < 1)) return SGEMM_MI355_ERR_DIM;
   if (g.M > kMostRows || g.N > kMostRows || g.K > kMostRows || p > kMostRows) return SGEMM_MI355_ERR_EXTENT;
   const int least = at_least_1((int)p);
-  if (g.lda < least || g.ldb < least || g.ldc < at_least_1(g.N)) return SGEMM_MI355_ERR_LD;
+  if (g.lda < least || g.ldb < least || g.ldc < at_least_1(g.N) || (g.residual != nullptr && g.ldr < at_least_1(g.N)) ||
+      (g.P != nullptr && g.ldp < at_least_1(g.N)))
+    return SGEMM_MI355_ERR_LD;
   if (g.sa_row < 0 || g.sa_block < 0 || g.sb_row < 0 || g.sb_block < 0 || g.strideB < 0 || g.stride_sb < 0)
     return SGEMM_MI355_ERR_STRIDE;
   if (g.strideC < 0 || (form == FP8_WGRAD && groups > 1 && g.M > 0 && g.N > 0 &&
@@ -70,7 +73,11 @@ int check_product(const Fp8Args& g, Fp8Form form, int64_t p, int64_t groups) {
   m.strided(g.SA, 1, 0, g.M, g.sa_row, blocks, g.sa_block, 4, false);
   m.strided(g.B, p > 0 ? experts : 0, g.strideB, g.N, g.ldb, p, 1, 1, false);
   m.strided(g.SB, experts, g.stride_sb, sb_rows, g.sb_row, blocks, g.sb_block, 4, false);
-  if (form != FP8_DENSE) m.dense(g.offsets, 1, (int64_t)g.experts + 1, g.experts, 4, false);
+  if (form == FP8_EXPERTS || form == FP8_WGRAD) m.dense(g.offsets, 1, (int64_t)g.experts + 1, g.experts, 4, false);
+  if (g.bias != nullptr) m.dense(g.bias, 1, g.N, g.N, 4, false);
+  if (g.residual != nullptr && (g.residual != g.C || g.ldr != g.ldc))  // in the place of C it is one matrix
+    m.dense(g.residual, g.M, g.N, g.ldr, element_size(g.type), false);
+  if (g.P != nullptr) m.dense(g.P, g.M, g.N, g.ldp, element_size(g.type), true);
   const int64_t results = form == FP8_WGRAD ? groups : 1;
   m.strided(g.C, results, g.strideC, g.M, g.ldc, g.N, 1, element_size(g.type), true);
   return m.check();
@@ -127,6 +134,19 @@ int sgemm_mi355_fp8_gemm(int type, int M, int N, int K, const unsigned char* A, 
   if (v != SGEMM_MI355_OK || M == 0 || N == 0) return v;
   if (!fp8_launchable(FP8_DENSE, g)) return SGEMM_MI355_ERR_EXTENT;
   return done(launch_fp8_gemm(FP8_DENSE, g, stream));
+}
+
+int sgemm_mi355_fp8_gemm_epilogue(int type, int M, int N, int K, const unsigned char* A, int lda, const float* SA,
+                                  long long sa_row, long long sa_block, const unsigned char* B, int ldb, const float* SB,
+                                  long long sb_row, long long sb_block, int sb_rows, const float* bias, int act,
+                                  const void* residual, int ldr, void* P, int ldp, void* C, int ldc, hipStream_t stream) {
+  Fp8Args g{type_of_c(type), M, N, K, A, lda, SA, sa_row, sa_block, B, ldb, 0, SB, sb_row, sb_block, 0, sb_rows,
+            nullptr, 0, 0.0f, C, ldc, 0, fp32_sums(type)};
+  g.bias = bias, g.act = act, g.residual = residual, g.ldr = ldr, g.P = P, g.ldp = ldp;
+  const int v = check_product(g, FP8_EPILOGUE, K, 1);
+  if (v != SGEMM_MI355_OK || M == 0 || N == 0) return v;
+  if (!fp8_launchable(FP8_EPILOGUE, g)) return SGEMM_MI355_ERR_EXTENT;
+  return done(launch_fp8_gemm(FP8_EPILOGUE, g, stream));
 }
 
 int sgemm_mi355_fp8_gemm_experts(int type, int rows, int N, int K, int experts, const unsigned char* A, int lda,

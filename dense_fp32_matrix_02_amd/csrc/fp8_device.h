@@ -1,7 +1,7 @@
 // Device code shared by the FP8 product kernels.
 #pragma once
 
-#include "fp8_internal.h"
+#include "activation.h"
 
 namespace sgemm_impl {
 namespace {
@@ -123,6 +123,48 @@ __device__ __forceinline__ void store_c(const Fp8Args& g, void* C, int64_t at, i
   if (g.type == SGEMM_MI355_F32) store_as((float*)C + at, valid, v, g.beta);
   else if (g.type == SGEMM_MI355_BF16) store_as((__hip_bfloat16*)C + at, valid, v, g.beta);
   else store_as((__half*)C + at, valid, v, g.beta);
+}
+
+// The epilogue of W neighbours (m, n) .. of C, `valid` of which exist: v holds
+// the products' sums, r the residual's values (zeros without one).
+template <class T, int W>
+__device__ __forceinline__ void finish_as(const Fp8Args& g, int64_t m, int n, int valid, const float (&bias)[W],
+                                          const float (&r)[W], float (&v)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] += bias[i];
+  if (g.P != nullptr) store_as<T, W>((T*)g.P + m * g.ldp + n, valid, v, 0.0f);
+  activate(g.act, v);
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] += r[i];
+  store_as<T, W>((T*)g.C + m * g.ldc + n, valid, v, 0.0f);
+}
+// `valid` of W values at p as FP32, zeros for the others and without a p.
+template <class T, int W>
+__device__ __forceinline__ void load_as(const T* p, bool there, int valid, float (&v)[W]) {
+  if (there && valid >= W) {
+    T e[W];
+    __builtin_memcpy(e, p, sizeof(e));
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = there && i < valid ? to_f32(p[i]) : 0.0f;
+  }
+}
+// The same for one run of values of a lane, with its loads.
+template <int W>
+__device__ __forceinline__ void finish_c(const Fp8Args& g, int64_t m, int n, float (&v)[W]) {
+  const int valid = g.N - n;
+  float bias[W], r[W];
+  load_as(g.bias + n, g.bias != nullptr, valid, bias);
+  auto as = [&](auto t) __attribute__((always_inline)) {
+    using T = decltype(t);
+    load_as((const T*)g.residual + m * g.ldr + n, g.residual != nullptr, valid, r);
+    finish_as<T>(g, m, n, valid, bias, r, v);
+  };
+  if (g.type == SGEMM_MI355_F32) as(float{});
+  else if (g.type == SGEMM_MI355_BF16) as(__hip_bfloat16{});
+  else as(__half{});
 }
 
 // The experts' tiles of BM rows, numbered expert by expert and then those of

@@ -33,8 +33,9 @@ hipError_t launch_quantize_tiles(int type, const QuantArgs& q, hipStream_t s);
 
 // One FP8 product, or one for each expert. DENSE: C = A.B^T + beta*C. EXPERTS:
 // rows of A and C belong to experts by `offsets`, B_e = B + e*strideB.
-// WGRAD: the summed axis belongs to experts, C_e = C + e*strideC.
-enum Fp8Form { FP8_DENSE = 0, FP8_EXPERTS = 1, FP8_WGRAD = 2 };
+// WGRAD: the summed axis belongs to experts, C_e = C + e*strideC. EPILOGUE:
+// C = act(p) + residual with p = A.B^T + bias.
+enum Fp8Form { FP8_DENSE = 0, FP8_EXPERTS = 1, FP8_WGRAD = 2, FP8_EPILOGUE = 3 };
 
 struct Fp8Args {
   int type, M, N, K;  // WGRAD: K = the rows that offsets count
@@ -53,6 +54,13 @@ struct Fp8Args {
   void* C;
   int64_t ldc, strideC;
   bool wide;  // block sums have to be FP32 sums: C is FP32, or the caller asks for it
+  // EPILOGUE
+  const float* bias;  // null: none
+  int act;
+  const void* residual;  // null: none
+  int64_t ldr;
+  void* P;  // p in C's type; null: not asked for
+  int64_t ldp;
 };
 
 hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s);
@@ -151,6 +159,23 @@ inline hipError_t by_type(int type, F&& f) {
     case SGEMM_MI355_F32: return f(float{});
     case SGEMM_MI355_BF16: return f(__hip_bfloat16{});
     default: return f(__half{});
+  }
+}
+
+// A number as a type, for templates that a lambda picks.
+template <int A>
+struct Act {
+  static constexpr int value = A;
+};
+// f(Act) for the activation.
+template <class F>
+inline hipError_t by_act(int act, F&& f) {
+  switch (act) {
+    case SGEMM_MI355_NONE: return f(Act<SGEMM_MI355_NONE>{});
+    case SGEMM_MI355_RELU: return f(Act<SGEMM_MI355_RELU>{});
+    case SGEMM_MI355_SILU: return f(Act<SGEMM_MI355_SILU>{});
+    case SGEMM_MI355_GELU: return f(Act<SGEMM_MI355_GELU>{});
+    default: return f(Act<SGEMM_MI355_GELU_TANH>{});
   }
 }
 

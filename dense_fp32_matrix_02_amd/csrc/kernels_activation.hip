@@ -1,0 +1,196 @@
+// Gated activations into e4m3, their backward pass, the backward pass of a
+// product's epilogue, and sums of columns. Bound by the bytes read and written.
+
+#include "activation.h"
+#include "fp8_quantize.h"
+#include "layer_internal.h"
+
+namespace sgemm_impl {
+namespace {
+
+// z = act(g) u of H = [g | u]. Sixteen lanes hold one block of 128 of a row of
+// z, eight values each.
+template <class T, int ACT>
+__global__ void __launch_bounds__(256) gated_kernel(GatedArgs a) {
+  const uint32_t blocks = (uint32_t)(a.cols + kBlock - 1) / kBlock;
+  const uint64_t group = (uint64_t)blockIdx.x * 16 + threadIdx.x / 16;
+  if (group >= (uint64_t)blocks * (uint32_t)a.rows) return;  // the same for all 16 lanes of a block
+  const uint32_t row = (uint32_t)group / blocks, b = (uint32_t)group - row * blocks;
+  const int col = (int)(b * kBlock) + 8 * (threadIdx.x % 16), valid = a.cols - col;
+  const T* h = (const T*)a.H + row * a.ldh + col;
+  float g[8], z[8];
+  load8(h, valid, g);
+  load8(h + a.cols, valid, z);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float value, slope;
+    activation<ACT>(g[i], value, slope);
+    z[i] *= value;
+    m = max(m, i < valid ? mag(z[i]) : 0u);
+  }
+  if (a.Z != nullptr) store8((T*)a.Z + row * a.ldz + col, valid, z);
+  if (a.Q == nullptr) return;
+#pragma unroll
+  for (int d = 1; d < 16; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+  const float s = scale_of(m);
+  store_bytes(a.Q + row * a.ldq + col, quantize8(z, s), valid);
+  if (threadIdx.x % 16 == 0) a.S[row * a.s_row + b * a.s_block] = s;
+}
+
+// dg = act'(g) u dz and du = act(g) dz: eight neighbours of a row of z per thread.
+template <class T, int ACT>
+__global__ void __launch_bounds__(256) gated_backward_kernel(GatedArgs a) {
+  const uint32_t chunks = (uint32_t)(a.cols + 7) / 8;
+  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (uint64_t)chunks * (uint32_t)a.rows) return;
+  const uint32_t row = (uint32_t)id / chunks;
+  const int col = (int)(8 * ((uint32_t)id - row * chunks)), valid = a.cols - col;
+  const T* h = (const T*)a.H + row * a.ldh + col;
+  float g[8], u[8], dz[8];
+  load8(h, valid, g);
+  load8(h + a.cols, valid, u);
+  load8((const T*)a.dZ + row * a.lddz + col, valid, dz);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float value, slope;
+    activation<ACT>(g[i], value, slope);
+    g[i] = slope * u[i] * dz[i];
+    u[i] = value * dz[i];
+  }
+  T* d = (T*)a.dH + row * a.lddh + col;
+  store8(d, valid, g);
+  store8(d + a.cols, valid, u);
+}
+
+// dp = act'(p) dc, and its sum over a group's rows. A workgroup has 8*LANES
+// columns of one group: LANES threads side by side, 256/LANES rows at a time;
+// these threads' sums are added in their order.
+template <class T, int ACT, int LANES>
+__global__ void __launch_bounds__(256) epilogue_backward_kernel(EpilogueBackArgs a) {
+  constexpr int ROWS = 256 / LANES;
+  __shared__ __align__(16) float part[ROWS][8 * LANES];
+  const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
+  const int strips = (a.cols + 8 * LANES - 1) / (8 * LANES);
+  const int group = blockIdx.x / strips;
+  const int col = 8 * ((blockIdx.x - group * strips) * LANES + lane), valid = a.cols - col;
+  const int64_t first = (int64_t)group * a.per, end = min((int64_t)a.rows, first + a.per);
+  float sum[8] = {};
+  if (valid > 0) {
+#pragma unroll 2
+    for (int64_t row = first + team; row < end; row += ROWS) {
+      float p[8], d[8];
+      load8((const T*)a.P + row * a.ldp + col, valid, p);
+      load8((const T*)a.dC + row * a.lddc + col, valid, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float value, slope;
+        activation<ACT>(p[i], value, slope);
+        d[i] *= slope;
+        sum[i] += d[i];
+      }
+      store8((T*)a.dP + row * a.lddp + col, valid, d);
+    }
+  }
+  if (a.sums == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[team][8 * lane + i] = sum[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 8 * LANES; c += 256) {
+    const int at = 8 * LANES * (blockIdx.x - group * strips) + c;
+    float total = 0.0f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) total += part[r][c];
+    if (at < a.cols) a.sums[(int64_t)group * a.cols + at] = total;
+  }
+}
+
+// out[c] = sum over the groups of P[group][c], in an order that depends on the
+// number of groups alone. A workgroup has 64 columns: 16 threads side by side,
+// 16 groups at a time.
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* P, int groups, int cols, float* out) {
+  __shared__ __align__(16) float part[16][64];
+  const int lane = threadIdx.x % 16, team = threadIdx.x / 16;
+  const int col = blockIdx.x * 64 + 4 * lane;
+  float sum[4] = {};
+  if (col + 4 <= cols) {
+#pragma unroll 4
+    for (int g = team; g < groups; g += 16) {
+      float v[4];
+      __builtin_memcpy(v, P + (int64_t)g * cols + col, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += v[i];
+    }
+  } else {
+    for (int g = team; g < groups; g += 16)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < cols) sum[i] += P[(int64_t)g * cols + col + i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[team][4 * lane + i] = sum[i];
+  __syncthreads();
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && c < cols) {
+    float total = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) total += part[t][threadIdx.x];
+    out[c] = total;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_column_sums(const float* sums, int groups, int cols, float* out, hipStream_t s) {
+  void* args[] = {&sums, &groups, &cols, &out};
+  return hipLaunchKernel((const void*)&column_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), args, 0, s);
+}
+
+hipError_t launch_gated(int type, int act, const GatedArgs& a, hipStream_t s) {
+  const int64_t groups = (int64_t)((a.cols + kBlock - 1) / kBlock) * a.rows;
+  return by_type(type, [&](auto t) {
+    return by_act(act, [&](auto f) {
+      return launch_with((const void*)&gated_kernel<decltype(t), decltype(f)::value>, dim3((unsigned)((groups + 15) / 16)),
+                         dim3(256), a, s);
+    });
+  });
+}
+
+hipError_t launch_gated_backward(int type, int act, const GatedArgs& a, hipStream_t s) {
+  const int64_t chunks = (int64_t)((a.cols + 7) / 8) * a.rows;
+  return by_type(type, [&](auto t) {
+    return by_act(act, [&](auto f) {
+      return launch_with((const void*)&gated_backward_kernel<decltype(t), decltype(f)::value>,
+                         dim3((unsigned)((chunks + 255) / 256)), dim3(256), a, s);
+    });
+  });
+}
+
+namespace {
+constexpr int kNarrow = 128;  // columns up to which sixteen threads share a row
+int strips_of(int cols) { return cols <= kNarrow ? 1 : (cols + 511) / 512; }
+}  // namespace
+
+void epilogue_groups(int rows, int cols, EpilogueBackArgs& a) {
+  const int64_t wanted = 2048 / strips_of(cols) > 1 ? 2048 / strips_of(cols) : 1;
+  const int least = cols <= kNarrow ? 64 : 32;  // rows of a group: some for each thread
+  const int64_t per = ((int64_t)rows + wanted - 1) / wanted;
+  a.per = per > least ? (int)per : least;
+  a.groups = (int)(((int64_t)rows + a.per - 1) / a.per);
+}
+
+hipError_t launch_epilogue_backward(int type, int act, const EpilogueBackArgs& a, float* dbias, hipStream_t s) {
+  const hipError_t e = by_type(type, [&](auto t) {
+    return by_act(act, [&](auto f) {
+      using T = decltype(t);
+      constexpr int ACT = decltype(f)::value;
+      return launch_with(a.cols <= kNarrow ? (const void*)&epilogue_backward_kernel<T, ACT, 16>
+                                           : (const void*)&epilogue_backward_kernel<T, ACT, 64>,
+                         dim3((unsigned)(a.groups * strips_of(a.cols))), dim3(256), a, s);
+    });
+  });
+  if (e != hipSuccess || a.sums == nullptr || a.groups == 1) return e;
+  return launch_column_sums(a.sums, a.groups, a.cols, dbias, s);
+}
+
+}  // namespace sgemm_impl

@@ -105,6 +105,33 @@ __global__ void __launch_bounds__(256) fp8_gemm_kernel(Fp8Args g) {
         }
       }
   }
+  if constexpr (FORM == FP8_EPILOGUE) {
+    // By way of LDS, 32 rows of the wave at a time, so that the epilogue is a
+    // loop's body and not a copy for each of the lane's 16 runs of values.
+    float* out = (float*)lds + wave * (32 * 64);
+    __syncthreads();  // all reads of the slab have been made
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(f32x4*)(out + l32 * 64 + 4 * ((8 * j + 2 * q + h) ^ (l32 % 16))) =
+              f32x4{acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+      __builtin_amdgcn_wave_barrier();  // LDS serves a wave in order
+      const int c = lane % 16, n = t.n0 + wn + 4 * c;
+#pragma unroll 1
+      for (int r = lane / 16; r < 32; r += 4) {
+        const int m = t.m0 + wm + 32 * i + r;
+        if (m >= t.rows_a) break;
+        float v[4];
+        *(f32x4*)v = *(const f32x4*)(out + r * 64 + 4 * (c ^ (r % 16)));
+        finish_c(g, m, n, v);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = t.m0 + wm + 32 * i + l32;
@@ -172,7 +199,7 @@ Choice choose(Fp8Form form, const Fp8Args& g) {
   // tiles do not, so that some CUs would work on two (N 4096, K 2048, fp32: M
   // 1536 33.3 us against 37.6; else they are slower: M 768 30.2 against 26.4,
   // M 2304 56.8 against 55.3).
-  if (wide && form == FP8_DENSE && groups(192, 128) <= 1.0) offer({Choice::TILE, wide, 192, 128, 512}, 8.0 + 12.6 * k + tail);
+  if (wide && (form == FP8_DENSE || form == FP8_EPILOGUE) && groups(192, 128) <= 1.0) offer({Choice::TILE, wide, 192, 128, 512}, 8.0 + 12.6 * k + tail);
   if (!wide) {
     const double r = groups(256, 256);
     offer({Choice::TILE, wide, 256, 256, 512},
@@ -212,6 +239,7 @@ hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s) {
                        : c.kernel == Choice::SKINNY ? fp8_skinny_kernel_for(form, g.sb_rows == kBlock, c.bm)
                        : form == FP8_EXPERTS        ? (const void*)&fp8_gemm_kernel<FP8_EXPERTS>
                        : form == FP8_WGRAD          ? (const void*)&fp8_gemm_kernel<FP8_WGRAD>
+                       : form == FP8_EPILOGUE       ? (const void*)&fp8_gemm_kernel<FP8_EPILOGUE>
                                                     : (const void*)&fp8_gemm_kernel<FP8_DENSE>;
   return launch_with(kernel, grid, dim3((unsigned)c.threads), g, s);
 }

@@ -108,8 +108,10 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves, MF == 4 ? 2 : MF == 1 ? 6 :
 #pragma unroll
     for (int w = 1; w < NW; ++w) sum += part[w][wave][lane];
     const int m = t.m0 + 16 * wave + r16, n = t.n0 + 4 * quad;
-    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    if (m < t.rows_a) store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if (m >= t.rows_a) return;
+    if constexpr (FORM == FP8_EPILOGUE) finish_c(g, m, n, v);
+    else store_c(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
   }
 }
 
@@ -117,6 +119,8 @@ template <int MF>
 const void* of_width(Fp8Form form, bool tall) {
   if (form == FP8_EXPERTS)
     return tall ? (const void*)&fp8_skinny_kernel<FP8_EXPERTS, true, MF> : (const void*)&fp8_skinny_kernel<FP8_EXPERTS, false, MF>;
+  if (form == FP8_EPILOGUE)
+    return tall ? (const void*)&fp8_skinny_kernel<FP8_EPILOGUE, true, MF> : (const void*)&fp8_skinny_kernel<FP8_EPILOGUE, false, MF>;
   return tall ? (const void*)&fp8_skinny_kernel<FP8_DENSE, true, MF> : (const void*)&fp8_skinny_kernel<FP8_DENSE, false, MF>;
 }
 

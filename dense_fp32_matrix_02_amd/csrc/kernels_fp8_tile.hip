@@ -299,7 +299,47 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
     const int64_t at = (int64_t)(t.m0 + wm + 16 * i0) * g.ldc + n;
     auto rows_to_c = [&](auto* C) __attribute__((always_inline)) {
       using T = std::remove_pointer_t<decltype(C)>;
-      if (g.beta == 0.0f && n + 8 <= g.N) {
+      if constexpr (FORM == FP8_EPILOGUE) {
+        // Rows by twos, the next two's residual asked for before these two are
+        // stored: past a store the compiler may not move a load (C can be the residual).
+        constexpr int APART = 64 / LANES;
+        const int64_t m = t.m0 + wm + 16 * i0;
+        struct alignas(sizeof(T)) Run {
+          T e[8];
+        };
+        auto ask = [&](int r) __attribute__((always_inline)) {
+          Run x = {};
+          const T* at = (const T*)g.residual + (m + r) * g.ldr + n;
+          if (g.residual != nullptr && r < rows) {
+            if (n + 8 <= g.N) {
+              __builtin_memcpy(&x, at, sizeof(x));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (n + i < g.N) x.e[i] = at[i];
+            }
+          }
+          return x;
+        };
+        float bias[8];
+        load_as(g.bias + n, g.bias != nullptr, g.N - n, bias);
+        int r0 = lane / LANES;
+        Run next[2] = {ask(r0), ask(r0 + APART)};
+#pragma unroll 1
+        for (; r0 < rows; r0 += 2 * APART) {
+          const Run now[2] = {next[0], next[1]};
+          next[0] = ask(r0 + 2 * APART), next[1] = ask(r0 + 3 * APART);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (r0 + u * APART >= rows) break;
+            float v[8], res[8];
+            strip(r0 + u * APART, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) res[i] = to_f32(now[u].e[i]);
+            finish_as<T>(g, m + r0 + u * APART, n, g.N - n, bias, res, v);
+          }
+        }
+      } else if (g.beta == 0.0f && n + 8 <= g.N) {
 #pragma unroll 4
         for (int r = lane / LANES; r < rows; r += 64 / LANES) {
           float v[8];
@@ -315,8 +355,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
         }
       }
     };
-    if (g.type == SGEMM_MI355_F32) rows_to_c((float*)t.C);
-    else if (g.type == SGEMM_MI355_BF16) rows_to_c((__hip_bfloat16*)t.C);
+    if (g.type == SGEMM_MI355_F32) {
+      if constexpr (WIDE || FORM != FP8_EPILOGUE) rows_to_c((float*)t.C);  // FP32 results have widened values
+    } else if (g.type == SGEMM_MI355_BF16) rows_to_c((__hip_bfloat16*)t.C);
     else rows_to_c((__half*)t.C);
     __builtin_amdgcn_wave_barrier();
   }
@@ -328,6 +369,9 @@ const void* of_shape(Fp8Form form, bool tall) {
   if (form == FP8_EXPERTS)
     return tall ? (const void*)&fp8_tile_kernel<FP8_EXPERTS, WIDE, true, BM, BN, WM, WN>
                 : (const void*)&fp8_tile_kernel<FP8_EXPERTS, WIDE, false, BM, BN, WM, WN>;
+  if (form == FP8_EPILOGUE)
+    return tall ? (const void*)&fp8_tile_kernel<FP8_EPILOGUE, WIDE, true, BM, BN, WM, WN>
+                : (const void*)&fp8_tile_kernel<FP8_EPILOGUE, WIDE, false, BM, BN, WM, WN>;
   return tall ? (const void*)&fp8_tile_kernel<FP8_DENSE, WIDE, true, BM, BN, WM, WN>
               : (const void*)&fp8_tile_kernel<FP8_DENSE, WIDE, false, BM, BN, WM, WN>;
 }
@@ -336,7 +380,10 @@ const void* of_shape(Fp8Form form, bool tall) {
 
 const void* fp8_tile_kernel_for(Fp8Form form, bool wide, bool tall, int bm) {
   if (bm == 256) return of_shape<false, 256, 256, 4, 2>(form, tall);
-  if (bm == 192)  // dense products into FP32 only
+  if (bm == 192 && form == FP8_EPILOGUE)
+    return tall ? (const void*)&fp8_tile_kernel<FP8_EPILOGUE, true, true, 192, 128, 4, 2>
+                : (const void*)&fp8_tile_kernel<FP8_EPILOGUE, true, false, 192, 128, 4, 2>;
+  if (bm == 192)  // single products with FP32 sums only
     return tall ? (const void*)&fp8_tile_kernel<FP8_DENSE, true, true, 192, 128, 4, 2>
                 : (const void*)&fp8_tile_kernel<FP8_DENSE, true, false, 192, 128, 4, 2>;
   return wide ? of_shape<true, 128, 128, 2, 2>(form, tall) : of_shape<false, 128, 128, 2, 2>(form, tall);

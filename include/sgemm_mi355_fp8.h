@@ -106,6 +106,28 @@ int sgemm_mi355_fp8_gemm(int type, int M, int N, int K,
                          const unsigned char *B, int ldb, const float *SB, long long sb_row, long long sb_block,
                          int sb_rows, float beta, void *C, int ldc, hipStream_t stream);
 
+/* Activations, with p in FP32; value and slope at an infinity are the limits there, at a NaN they are NaN (but NONE's slope, 1). */
+#define SGEMM_MI355_NONE 0      /* p */
+#define SGEMM_MI355_RELU 1      /* max(p, 0) */
+#define SGEMM_MI355_SILU 2      /* p / (1 + exp(-p)) */
+#define SGEMM_MI355_GELU 3      /* p * Phi(p), Phi the normal distribution's integral */
+#define SGEMM_MI355_GELU_TANH 4 /* p / 2 * (1 + tanh(sqrt(2/pi) * (p + 0.044715 p^3))) */
+
+/*
+ * The product with an epilogue:
+ *   p = A.B^T + bias,  C = act(p) + residual,
+ * p and act(p) in FP32 from the product's sums, C and (where it is asked for)
+ * P = p each rounded once to `type`. bias: N floats, or null. residual: M x N
+ * of `type`, or null; it may be C itself, at the same address and row stride.
+ * P: M x N of `type`, or null. Everything else is as in sgemm_mi355_fp8_gemm
+ * (K == 0 gives p = bias). SGEMM_MI355_ERR_OP: an unknown activation.
+ */
+int sgemm_mi355_fp8_gemm_epilogue(int type, int M, int N, int K,
+                                  const unsigned char *A, int lda, const float *SA, long long sa_row, long long sa_block,
+                                  const unsigned char *B, int ldb, const float *SB, long long sb_row, long long sb_block,
+                                  int sb_rows, const float *bias, int act, const void *residual, int ldr,
+                                  void *P, int ldp, void *C, int ldc, hipStream_t stream);
+
 /*
  * Experts: rows offsets[e] .. offsets[e+1]-1 of A (rows x K, sorted by
  * expert) meet B_e = B + e*strideB (N x K), with SB_e = SB + e*stride_sb:
