@@ -25,6 +25,10 @@ from ._fp8 import (  # noqa: F401
     gemm_fp8_experts, gemm_fp8_experts_wgrad, quantize_fp8, quantize_fp8_cols, sgemm_mi355_fp8_gemm,
     sgemm_mi355_fp8_gemm_experts, sgemm_mi355_fp8_gemm_experts_wgrad, sgemm_mi355_fp8_kernel_name,
     sgemm_mi355_fp8_quantize_cols, sgemm_mi355_fp8_quantize_rows, sgemm_mi355_fp8_quantize_tiles)
+from ._experts import (  # noqa: F401
+    EXPERTS_DGRAD, EXPERTS_FORWARD, EXPERTS_WGRAD, gemm_experts, gemm_experts_dgrad, gemm_experts_wgrad,
+    sgemm_mi355_experts_gemm, sgemm_mi355_experts_gemm_dgrad, sgemm_mi355_experts_gemm_wgrad,
+    sgemm_mi355_experts_kernel_name)
 from ._layer import (  # noqa: F401
     GELU, GELU_TANH, MAX_NORM_COLS, NONE, RELU, SILU, epilogue_backward, gated, gated_backward, gated_fp8,
     gemm_fp8_epilogue, rms_norm, rms_norm_backward, rms_norm_fp8, sgemm_mi355_epilogue_backward,

@@ -1,0 +1,154 @@
+// Device code shared by the kernels of the 16-bit experts' products.
+#pragma once
+
+#include "sgemm_internal.h"
+#include "experts_internal.h"
+#include "fp8_device.h"
+
+namespace sgemm_impl {
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kSlab = 64;  // values of the summed axis in a slab: 128 bytes of a row
+
+// 16 x 16 products over 32 values of the summed axis, added to c: a lane has
+// eight of them, of row l%16 of either operand; rows of the result are b's,
+// columns a's; lane l holds rows 4*(l/16) .. +3 of column l%16.
+template <class E>
+__device__ __forceinline__ f32x4 mfma16(i32x4 b, i32x4 a, f32x4 c) {
+  if constexpr (sizeof(E) == sizeof(__half) && __is_same(E, __half))
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ s16x4 read_transposed(const uint8_t* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+#else
+  return s16x4{};
+#endif
+}
+
+// An operand's part of a slab: BX rows (or, ACROSS, columns) of the tile.
+template <bool ACROSS_, int BX, int NW>
+struct Part {
+  static constexpr bool ACROSS = ACROSS_;
+  static constexpr int PITCH = ACROSS ? 2 * BX : 2 * kSlab;  // bytes of a row in LDS
+  static constexpr int REGIONS = BX / 8 / NW;                // 1 KiB direct loads per wave
+  static constexpr int LANES = PITCH / 16;                   // lanes that load a row
+  static constexpr int STEP = NW * 64 / LANES;               // rows from one of a wave's regions to its next
+  static_assert(BX % (8 * NW) == 0 && STEP % 16 == 0, "a lane's place in its row is the same in all its regions");
+
+  // Which of the groups of 32 bytes of row k of an ACROSS part lies where:
+  // group c at c ^ f(k). A transposed read takes 32 bytes of each of rows k ..
+  // k+3 and k+8 .. k+11 at once, which have to meet different banks.
+  static __device__ __forceinline__ int f(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+  // The row of its first region that a lane loads, and the bytes in it.
+  static __device__ __forceinline__ void source(int wave, int lane, int& row, int& bytes) {
+    row = wave * (64 / LANES) + lane / LANES;
+    const int c = lane % LANES;
+    bytes = 16 * (ACROSS ? c ^ (f(row) << 1) : swz(row, c));
+  }
+  // Where a lane reads its share of fragment 0 of the strip that begins at row
+  // (column) w0; fragment j is at this ^ (j << 5) (ACROSS) or + j * 16 * PITCH.
+  static __device__ __forceinline__ int place(int w0, int lane) {
+    const int r16 = lane % 16, quad = lane / 16;
+    if (!ACROSS) return (w0 + r16) * PITCH + 16 * swz(r16, quad);
+    return (8 * quad + r16 / 4) * PITCH + (((w0 / 16) ^ f(8 * quad + r16 / 4)) << 5) + 8 * (r16 % 4);
+  }
+  // Values 8*quad .. +7 of half x of the slab, of row l%16 of fragment j.
+  static __device__ __forceinline__ i32x4 read(const uint8_t* part, int place, int j, int x) {
+    if constexpr (!ACROSS) {
+      return *(const i32x4*)(part + ((place + j * 16 * PITCH) ^ (x * 64)));
+    } else {
+      const uint8_t* p = part + (place ^ (j << 5)) + 32 * x * PITCH;
+      const s16x4 lo = read_transposed(p), hi = read_transposed(p + 4 * PITCH);
+      i32x4 v;
+      __builtin_memcpy(&v, &lo, 8);
+      __builtin_memcpy((char*)&v + 8, &hi, 8);
+      return v;
+    }
+  }
+};
+
+// What one workgroup computes: a tile of one product. A and B begin with the
+// first row of their product; rows_a is an end in rows of A (FORWARD, DGRAD).
+struct ExpertsTile {
+  const uint8_t *A, *B;
+  int rows_a;
+  int m0, n0;
+  int K;
+  void* C;
+};
+
+template <int FORM, int BM, int BN>
+__device__ __forceinline__ bool find_experts_tile(const ExpertsArgs& g, ExpertsTile& t) {
+  const int tiles_n = (g.N + BN - 1) / BN;
+  t.A = (const uint8_t*)g.A, t.B = (const uint8_t*)g.B, t.C = g.C;
+  t.rows_a = g.M, t.K = g.K;
+  if constexpr (FORM == EXPERTS_WGRAD) {
+    int tm, tn, begin, end;
+    tile_coords(blockIdx.x, (g.M + BM - 1) / BM, tiles_n, 8, tm, tn);
+    t.m0 = tm * BM, t.n0 = tn * BN;
+    const int e = blockIdx.y;
+    expert_rows(g.offsets, e, g.K, begin, end);
+    t.K = end - begin;
+    t.A += 2 * (begin * g.lda), t.B += 2 * (begin * g.ldb);
+    t.C = (char*)g.C + e * g.strideC * (g.c_type == SGEMM_MI355_F32 ? 4 : 2);
+    return true;
+  } else {
+    const int lane = threadIdx.x % 64;
+    int begin, end, upto, total = 0, last_end = 0;
+    for (int e0 = 0; e0 < g.experts; e0 += 64) {
+      expert_tiles<BM>(g, e0, lane, begin, end, upto);
+      total += __builtin_amdgcn_readlane(upto, 63);
+      last_end = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
+    }
+    total += (g.M - last_end + BM - 1) / BM;
+    const int64_t tiles = (int64_t)total * tiles_n;
+    if (blockIdx.x >= tiles) return false;
+    const int64_t each = tiles / 8, more = tiles % 8, xcd = blockIdx.x % 8;
+    const int64_t id = xcd * each + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    const int tm = (int)(id / tiles_n);
+    t.n0 = (int)(id - (int64_t)tm * tiles_n) * BN;
+    int before = 0;
+    for (int e0 = 0; e0 < g.experts; e0 += 64) {
+      const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto);
+      const uint64_t past = __ballot(tm < before + upto);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        // The same in every lane: kept in scalar registers.
+        t.m0 = __builtin_amdgcn_readlane(begin, l) + (tm - before - __builtin_amdgcn_readlane(upto - own, l)) * BM;
+        t.rows_a = __builtin_amdgcn_readlane(end, l);
+        t.B += 2 * (e0 + l) * g.strideB;
+        return true;
+      }
+      before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    // Rows no expert has: a product over nothing.
+    t.m0 = last_end + (tm - before) * BM;
+    t.K = 0;
+    return t.m0 < g.M;
+  }
+}
+
+// `valid` of W neighbours of C at element `at`, added to beta * C.
+template <int W>
+__device__ __forceinline__ void store_experts(const ExpertsArgs& g, void* C, int64_t at, int valid, const float (&v)[W]) {
+  if (g.c_type == SGEMM_MI355_F32) store_as((float*)C + at, valid, v, g.beta);
+  else if (g.c_type == SGEMM_MI355_BF16) store_as((__hip_bfloat16*)C + at, valid, v, g.beta);
+  else store_as((__half*)C + at, valid, v, g.beta);
+}
+
+inline int64_t experts_grid(ExpertsForm form, const ExpertsArgs& g, int bm, int bn) {
+  const int64_t tiles_n = (g.N + bn - 1) / bn;
+  return tiles_n * (form == EXPERTS_WGRAD ? (int64_t)((g.M + bm - 1) / bm) : (int64_t)g.M / bm + g.experts + 1);
+}
+
+}  // namespace
+}  // namespace sgemm_impl

@@ -169,8 +169,8 @@ __device__ __forceinline__ void finish_c(const Fp8Args& g, int64_t m, int n, flo
 
 // The experts' tiles of BM rows, numbered expert by expert and then those of
 // the rows that no expert has. The wave counts 64 experts at a time.
-template <int BM>
-__device__ __forceinline__ int expert_tiles(const Fp8Args& g, int e0, int lane, int& begin, int& end, int& upto) {
+template <int BM, class Args>
+__device__ __forceinline__ int expert_tiles(const Args& g, int e0, int lane, int& begin, int& end, int& upto) {
   begin = 0, end = 0;
   if (e0 + lane < g.experts) expert_rows(g.offsets, e0 + lane, g.M, begin, end);
   const int own = (end - begin + BM - 1) / BM;

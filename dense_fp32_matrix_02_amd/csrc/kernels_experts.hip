@@ -1,0 +1,227 @@
+// Products by expert of 16-bit operands: the kernel for operands of any
+// alignment, the kernel for few rows, and the choice.
+
+#include <cmath>
+#include <type_traits>
+
+#include "experts_device.h"
+
+namespace sgemm_impl {
+namespace {
+
+// A 128 x 128 tile by four waves of 64 x 64: operands of any alignment. Slabs
+// come through registers, the next one on the way while one is multiplied, and
+// lie in LDS as in the kernel for aligned operands.
+template <int FORM, class E>
+__global__ void __launch_bounds__(256, 2) experts_staged_kernel(ExpertsArgs g) {
+  constexpr bool ACROSS_A = FORM == EXPERTS_WGRAD, ACROSS_B = FORM != EXPERTS_FORWARD;
+  constexpr int BM = 128, BN = 128, MF = 4, NF = 4, NW = 4;
+  using PA = Part<ACROSS_A, BM, NW>;
+  using PB = Part<ACROSS_B, BN, NW>;
+  constexpr int BYTES_A = 2 * kSlab * BM, BYTES = BYTES_A + 2 * kSlab * BN;
+  __shared__ __align__(1024) uint8_t slabs[2][BYTES];
+  ExpertsTile t;
+  if (!find_experts_tile<FORM, BM, BN>(g, t)) return;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int r16 = lane % 16, quad = lane / 16;
+  const int wm = (wave / 2) * 64, wn = (wave % 2) * 64;
+  const int rows_c = FORM == EXPERTS_WGRAD ? g.M : t.rows_a;
+  const int count = (t.K + kSlab - 1) / kSlab;
+  i32x4 held[PA::REGIONS + PB::REGIONS];
+  // The 16 bytes that this lane brings of region q of a part: zeros past the summed axis' end.
+  auto fetch = [&](auto part, const uint8_t* base, int64_t ld, int first, int end, int q, int b) __attribute__((always_inline)) {
+    using P = decltype(part);
+    int row, in;
+    P::source(wave, lane, row, in);
+    row += q * P::STEP;
+    if constexpr (P::ACROSS) {
+      const int k = b * kSlab + row, col = first + in / 2;
+      if (k >= t.K) return i32x4{0, 0, 0, 0};
+      return load16(base + 2 * (k * ld), 2 * col, 2 * end);
+    } else {
+      return load16(base + 2 * (min(first + row, end - 1) * ld), 2 * (b * kSlab) + in, 2 * t.K);
+    }
+  };
+  auto fetch_all = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < PA::REGIONS; ++q) held[q] = fetch(PA{}, t.A, g.lda, t.m0, ACROSS_A ? g.M : t.rows_a, q, b);
+#pragma unroll
+    for (int q = 0; q < PB::REGIONS; ++q) held[PA::REGIONS + q] = fetch(PB{}, t.B, g.ldb, t.n0, g.N, q, b);
+  };
+  f32x4 acc[NF][MF] = {};
+  const int at_a = PA::place(wm, lane), at_b = PB::place(wn, lane);
+  if (count > 0) fetch_all(0);
+#pragma unroll 1
+  for (int b = 0; b < count; ++b) {
+    uint8_t* slab = slabs[b % 2];
+#pragma unroll
+    for (int q = 0; q < PA::REGIONS + PB::REGIONS; ++q) *(i32x4*)(slab + (q * NW + wave) * 1024 + 16 * lane) = held[q];
+    // One barrier: the other buffer's readers passed it a slab ago.
+    __syncthreads();
+    if (b + 1 < count) fetch_all(b + 1);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      i32x4 fa[MF];
+#pragma unroll
+      for (int i = 0; i < MF; ++i) fa[i] = PA::read(slab, at_a, i, x);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const i32x4 fb = PB::read(slab + BYTES_A, at_b, j, x);
+#pragma unroll
+        for (int i = 0; i < MF; ++i) acc[j][i] = mfma16<E>(fb, fa[i], acc[j][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    const int m = t.m0 + wm + 16 * i + r16;
+    if (m >= rows_c) continue;
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const int n = t.n0 + wn + 16 * j + 4 * quad;
+      const float v[4] = {acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3]};
+      store_experts(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
+    }
+  }
+}
+
+constexpr int kRowsWaves = 8;
+
+// FORWARD with few rows (a decoding step): a workgroup has 16 rows of an
+// expert's weights and 16*MF of A over the whole of K. Its waves take every
+// eighth slab, straight from memory to registers, and their sums are added in
+// wave order through LDS. Bound by the weights' bytes.
+template <class E, int MF>
+__global__ void __launch_bounds__(64 * kRowsWaves, MF == 4 ? 2 : MF == 1 ? 6 : 4) experts_rows_kernel(ExpertsArgs g) {
+  constexpr int BM = 16 * MF, BN = 16, NW = kRowsWaves;
+  constexpr int AHEAD = 2;  // slabs that a wave has in flight
+  __shared__ __align__(16) f32x4 part[NW][MF][64];
+  ExpertsTile t;
+  if (!find_experts_tile<EXPERTS_FORWARD, BM, BN>(g, t)) return;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int r16 = lane % 16, quad = lane / 16;
+  const uint8_t* b = t.B + 2 * (min(t.n0 + r16, g.N - 1) * g.ldb);
+  const uint8_t* a[MF];
+  bool there[MF];  // rows that do not exist cost no loads
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    there[i] = t.m0 + 16 * i + r16 < t.rows_a;
+    a[i] = t.A + 2 * ((there[i] ? t.m0 + 16 * i + r16 : t.m0) * g.lda);
+  }
+  f32x4 acc[MF] = {};
+  struct Held {
+    i32x4 b[2], a[MF][2];
+  };
+  // `whole`: no value of the slab lies past K.
+  auto fetch = [&](Held& h, int slab, auto whole) __attribute__((always_inline)) {
+    const int k = 2 * slab * kSlab + 16 * quad;
+    auto chunk = [&](const uint8_t* row, int at) __attribute__((always_inline)) {
+      if constexpr (decltype(whole)::value) return *(const i32x4*)(row + at);
+      else return load16_end(row, at, 2 * t.K);
+    };
+    h.b[0] = chunk(b, k), h.b[1] = chunk(b, k + 64);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      h.a[i][0] = h.a[i][1] = i32x4{0, 0, 0, 0};
+      if (there[i]) h.a[i][0] = chunk(a[i], k), h.a[i][1] = chunk(a[i], k + 64);
+    }
+  };
+  auto multiply = [&](const Held& h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < MF; ++i) acc[i] = mfma16<E>(h.b[x], h.a[i][x], acc[i]);
+  };
+  const int full = t.K / kSlab;
+  int slab = wave;
+  for (; slab + (AHEAD - 1) * NW < full; slab += NW * AHEAD) {
+    Held h[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) fetch(h[u], slab + u * NW, std::true_type{});
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) multiply(h[u]);
+  }
+#pragma unroll 1
+  for (; slab < full; slab += NW) {
+    Held h;
+    fetch(h, slab, std::true_type{});
+    multiply(h);
+  }
+  if (slab == full && t.K % kSlab != 0) {  // the wave whose turn the partial slab is
+    Held h;
+    fetch(h, slab, std::false_type{});
+    multiply(h);
+  }
+#pragma unroll
+  for (int i = 0; i < MF; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave < MF) {
+    f32x4 sum = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += part[w][wave][lane];
+    const int m = t.m0 + 16 * wave + r16, n = t.n0 + 4 * quad;
+    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if (m < t.rows_a) store_experts(g, t.C, (int64_t)m * g.ldc + n, g.N - n, v);
+  }
+}
+
+template <class E>
+const void* rows_kernel(int bm) {
+  return bm == 16 ? (const void*)&experts_rows_kernel<E, 1> : bm == 32 ? (const void*)&experts_rows_kernel<E, 2>
+                                                                       : (const void*)&experts_rows_kernel<E, 4>;
+}
+template <class E>
+const void* staged_kernel(ExpertsForm form) {
+  return form == EXPERTS_FORWARD ? (const void*)&experts_staged_kernel<EXPERTS_FORWARD, E>
+         : form == EXPERTS_DGRAD ? (const void*)&experts_staged_kernel<EXPERTS_DGRAD, E>
+                                 : (const void*)&experts_staged_kernel<EXPERTS_WGRAD, E>;
+}
+
+// The kernel for a call and its tile.
+struct Choice {
+  enum Kernel { STAGED, TILE, ROWS } kernel;
+  int bm, bn, threads;
+};
+
+Choice choose(ExpertsForm form, const ExpertsArgs& g) {
+  // Direct loads: chunks of 16 bytes that lie in one row, offsets within a tile below 2^31.
+  const bool direct = (((uintptr_t)g.A | (uintptr_t)g.B) & 15) == 0 && ((g.lda | g.ldb | g.strideB) & 7) == 0 &&
+                      g.lda < 1 << 22 && g.ldb < 1 << 22 && (form == EXPERTS_WGRAD ? g.M % 8 == 0 : g.K >= 8) &&
+                      (form == EXPERTS_FORWARD || g.N % 8 == 0);
+  if (!direct) return {Choice::STAGED, 128, 128, 256};
+  const int used = form == EXPERTS_WGRAD ? 1 : g.experts < g.M ? g.experts : g.M;
+  const int64_t rows = g.M / (used < 1 ? 1 : used);
+  if (form == EXPERTS_FORWARD && rows <= 64) {
+    const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return {Choice::ROWS, bm, 16, 64 * kRowsWaves};
+  }
+  if (rows >= 192 && experts_grid(form, g, 256, 256) * (form == EXPERTS_WGRAD ? g.experts : 1) >= 200)
+    return {Choice::TILE, 256, 256, 512};
+  return {Choice::TILE, 128, 128, 256};
+}
+
+}  // namespace
+
+bool experts_launchable(ExpertsForm form, const ExpertsArgs& g) {
+  const Choice c = choose(form, g);
+  return experts_grid(form, g, c.bm, c.bn) * c.threads <= (int64_t)UINT32_MAX && (form != EXPERTS_WGRAD || g.experts <= kMaxGridY);
+}
+
+const char* experts_kernel_name(ExpertsForm form, const ExpertsArgs& g) {
+  const Choice c = choose(form, g);
+  if (c.kernel == Choice::STAGED) return "staged_128x128";
+  if (c.kernel == Choice::TILE) return c.bm == 256 ? "tile_256x256" : "tile_128x128";
+  return c.bm == 64 ? "rows_64" : c.bm == 32 ? "rows_32" : "rows_16";
+}
+
+hipError_t launch_experts(ExpertsForm form, const ExpertsArgs& g, hipStream_t s) {
+  const Choice c = choose(form, g);
+  const bool bf16 = g.type == SGEMM_MI355_BF16;
+  const dim3 grid((unsigned)experts_grid(form, g, c.bm, c.bn), form == EXPERTS_WGRAD ? (unsigned)g.experts : 1u);
+  const void* kernel = c.kernel == Choice::TILE   ? experts_tile_kernel_for(form, g.type, c.bm)
+                       : c.kernel == Choice::ROWS ? (bf16 ? rows_kernel<__hip_bfloat16>(c.bm) : rows_kernel<__half>(c.bm))
+                                                  : (bf16 ? staged_kernel<__hip_bfloat16>(form) : staged_kernel<__half>(form));
+  return launch_with(kernel, grid, dim3((unsigned)c.threads), g, s);
+}
+
+}  // namespace sgemm_impl
