@@ -189,15 +189,43 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
                       g.lda < 1 << 22 && g.ldb < 1 << 22 && (form == EXPERTS_WGRAD ? g.M % 8 == 0 : g.K >= 8) &&
                       (form == EXPERTS_FORWARD || g.N % 8 == 0);
   if (!direct) return {Choice::STAGED, 128, 128, 256};
-  const int used = form == EXPERTS_WGRAD ? 1 : g.experts < g.M ? g.experts : g.M;
-  const int64_t rows = g.M / (used < 1 ? 1 : used);
-  if (form == EXPERTS_FORWARD && rows <= 64) {
-    const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    return {Choice::ROWS, bm, 16, 64 * kRowsWaves};
-  }
-  if (rows >= 192 && experts_grid(form, g, 256, 256) * (form == EXPERTS_WGRAD ? g.experts : 1) >= 200)
-    return {Choice::TILE, 256, 256, 512};
-  return {Choice::TILE, 128, 128, 256};
+  // The number of BM x BN tiles: an expert with rows has one tile of rows, and
+  // half a tile more on average where it has many.
+  const int used = g.experts < g.M ? g.experts : g.M < 1 ? 1 : g.M;
+  auto tiles = [&](int bm, int bn) {
+    const int64_t whole = (g.M + bm - 1) / bm;
+    const int64_t tiles_m = form == EXPERTS_WGRAD ? whole * g.experts
+                            : g.experts == 1      ? whole
+                            : whole + used / 2 > used ? whole + used / 2 : used;
+    return (double)(tiles_m * ((g.N + bn - 1) / bn));
+  };
+  // 256 x 256 tiles, one to a CU, where they fill more than half of the chip
+  // and have rows to fill (us, 256 x 256 and 128 x 128 tiles: 8 experts of 512
+  // rows, N 2048, K 4096, 160 tiles 99.7 and 115.8, of 256 rows, 96 tiles 96.9
+  // and 63.0; 32 experts, N 2048, K 1024, of 128 rows 33.6 and 43.5, of 64 rows
+  // 28.7 and 25.4; weights' gradients of 1024 rows, 2048 x 4096, 128 tiles 33.1
+  // and 24.8, 4096 x 4096 41.3 and 46.2).
+  if (tiles(256, 256) >= 140 && (form == EXPERTS_WGRAD || g.M / used >= 96)) return {Choice::TILE, 256, 256, 512};
+  if (form != EXPERTS_FORWARD) return {Choice::TILE, 128, 128, 256};
+  // The least of the estimated times: for each round of the chip a start and
+  // the slabs, or the weights at the rate that the kernel reaches, fitted to 1
+  // to 32 experts of 1 to 128 rows, N and K 256 to 4096 (the choice is 1.018
+  // of the fastest there on average). Few rows a workgroup load less and begin
+  // sooner, but read the weights again for each 16 to 64 rows (8 experts, N
+  // 2048, K 4096, rows 16 / 32 / 64 and tiles: of 4 rows 32, 32, 31 and 60, of
+  // 32 rows 73, 66, 58 and 60).
+  const double k = g.K / 1024.0, weights = (double)used * g.N * (double)g.K * 2.0 / 1.0e6;
+  const double rounds = std::ceil(tiles(128, 128) / 512.0);
+  Choice best{Choice::TILE, 128, 128, 256};
+  double least = std::fmax(2.3 + rounds * (0.6 + 11.0 * k), 2.0 + weights / 4.8);
+  auto offer = [&](int bm, double start, double slabs, double rate) {
+    const double r = std::fmax(tiles(bm, 16) / 256.0, 1.0), time = std::fmax(3.2 + r * (start + slabs * k), 2.0 + weights / rate);
+    if (time < least) best = {Choice::ROWS, bm, 16, 64 * kRowsWaves}, least = time;
+  };
+  offer(64, 1.08, 1.65, 5.0);
+  offer(32, 0.76, 1.58, 5.0);
+  offer(16, 0.58, 1.43, 5.7);
+  return best;
 }
 
 }  // namespace

@@ -9,22 +9,10 @@
 // sixteen lanes read four rows by sixteen columns, and each gets the four
 // values of its column). No operand is copied or transposed beforehand.
 
-#include <type_traits>
-
 #include "experts_device.h"
 
 namespace sgemm_impl {
 namespace {
-
-constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
-
-// 16 bytes at base + offset (none beyond base + bytes) to LDS at lds + 16*lane.
-__device__ __forceinline__ void copy16_to_lds(const uint8_t* base, int bytes, uint32_t offset, uint8_t* lds) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass has no type for the buffer
-  const auto buffer = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00027000);  // plain bytes, range-checked
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (lds_void*)lds, 16, offset, 0, 0, 0);
-#endif
-}
 
 template <int FORM, class E, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsArgs g) {
@@ -32,14 +20,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsAr
   constexpr int NW = WM * WN, NT = 64 * NW, MF = BM / WM / 16, NF = BN / WN / 16;
   using PA = Part<ACROSS_A, BM, NW>;
   using PB = Part<ACROSS_B, BN, NW>;
-  constexpr int REGIONS = PA::REGIONS + PB::REGIONS, BYTES_A = 2 * kSlab * BM, BYTES = BYTES_A + 2 * kSlab * BN;
+  constexpr int REGIONS = PA::REGIONS + PB::REGIONS, BYTES_A = PA::BYTES, BYTES = BYTES_A + PB::BYTES;
   // One array per stage, so that the compiler sees that reads of one do not
   // wait for loads into the other.
   __shared__ __align__(1024) uint8_t slab0[BYTES], slab1[BYTES];
   ExpertsTile t;
   if (!find_experts_tile<FORM, BM, BN>(g, t)) return;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int r16 = lane % 16, quad = lane / 16;
   const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
   const int rows_c = FORM == EXPERTS_WGRAD ? g.M : t.rows_a;  // C's end below the tile
   // Whole slabs, and what is left. Where both operands run across the summed
@@ -175,52 +162,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsAr
     if (b < full) step(b, slab0, slab1);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the workgroup
   }
-  // To C by way of LDS, ROUND fragments of A's rows at a time, so that a lane
-  // stores eight neighbours and a row's strip is stored at a stretch, in a loop
-  // of rows that is not unrolled: its code runs once per tile.
-  constexpr int WIDTH = 16 * NF, LANES = WIDTH / 8;  // floats of a row of the strip, and lanes that store one
-  constexpr int ROOM = BYTES * 2 / NW / (16 * WIDTH * 4);  // fragments that a wave's share of the slabs holds
-  constexpr int ROUND = ROOM >= MF ? MF : ROOM >= 2 && MF % 2 == 0 ? 2 : 1;
-  static_assert(ROUND >= 1 && MF % ROUND == 0, "whole rounds");
-  float* out = (float*)(wave < NW / 2 ? slab0 : slab1) + wave % (NW / 2) * (ROUND * 16 * WIDTH);
+  float* out = (float*)(wave < NW / 2 ? slab0 : slab1) + wave % (NW / 2) * (BYTES * 2 / NW / 4);
   __syncthreads();  // all reads of the slabs have been made
-#pragma unroll
-  for (int i0 = 0; i0 < MF; i0 += ROUND) {
-    // Chunk c of four floats of row r lies at place c ^ (r % 16): 16 rows' writes of one chunk meet all banks.
-#pragma unroll
-    for (int i = 0; i < ROUND; ++i)
-#pragma unroll
-      for (int j = 0; j < NF; ++j) *(f32x4*)(out + (16 * i + r16) * WIDTH + 4 * ((4 * j + quad) ^ r16)) = acc[j][i0 + i];
-    __builtin_amdgcn_wave_barrier();  // LDS serves a wave in order
-    const int c = 2 * (lane % LANES), n = t.n0 + wn + 4 * c;
-    const int rows = min(16 * ROUND, rows_c - t.m0 - wm - 16 * i0);
-    const int64_t at = (int64_t)(t.m0 + wm + 16 * i0) * g.ldc + n;
-    auto rows_to_c = [&](auto* C) __attribute__((always_inline)) {
-      using T = std::remove_pointer_t<decltype(C)>;
-      auto strip = [&](int r, float (&v)[8]) __attribute__((always_inline)) {
-        *(f32x4*)v = *(const f32x4*)(out + r * WIDTH + 4 * (c ^ (r % 16)));
-        *(f32x4*)(v + 4) = *(const f32x4*)(out + r * WIDTH + 4 * ((c + 1) ^ (r % 16)));
-      };
-      if (g.beta == 0.0f && n + 8 <= g.N) {
-#pragma unroll 4
-        for (int r = lane / LANES; r < rows; r += 64 / LANES) {
-          float v[8];
-          strip(r, v);
-          store8(C + at + r * g.ldc, 8, v);
-        }
-      } else {
-#pragma unroll 1
-        for (int r = lane / LANES; r < rows; r += 64 / LANES) {
-          float v[8];
-          strip(r, v);
-          store_as<T, 8>(C + at + r * g.ldc, g.N - n, v, g.beta);
-        }
-      }
-    };
-    if (g.c_type == SGEMM_MI355_F32) rows_to_c((float*)t.C);
-    else rows_to_c((E*)t.C);
-    __builtin_amdgcn_wave_barrier();
-  }
+  strips_to_c<E, MF, NF, BYTES * 2 / NW>(g, t, acc, out, wm, wn, rows_c, lane);
 }
 
 template <class E, int BM, int BN, int WM, int WN>

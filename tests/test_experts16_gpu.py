@@ -129,8 +129,8 @@ def test_larger_products_of_whole_numbers_are_exact(form, counts, N, K, kind):
 
 
 KERNELS = {  # calls whose kernel is known
-    ("forward", "rows_16"): ([3, 9, 0, 16], 100, 328), ("forward", "rows_32"): ([25, 20, 32, 1, 31], 100, 328),
-    ("forward", "rows_64"): ([50, 40, 64, 1, 61], 100, 328), ("forward", "tile_128x128"): ([100, 90, 128, 1, 140], 300, 328),
+    ("forward", "rows_16"): ([3, 9, 0, 16], 100, 328), ("forward", "rows_32"): ([100, 90, 128, 1, 140], 300, 328),
+    ("forward", "rows_64"): ([30, 40, 64, 1, 61], 1000, 1032), ("forward", "tile_128x128"): ([250, 300, 280, 1, 270], 600, 72),
     ("forward", "tile_256x256"): ([2000, 1000, 1999], 4000, 136), ("dgrad", "tile_128x128"): ([100, 90, 128, 1, 140], 328, 304),
     ("dgrad", "tile_256x256"): ([2000, 1000, 1999], 136, 4000), ("wgrad", "tile_128x128"): ([100, 90, 128, 1, 140], 328, 304),
     ("wgrad", "tile_256x256"): ([70, 1, 200, 64], 2000, 2008), ("forward", "staged_128x128"): ([100, 90, 128, 1, 140], 301, 333),
