@@ -10,8 +10,9 @@ from __future__ import annotations
 
 import ctypes
 
+from ._binding import MOST
 from ._fp8 import (_bind, _blocks, _bytes_out, _check, _empty, _F, FP32_SUMS, _gpu, _I, _ld, _Library, _operand, _P,
-                   _result, _SCALES, _stream_of, _type_of, torch)
+                   _result, _SCALES, _stream_of, _type_of, _types, torch)
 
 NONE, RELU, SILU, GELU, GELU_TANH = 0, 1, 2, 3, 4
 MAX_NORM_COLS = 16384
@@ -29,8 +30,8 @@ _SIGNATURES = {
     "sgemm_mi355_fp8_gemm_epilogue": [_I] * 4 + [_P, _I, *_SCALES, _P, _I, *_SCALES, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P],
 }
 _RESULTS = {"sgemm_mi355_rms_norm_backward_workspace_size": _SIZE, "sgemm_mi355_epilogue_backward_workspace_size": _SIZE}
-for _name, _types in _SIGNATURES.items():
-    globals()[_name] = _bind(_name, _types, _RESULTS.get(_name, _I))
+for _name, _arguments in _SIGNATURES.items():
+    globals()[_name] = _bind(_name, _arguments, _RESULTS.get(_name, _I))
 _c = _Library(_SIGNATURES, _RESULTS)
 
 
@@ -56,18 +57,34 @@ def _act(name):
 
 def _vector(x, name, length, device, dtype=None):
     """Address of a dense 1-D tensor of `length` values on this GPU."""
-    _gpu(x, name, dtype, device)
-    if x.dim() != 1 or x.numel() != length or (length > 1 and x.stride(0) != 1):
+    if x.get_device() != device or (dtype is not None and x.dtype != dtype):
+        _gpu(x, name, dtype, device)
+    if x.dim() != 1 or x.numel() != length or not x.is_contiguous():
         raise ValueError(f"{name} must be a dense 1-D tensor of {length} values")
     return x.data_ptr()
 
 
-def _like(x, name, other, device, shape=None):
-    """Address and row stride of a 2-D tensor of other's dtype (and shape)."""
-    _gpu(x, name, other.dtype, device)
-    shape = other.shape if shape is None else shape
-    if x.shape != shape:
+def _matrix(x, name):
+    """(GPU, type, address, row stride, shape) of a 2-D tensor with contiguous rows."""
+    on, kind = x.get_device(), _types.get(x.dtype)
+    if on < 0 or kind is None:
+        on, kind = _gpu(x, name), _type_of(x.dtype, name)
+    shape, strides = x.shape, x.stride()
+    # _ld's own first test, without the call: most matrices pass it
+    if len(strides) == 2 and strides[1] == 1 and 1 < shape[0] <= MOST >= strides[0] >= shape[1] > 0:
+        return on, kind, x.data_ptr(), strides[0], shape
+    return on, kind, x.data_ptr(), _ld(x, name), shape
+
+
+def _like(x, name, dtype, device, shape):
+    """Address and row stride of a 2-D tensor of this dtype and shape on this GPU."""
+    if x.get_device() != device or x.dtype != dtype:
+        _gpu(x, name, dtype, device)
+    sizes, strides = x.shape, x.stride()
+    if sizes != shape:
         raise ValueError(f"{name} must be {' x '.join(map(str, shape))}")
+    if strides[1] == 1 and 1 < sizes[0] <= MOST >= strides[0] >= sizes[1] > 0:
+        return x.data_ptr(), strides[0]
     return x.data_ptr(), _ld(x, name)
 
 
@@ -85,21 +102,20 @@ def _quantised_out(rows, cols, device, stream):
 
 
 def _norm_input(X, weight, residual, H, stream):
-    on = _gpu(X, "X")
-    kind, ldx = _type_of(X.dtype, "X"), _ld(X, "X")
-    w = _vector(weight, "weight", X.shape[1], on)
+    on, kind, x, ldx, shape = _matrix(X, "X")
+    cols = shape[1]
+    w = _vector(weight, "weight", cols, on)
     w_kind = _type_of(weight.dtype, "weight")
     if residual is None:
         if H is not None:
             raise ValueError("H needs a residual; without one it is X")
-        return on, kind, (X.data_ptr(), ldx, None, 0, w, w_kind), X, (None, 0)
-    r = _like(residual, "residual", X, on)
+        return on, kind, (x, ldx, None, 0, w, w_kind), X, None, 0, shape
+    dtype = X.dtype
+    r, ldr = _like(residual, "residual", dtype, on, shape)
     if H is None:
-        H = _empty(X.shape, X.dtype, X.device, stream)
-        h = H.data_ptr(), X.shape[1] or 1
-    else:
-        h = _like(H, "H", X, on)
-    return on, kind, (X.data_ptr(), ldx, *r, w, w_kind), H, h
+        H = _empty(shape, dtype, X.device, stream)
+        return on, kind, (x, ldx, r, ldr, w, w_kind), H, H.data_ptr(), cols or 1, shape
+    return on, kind, (x, ldx, r, ldr, w, w_kind), H, *_like(H, "H", dtype, on, shape), shape
 
 
 def rms_norm_fp8(X, weight, *, residual=None, eps: float = 1e-6, H=None, wide: bool = False, stream=None):
@@ -113,23 +129,21 @@ def rms_norm_fp8(X, weight, *, residual=None, eps: float = 1e-6, H=None, wide: b
     given, the residual itself for an update in place. ``wide``: the norm in
     X's dtype too, as a fifth result.
     """
-    on, kind, x, H, h = _norm_input(X, weight, residual, H, stream)
-    rows, cols = X.shape
+    on, kind, x, H, h, ldh, (rows, cols) = _norm_input(X, weight, residual, H, stream)
     Q, ldq, S = _quantised_out(rows, cols, X.device, stream)
     rstd = _empty((rows,), torch.float32, X.device, stream)
     Y = _empty((rows, cols), X.dtype, X.device, stream) if wide else None
-    _check(_launch(_c.rms_norm, on, kind, rows, cols, *x, eps, *h, rstd.data_ptr(), None if Y is None else Y.data_ptr(), cols,
+    _check(_launch(_c.rms_norm, on, kind, rows, cols, *x, eps, h, ldh, rstd.data_ptr(), None if Y is None else Y.data_ptr(), cols,
                        Q.data_ptr(), ldq, S.data_ptr(), 1, rows or 1, _stream_of(on, stream)), "rms_norm")
     return (Q, S, H, rstd, Y) if wide else (Q, S, H, rstd)
 
 
 def rms_norm(X, weight, *, residual=None, eps: float = 1e-6, H=None, stream=None):
     """(Y, H, rstd): the norm of X + residual in X's dtype; the rest as in rms_norm_fp8."""
-    on, kind, x, H, h = _norm_input(X, weight, residual, H, stream)
-    rows, cols = X.shape
+    on, kind, x, H, h, ldh, (rows, cols) = _norm_input(X, weight, residual, H, stream)
     Y = _empty((rows, cols), X.dtype, X.device, stream)
     rstd = _empty((rows,), torch.float32, X.device, stream)
-    _check(_launch(_c.rms_norm, on, kind, rows, cols, *x, eps, *h, rstd.data_ptr(), Y.data_ptr(), cols, None, 0, None, 0, 0,
+    _check(_launch(_c.rms_norm, on, kind, rows, cols, *x, eps, h, ldh, rstd.data_ptr(), Y.data_ptr(), cols, None, 0, None, 0, 0,
                        _stream_of(on, stream)), "rms_norm")
     return Y, H, rstd
 
@@ -139,18 +153,17 @@ def rms_norm_backward(dY, H, rstd, weight, *, dH=None, stream=None):
     rstd that the forward call returned. dX (of H's dtype) is the gradient of X
     and of the residual; ``dH``, the gradient of H from elsewhere, is added to
     it. dweight is float32."""
-    on = _gpu(H, "H")
-    kind, ldh = _type_of(H.dtype, "H"), _ld(H, "H")
-    rows, cols = H.shape
-    dy = _like(dY, "dY", H, on)
+    on, kind, h, ldh, shape = _matrix(H, "H")
+    rows, cols = shape
+    dy = _like(dY, "dY", H.dtype, on, shape)
     a = _vector(rstd, "rstd", rows, on, torch.float32)
     w = _vector(weight, "weight", cols, on)
-    d = (None, 0) if dH is None else _like(dH, "dH", H, on)
-    dX = _empty((rows, cols), H.dtype, H.device, stream)
+    d = (None, 0) if dH is None else _like(dH, "dH", H.dtype, on, shape)
+    dX = _empty(shape, H.dtype, H.device, stream)
     dw = _empty((cols,), torch.float32, H.device, stream)
     need = _c.rms_norm_backward_workspace_size(rows, cols)
     at, room = _room(need, H.device, stream)
-    _check(_launch(_c.rms_norm_backward, on, kind, rows, cols, *dy, H.data_ptr(), ldh, a, w, _type_of(weight.dtype, "weight"), *d,
+    _check(_launch(_c.rms_norm_backward, on, kind, rows, cols, *dy, h, ldh, a, w, _type_of(weight.dtype, "weight"), *d,
                                 dX.data_ptr(), cols, dw.data_ptr(), at, need, _stream_of(on, stream)), "rms_norm_backward")
     if rows == 0:  # the C call writes nothing then
         _zero(dw, stream)
@@ -166,11 +179,10 @@ def _zero(x, stream):
 
 
 def _halves(H):
-    kind, ldh = _type_of(H.dtype, "H"), _ld(H, "H")
-    rows, cols = H.shape
+    on, kind, h, ldh, (rows, cols) = _matrix(H, "H")
     if cols % 2:
         raise ValueError("H must have an even number of columns")
-    return kind, ldh, rows, cols // 2
+    return on, kind, h, ldh, rows, cols // 2
 
 
 def gated_fp8(H, *, activation: str = "silu", wide: bool = False, stream=None):
@@ -178,32 +190,29 @@ def gated_fp8(H, *, activation: str = "silu", wide: bool = False, stream=None):
     columns, as quantize_fp8 gives them, from its float32 values; g is the
     first half of H's columns, u the second. ``wide``: z in H's dtype too, as a
     third result. Activations: "silu", "gelu", "gelu_tanh", "relu", "none"."""
-    on = _gpu(H, "H")
-    kind, ldh, rows, cols = _halves(H)
+    on, kind, h, ldh, rows, cols = _halves(H)
     Q, ldq, S = _quantised_out(rows, cols, H.device, stream)
     Z = _empty((rows, cols), H.dtype, H.device, stream) if wide else None
-    _check(_launch(_c.gated, on, kind, _act(activation), rows, cols, H.data_ptr(), ldh, None if Z is None else Z.data_ptr(), cols or 1,
+    _check(_launch(_c.gated, on, kind, _act(activation), rows, cols, h, ldh, None if Z is None else Z.data_ptr(), cols or 1,
                     Q.data_ptr(), ldq, S.data_ptr(), 1, rows or 1, _stream_of(on, stream)), "gated")
     return (Q, S, Z) if wide else (Q, S)
 
 
 def gated(H, *, activation: str = "silu", stream=None):
     """z = act(g) * u in H's dtype; g is the first half of H's columns, u the second."""
-    on = _gpu(H, "H")
-    kind, ldh, rows, cols = _halves(H)
+    on, kind, h, ldh, rows, cols = _halves(H)
     Z = _empty((rows, cols), H.dtype, H.device, stream)
-    _check(_launch(_c.gated, on, kind, _act(activation), rows, cols, H.data_ptr(), ldh, Z.data_ptr(), cols or 1, None, 0, None, 0, 0,
+    _check(_launch(_c.gated, on, kind, _act(activation), rows, cols, h, ldh, Z.data_ptr(), cols or 1, None, 0, None, 0, 0,
                     _stream_of(on, stream)), "gated")
     return Z
 
 
 def gated_backward(dZ, H, *, activation: str = "silu", stream=None):
     """dH = [act'(g) * u * dZ | act(g) * dZ], of H's dtype, for the gradient dZ of z."""
-    on = _gpu(H, "H")
-    kind, ldh, rows, cols = _halves(H)
-    dz = _like(dZ, "dZ", H, on, (rows, cols))
+    on, kind, h, ldh, rows, cols = _halves(H)
+    dz = _like(dZ, "dZ", H.dtype, on, (rows, cols))
     dH = _empty((rows, 2 * cols), H.dtype, H.device, stream)
-    _check(_launch(_c.gated_backward, on, kind, _act(activation), rows, cols, *dz, H.data_ptr(), ldh, dH.data_ptr(), 2 * cols or 1,
+    _check(_launch(_c.gated_backward, on, kind, _act(activation), rows, cols, *dz, h, ldh, dH.data_ptr(), 2 * cols or 1,
                              _stream_of(on, stream)), "gated_backward")
     return dH
 
@@ -231,7 +240,7 @@ def gemm_fp8_epilogue(A, SA, B, SB, C=None, *, bias=None, activation=None, resid
     C = _result(C, (M, N), dtype, A, on, 0.0, stream)
     kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
     v = None if bias is None else _vector(bias, "bias", N, on, torch.float32)
-    r = (None, 0) if residual is None else _like(residual, "residual", C, on)
+    r = (None, 0) if residual is None else _like(residual, "residual", C.dtype, on, (M, N))
     P = _empty((M, N), C.dtype, A.device, stream) if pre else None
     _check(_launch(_c.fp8_gemm_epilogue, on, kind, M, N, K, *a[:5], *b, v, _act(activation), *r, None if P is None else P.data_ptr(),
                                 N or 1, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)), "fp8_gemm_epilogue")
@@ -243,15 +252,14 @@ def epilogue_backward(dC, P, *, activation=None, bias: bool = True, stream=None)
     dtype, and its sum over the rows, the bias' gradient (float32; None without
     ``bias``), for the gradient dC of gemm_fp8_epilogue's result. The
     residual's gradient is dC."""
-    on = _gpu(P, "P")
-    kind, ldp = _type_of(P.dtype, "P"), _ld(P, "P")
-    rows, cols = P.shape
-    dc = _like(dC, "dC", P, on)
-    dP = _empty((rows, cols), P.dtype, P.device, stream)
+    on, kind, p, ldp, shape = _matrix(P, "P")
+    rows, cols = shape
+    dc = _like(dC, "dC", P.dtype, on, shape)
+    dP = _empty(shape, P.dtype, P.device, stream)
     db = _empty((cols,), torch.float32, P.device, stream) if bias else None
     need = _c.epilogue_backward_workspace_size(rows, cols) if bias else 0
     at, room = _room(need, P.device, stream)
-    _check(_launch(_c.epilogue_backward, on, kind, _act(activation), rows, cols, *dc, P.data_ptr(), ldp, dP.data_ptr(), cols or 1,
+    _check(_launch(_c.epilogue_backward, on, kind, _act(activation), rows, cols, *dc, p, ldp, dP.data_ptr(), cols or 1,
                                 None if db is None else db.data_ptr(), at, need, _stream_of(on, stream)), "epilogue_backward")
     if bias and rows == 0:  # the C call writes nothing then
         _zero(db, stream)

@@ -132,11 +132,20 @@ __device__ __forceinline__ void finish_as(const Fp8Args& g, int64_t m, int n, in
                                           const float (&r)[W], float (&v)[W]) {
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
-  if (g.P != nullptr) store_as<T, W>((T*)g.P + m * g.ldp + n, valid, v, 0.0f);
-  activate(g.act, v);
+  auto put = [&](T* c) __attribute__((always_inline)) {
+    if constexpr (W == 8) {
+      if (g.past && valid >= 8) {
+        store8_once(c, 8, v);
+        return;
+      }
+    }
+    store_as<T, W>(c, valid, v, 0.0f);
+  };
+  if (g.P != nullptr) put((T*)g.P + m * g.ldp + n);
+  activate<sizeof(T) == 2>(g.act, v);
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += r[i];
-  store_as<T, W>((T*)g.C + m * g.ldc + n, valid, v, 0.0f);
+  put((T*)g.C + m * g.ldc + n);
 }
 // `valid` of W values at p as FP32, zeros for the others and without a p.
 template <class T, int W>

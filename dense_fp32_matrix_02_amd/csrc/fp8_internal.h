@@ -61,6 +61,7 @@ struct Fp8Args {
   int64_t ldr;
   void* P;  // p in C's type; null: not asked for
   int64_t ldp;
+  bool past;  // C and P go past the caches
 };
 
 hipError_t launch_fp8_gemm(Fp8Form form, const Fp8Args& g, hipStream_t s);

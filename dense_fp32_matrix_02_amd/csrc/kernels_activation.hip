@@ -10,17 +10,17 @@ namespace {
 
 // z = act(g) u of H = [g | u]. Sixteen lanes hold one block of 128 of a row of
 // z, eight values each.
-template <class T, int ACT>
+template <class T, int ACT, int RUNS>
 __global__ void __launch_bounds__(256) gated_kernel(GatedArgs a) {
   const uint32_t blocks = (uint32_t)(a.cols + kBlock - 1) / kBlock;
   const uint64_t group = (uint64_t)blockIdx.x * 16 + threadIdx.x / 16;
   if (group >= (uint64_t)blocks * (uint32_t)a.rows) return;  // the same for all 16 lanes of a block
   const uint32_t row = (uint32_t)group / blocks, b = (uint32_t)group - row * blocks;
   const int col = (int)(b * kBlock) + 8 * (threadIdx.x % 16), valid = a.cols - col;
-  const T* h = (const T*)a.H + row * a.ldh + col;
+  const T* h = (const T*)a.H + row * a.ldh;
   float g[8], z[8];
-  load8(h, valid, g);
-  load8(h + a.cols, valid, z);
+  load_run<RUNS>(h, col, a.cols, g);
+  load_run<RUNS>(h + a.cols, col, a.cols, z);
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -29,28 +29,29 @@ __global__ void __launch_bounds__(256) gated_kernel(GatedArgs a) {
     z[i] *= value;
     m = max(m, i < valid ? mag(z[i]) : 0u);
   }
-  if (a.Z != nullptr) store8((T*)a.Z + row * a.ldz + col, valid, z);
+  if (a.Z != nullptr) store_run<RUNS>((T*)a.Z + row * a.ldz, col, a.cols, z);
   if (a.Q == nullptr) return;
 #pragma unroll
   for (int d = 1; d < 16; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
   const float s = scale_of(m);
-  store_bytes(a.Q + row * a.ldq + col, quantize8(z, s), valid);
+  store_run<RUNS>(a.Q + row * a.ldq, col, a.cols, quantize8(z, s));
   if (threadIdx.x % 16 == 0) a.S[row * a.s_row + b * a.s_block] = s;
 }
 
-// dg = act'(g) u dz and du = act(g) dz: eight neighbours of a row of z per thread.
-template <class T, int ACT>
+// dg = act'(g) u dz and du = act(g) dz: eight neighbours of a row of z per
+// thread.
+template <class T, int ACT, int RUNS>
 __global__ void __launch_bounds__(256) gated_backward_kernel(GatedArgs a) {
   const uint32_t chunks = (uint32_t)(a.cols + 7) / 8;
   const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= (uint64_t)chunks * (uint32_t)a.rows) return;
   const uint32_t row = (uint32_t)id / chunks;
-  const int col = (int)(8 * ((uint32_t)id - row * chunks)), valid = a.cols - col;
-  const T* h = (const T*)a.H + row * a.ldh + col;
+  const int col = (int)(8 * ((uint32_t)id - row * chunks));
+  const T* h = (const T*)a.H + row * a.ldh;
   float g[8], u[8], dz[8];
-  load8(h, valid, g);
-  load8(h + a.cols, valid, u);
-  load8((const T*)a.dZ + row * a.lddz + col, valid, dz);
+  load_run<RUNS>(h, col, a.cols, g);
+  load_run<RUNS>(h + a.cols, col, a.cols, u);
+  load_run<RUNS>((const T*)a.dZ + row * a.lddz, col, a.cols, dz);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float value, slope;
@@ -58,38 +59,38 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(GatedArgs a) {
     g[i] = slope * u[i] * dz[i];
     u[i] = value * dz[i];
   }
-  T* d = (T*)a.dH + row * a.lddh + col;
-  store8(d, valid, g);
-  store8(d + a.cols, valid, u);
+  T* d = (T*)a.dH + row * a.lddh;
+  store_run<RUNS>(d, col, a.cols, g);
+  store_run<RUNS>(d + a.cols, col, a.cols, u);
 }
 
 // dp = act'(p) dc, and its sum over a group's rows. A workgroup has 8*LANES
-// columns of one group: LANES threads side by side, 256/LANES rows at a time;
-// these threads' sums are added in their order.
-template <class T, int ACT, int LANES>
+// columns of one group: LANES threads side by side, 256/LANES rows at a time,
+// every groups-th such run of rows; these threads' sums are added in their order.
+template <class T, int ACT, int LANES, int RUNS>
 __global__ void __launch_bounds__(256) epilogue_backward_kernel(EpilogueBackArgs a) {
   constexpr int ROWS = 256 / LANES;
   __shared__ __align__(16) float part[ROWS][8 * LANES];
   const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
   const int strips = (a.cols + 8 * LANES - 1) / (8 * LANES);
   const int group = blockIdx.x / strips;
-  const int col = 8 * ((blockIdx.x - group * strips) * LANES + lane), valid = a.cols - col;
-  const int64_t first = (int64_t)group * a.per, end = min((int64_t)a.rows, first + a.per);
+  const int col = 8 * ((blockIdx.x - group * strips) * LANES + lane);
   float sum[8] = {};
-  if (valid > 0) {
-#pragma unroll 2
-    for (int64_t row = first + team; row < end; row += ROWS) {
+  if (col < a.cols) {
+#pragma unroll 4
+    for (int64_t row = (int64_t)group * ROWS + team; row < a.rows; row += (int64_t)a.groups * ROWS) {
       float p[8], d[8];
-      load8((const T*)a.P + row * a.ldp + col, valid, p);
-      load8((const T*)a.dC + row * a.lddc + col, valid, d);
+      load_run<RUNS>((const T*)a.P + row * a.ldp, col, a.cols, p);
+      load_run<RUNS>((const T*)a.dC + row * a.lddc, col, a.cols, d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float value, slope;
-        activation<ACT>(p[i], value, slope);
+        if constexpr (sizeof(T) == 2) activation16<ACT>(p[i], value, slope);
+        else activation<ACT>(p[i], value, slope);
         d[i] *= slope;
         sum[i] += d[i];
       }
-      store8((T*)a.dP + row * a.lddp + col, valid, d);
+      store_run<RUNS>((T*)a.dP + row * a.lddp, col, a.cols, d);
     }
   }
   if (a.sums == nullptr) return;
@@ -150,8 +151,10 @@ hipError_t launch_gated(int type, int act, const GatedArgs& a, hipStream_t s) {
   const int64_t groups = (int64_t)((a.cols + kBlock - 1) / kBlock) * a.rows;
   return by_type(type, [&](auto t) {
     return by_act(act, [&](auto f) {
-      return launch_with((const void*)&gated_kernel<decltype(t), decltype(f)::value>, dim3((unsigned)((groups + 15) / 16)),
-                         dim3(256), a, s);
+      constexpr int ACT = decltype(f)::value;
+      return launch_with(a.runs == RUNS_WHOLE ? (const void*)&gated_kernel<decltype(t), ACT, RUNS_WHOLE>
+                                              : (const void*)&gated_kernel<decltype(t), ACT, RUNS_ANY>,
+                         dim3((unsigned)((groups + 15) / 16)), dim3(256), a, s);
     });
   });
 }
@@ -160,8 +163,11 @@ hipError_t launch_gated_backward(int type, int act, const GatedArgs& a, hipStrea
   const int64_t chunks = (int64_t)((a.cols + 7) / 8) * a.rows;
   return by_type(type, [&](auto t) {
     return by_act(act, [&](auto f) {
-      return launch_with((const void*)&gated_backward_kernel<decltype(t), decltype(f)::value>,
-                         dim3((unsigned)((chunks + 255) / 256)), dim3(256), a, s);
+      constexpr int ACT = decltype(f)::value;
+      return by_runs(a.runs, [&](auto runs) {
+        return launch_with((const void*)&gated_backward_kernel<decltype(t), ACT, decltype(runs)::value>,
+                           dim3((unsigned)((chunks + 255) / 256)), dim3(256), a, s);
+      });
     });
   });
 }
@@ -174,9 +180,8 @@ int strips_of(int cols) { return cols <= kNarrow ? 1 : (cols + 511) / 512; }
 void epilogue_groups(int rows, int cols, EpilogueBackArgs& a) {
   const int64_t wanted = 2048 / strips_of(cols) > 1 ? 2048 / strips_of(cols) : 1;
   const int least = cols <= kNarrow ? 64 : 32;  // rows of a group: some for each thread
-  const int64_t per = ((int64_t)rows + wanted - 1) / wanted;
-  a.per = per > least ? (int)per : least;
-  a.groups = (int)(((int64_t)rows + a.per - 1) / a.per);
+  const int64_t groups = ((int64_t)rows + least - 1) / least;
+  a.groups = (int)(groups < wanted ? groups : wanted);
 }
 
 hipError_t launch_epilogue_backward(int type, int act, const EpilogueBackArgs& a, float* dbias, hipStream_t s) {
@@ -184,9 +189,11 @@ hipError_t launch_epilogue_backward(int type, int act, const EpilogueBackArgs& a
     return by_act(act, [&](auto f) {
       using T = decltype(t);
       constexpr int ACT = decltype(f)::value;
-      return launch_with(a.cols <= kNarrow ? (const void*)&epilogue_backward_kernel<T, ACT, 16>
-                                           : (const void*)&epilogue_backward_kernel<T, ACT, 64>,
-                         dim3((unsigned)(a.groups * strips_of(a.cols))), dim3(256), a, s);
+      const dim3 grid((unsigned)(a.groups * strips_of(a.cols)));
+      if (a.cols <= kNarrow) return launch_with((const void*)&epilogue_backward_kernel<T, ACT, 16, RUNS_ANY>, grid, dim3(256), a, s);
+      return by_runs(a.runs, [&](auto runs) {
+        return launch_with((const void*)&epilogue_backward_kernel<T, ACT, 64, decltype(runs)::value>, grid, dim3(256), a, s);
+      });
     });
   });
   if (e != hipSuccess || a.sums == nullptr || a.groups == 1) return e;

@@ -300,9 +300,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
     auto rows_to_c = [&](auto* C) __attribute__((always_inline)) {
       using T = std::remove_pointer_t<decltype(C)>;
       if constexpr (FORM == FP8_EPILOGUE) {
-        // Rows by twos, the next two's residual asked for before these two are
+        // Some rows at a time, the next ones' residual asked for before these are
         // stored: past a store the compiler may not move a load (C can be the residual).
-        constexpr int APART = 64 / LANES;
+        constexpr int APART = 64 / LANES, MOST = sizeof(T) == 2 ? 4 : 2, AT_ONCE = MOST * APART <= 16 * ROUND ? MOST : 16 * ROUND / APART;
+        static_assert(16 * ROUND % (AT_ONCE * APART) == 0, "the last rows of a pass are in the strip's own room");
         const int64_t m = t.m0 + wm + 16 * i0;
         struct alignas(sizeof(T)) Run {
           T e[8];
@@ -324,19 +325,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
         float bias[8];
         load_as(g.bias + n, g.bias != nullptr, g.N - n, bias);
         int r0 = lane / LANES;
-        Run next[2] = {ask(r0), ask(r0 + APART)};
-#pragma unroll 1
-        for (; r0 < rows; r0 += 2 * APART) {
-          const Run now[2] = {next[0], next[1]};
-          next[0] = ask(r0 + 2 * APART), next[1] = ask(r0 + 3 * APART);
+        Run next[AT_ONCE];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (r0 + u * APART >= rows) break;
-            float v[8], res[8];
-            strip(r0 + u * APART, v);
+        for (int u = 0; u < AT_ONCE; ++u) next[u] = ask(r0 + u * APART);
+#pragma unroll 1
+        for (; r0 < rows; r0 += AT_ONCE * APART) {
+          Run now[AT_ONCE];
+          float v[AT_ONCE][8];
+#pragma unroll
+          for (int u = 0; u < AT_ONCE; ++u) {
+            now[u] = next[u];
+            next[u] = ask(r0 + (AT_ONCE + u) * APART);
+            strip(r0 + u * APART, v[u]);  // past C's rows, but in the strip
+          }
+#pragma unroll
+          for (int u = 0; u < AT_ONCE; ++u) {
+            float res[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) res[i] = to_f32(now[u].e[i]);
-            finish_as<T>(g, m + r0 + u * APART, n, g.N - n, bias, res, v);
+            finish_as<T>(g, m + r0 + u * APART, n, r0 + u * APART < rows ? g.N - n : 0, bias, res, v[u]);
           }
         }
       } else if (g.beta == 0.0f && n + 8 <= g.N) {

@@ -41,6 +41,18 @@ int check_activation(int type, int act, int rows, int cols) {
   return SGEMM_MI355_OK;
 }
 
+// The form of the rows of matrices of rows x cols elements; `aligned`: each of
+// them 16-byte aligned. Past the caches (8192 x 8192 bf16 in the epilogue's
+// backward pass 75.5 us against 96.2 through them, 16384 x 2048 in the gated
+// one 57.4 and 70.1) go those that the caches do not hold for whoever comes
+// next; of smaller ones, or with rows that share lines with their neighbours
+// (3001 x 2047 in the norm: 23.7 against 17.7), it costs time.
+int runs_of(int rows, int cols, int size, bool aligned) {
+  if (cols % 8 != 0) return RUNS_ANY;
+  return aligned && (int64_t)rows * cols * size >= (int64_t)64 << 20 ? RUNS_ONCE : RUNS_WHOLE;
+}
+bool aligned16(const void* p, int64_t ld, int size) { return (((uintptr_t)p | (uint64_t)(ld * size)) & 15) == 0; }
+
 size_t sums_bytes(int groups, int cols) { return groups > 1 ? (size_t)groups * (size_t)cols * 4 : 0; }
 
 }  // namespace
@@ -73,7 +85,8 @@ int sgemm_mi355_rms_norm(int type, int rows, int cols, const void* X, int ldx, c
   add_quantised(m, rows, cols, Q, ldq, S, s_row, s_block);
   v = m.check();
   if (v != SGEMM_MI355_OK) return v;
-  const NormArgs a{rows, cols, X, ldx, R, ldr, W, w_type == SGEMM_MI355_F32, eps, H, ldh, rstd, Y, ldy, Q, ldq, S, s_row, s_block};
+  const NormArgs a{rows, cols, X, ldx, R, ldr, W, w_type == SGEMM_MI355_F32, eps, H, ldh, rstd, Y, ldy, Q, ldq, S, s_row, s_block,
+                   runs_of(rows, cols, size, aligned16(X, ldx, size) && aligned16(R, R ? ldr : 0, size) && aligned16(H, H ? ldh : 0, size))};
   return done(launch_norm(type, a, stream));
 }
 
@@ -105,7 +118,8 @@ int sgemm_mi355_rms_norm_backward(int type, int rows, int cols, const void* dY, 
   if (workspace_bytes < need) return SGEMM_MI355_ERR_WORKSPACE;
   const int groups = norm_groups(rows, cols);
   const NormBackArgs a{rows, cols, dY, lddy, H, ldh, rstd, W, w_type == SGEMM_MI355_F32, dH, lddh, dX, lddx,
-                       dW == nullptr ? nullptr : groups > 1 ? (float*)workspace : dW, groups};
+                       dW == nullptr ? nullptr : groups > 1 ? (float*)workspace : dW, groups,
+                       runs_of(rows, cols, size, aligned16(dX, lddx, size))};
   return done(launch_norm_backward(type, a, dW, stream));
 }
 
@@ -127,7 +141,7 @@ int sgemm_mi355_gated(int type, int act, int rows, int cols, const void* H, int 
   if (v != SGEMM_MI355_OK) return v;
   GatedArgs a{};
   a.rows = rows, a.cols = cols, a.H = H, a.ldh = ldh, a.Z = Z, a.ldz = ldz, a.Q = Q, a.ldq = ldq;
-  a.S = S, a.s_row = s_row, a.s_block = s_block;
+  a.S = S, a.s_row = s_row, a.s_block = s_block, a.runs = cols % 8 == 0 ? RUNS_WHOLE : RUNS_ANY;
   return done(launch_gated(type, act, a, stream));
 }
 
@@ -147,6 +161,8 @@ int sgemm_mi355_gated_backward(int type, int act, int rows, int cols, const void
   if (v != SGEMM_MI355_OK) return v;
   GatedArgs a{};
   a.rows = rows, a.cols = cols, a.H = H, a.ldh = ldh, a.dZ = dZ, a.lddz = lddz, a.dH = dH, a.lddh = lddh;
+  const int size = element_size(type);
+  a.runs = runs_of(rows, cols, size, aligned16(dZ, lddz, size) && aligned16(H, ldh, size) && aligned16(dH, lddh, size));
   return done(launch_gated_backward(type, act, a, stream));
 }
 
@@ -178,6 +194,8 @@ int sgemm_mi355_epilogue_backward(int type, int act, int rows, int cols, const v
   EpilogueBackArgs a{};
   a.rows = rows, a.cols = cols, a.dC = dC, a.lddc = lddc, a.P = P, a.ldp = ldp, a.dP = dP, a.lddp = lddp;
   epilogue_groups(rows, cols, a);
+  const int size = element_size(type);
+  a.runs = runs_of(rows, cols, size, aligned16(dC, lddc, size) && aligned16(P, ldp, size) && aligned16(dP, lddp, size));
   a.sums = dbias == nullptr ? nullptr : a.groups > 1 ? (float*)workspace : dbias;
   return done(launch_epilogue_backward(type, act, a, dbias, stream));
 }

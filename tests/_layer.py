@@ -17,16 +17,18 @@ def plain(x):
     return x.double().cpu().numpy()
 
 
-def activation(p, name):
-    """(value, slope, error of the value, error of the slope), the errors in U.
+def activation(p, name, short=False):
+    """(value, slope, error of the value, error of the slope), the errors in U; short: as for results of 16 bits.
 
-    exp_below is off by 4 U (power of two 2, its correction 1, products 1); a sigmoid by 4 + 1 (sum) + 2 (reciprocal) +
-    1 (product) = 8, and by what the rounding of its argument x changes it, |x| times x's relative error where it falls,
-    nothing where it is near 1 (then it is 1 - s that moves). The normal integral's tail: 4 of exp, 1 of the square, a
-    reciprocal of a rounded sum (3) that changes the polynomial by 4 times as much at most, nine steps of a polynomial
-    whose terms add up to 2.2 times its value (20 at most), 1 of the fit, 2 of products: 40. A power of two under 2^-126
-    is zero in the hardware's instruction: the sigmoid or the integral loses less than that (gelu at p = -13.4375, u =
-    4.375: exp(-p^2/2) = 6.2e-40 and z = -1.07e-39 come out as 0).
+    A sigmoid is off by 4 (exp_below: power of two 2, its correction 1, products 1) + 1 (sum) + 2 (reciprocal) + 1
+    (product) = 8, and by what the rounding of its argument x changes it, (1 - s) |x| times x's relative error. The
+    short one's exponential has no correction: its argument is off by 2 (silu: a product and its constant) or 4 (tanh: a
+    square, a fused product, a product, constants), and 1 - s is a difference, off by s's error and half a step of 1.
+    The normal integral's tail: 2 of the power of two, p^2/2 times its argument's 2, a reciprocal of a rounded sum (3)
+    that changes the polynomial by 4 times as much at most, nine steps of a polynomial whose terms add up to 2.2 times
+    its value (20 at most), 1 of the fit (144 of the short one, 8.6e-6), 2 of products: 37 (180). A power of two under
+    2^-126 is zero in the hardware's instruction: the sigmoid or the integral loses less than that (gelu at p = -13.4375,
+    u = 4.375: exp(-p^2/2) = 6.2e-40 and z = -1.07e-39 come out as 0).
     """
     lost = 2.0 ** -126 / U
     with np.errstate(over="ignore", invalid="ignore"):
@@ -34,27 +36,25 @@ def activation(p, name):
             return p, np.ones_like(p), 0 * p, 0 * p
         if name == "relu":
             return np.where(p <= 0, 0.0, p), np.where(p <= 0, 0.0, np.where(p > 0, 1.0, p)), 0 * p, 0 * p
+        q = np.clip(p, -1e4, 1e4)
+        if name == "gelu":
+            below, above, density = special.ndtr(q), special.ndtr(-q), np.exp(-0.5 * q * q) / np.sqrt(2 * np.pi)
+            value, slope = np.where(p > 1e4, p, q * below), below + q * density
+            tail = ((180 if short else 37) + q * q) * np.minimum(below, above)
+            return (value, slope, np.abs(q) * (tail + lost) + 2 * np.abs(value),
+                    tail + 2 * below + (8 + q * q) * np.abs(q) * density + (1 + np.abs(q)) * lost)
         if name == "silu":
-            s, c = special.expit(p), special.expit(-p)
-            a, b, q = p, np.ones_like(p), np.clip(p, -1e4, 1e4)
-            arg = 0.0
-        elif name == "gelu_tanh":
-            k, q = np.sqrt(2 / np.pi), np.clip(p, -1e4, 1e4)
-            a = 2 * k * (q + 0.044715 * q ** 3)
-            b = 2 * k * (1 + 3 * 0.044715 * q ** 2)
-            s, c = special.expit(a), special.expit(-a)
-            arg = np.minimum(6 * np.abs(a), 6 * 160)  # the argument has three products and a sum, and constants
+            a, b, off = q, np.ones_like(q), 2.0 if short else 0.0
         else:
-            q = np.clip(p, -1e4, 1e4)
-            below, density = special.ndtr(q), np.exp(-0.5 * q * q) / np.sqrt(2 * np.pi)
-            value, slope = q * below, below + q * density
-            value = np.where(p > 1e4, p, value)
-            return (value, slope, 42 * np.abs(value) + np.abs(q) * lost,
-                    42 * (below + np.abs(q) * density) + (1 + np.abs(q)) * lost)
-        value, slope = q * s, s + q * b * s * c
-        value = np.where(p > 1e4, p, value)
-        return (value, slope, (10 + arg) * np.abs(value) + np.abs(q) * lost,
-                (20 + 2 * arg) * (s + np.abs(q) * b * s * c) + (1 + np.abs(q) * b) * lost)
+            k = np.sqrt(2 / np.pi)
+            a, b, off = 2 * k * (q + 0.044715 * q ** 3), 2 * k * (1 + 3 * 0.044715 * q ** 2), 4.0 if short else 6.0
+        s, c = special.expit(a), special.expit(-a)
+        rel = 8 + off * np.minimum(np.abs(a), 200) * c  # of s
+        value, slope = np.where(p > 1e4, p, q * s), s + q * b * s * c
+        # 1 - s: relative in the long form, the difference's half step and s's own error in the short one
+        rest = s * c * (rel + 12 + off * np.minimum(np.abs(a), 200)) if not short else s * (1 + rel * s) + s * c * (rel + 12)
+        return (value, slope, (rel + 2) * np.abs(value) + np.abs(q) * lost,
+                (rel + 2) * s + np.abs(q) * b * rest + (1 + np.abs(q) * b) * lost)
 
 
 def quantised(Q, S, want, error):

@@ -223,7 +223,7 @@ def check_epilogue(C, P, product, size, K, kind, act, bias, residual):
     p = product + (0.0 if bias is None else bias)
     inside = R.product_bound(product, size, K, kind) - R.product_bound(product, 0 * size, K, kind) + L.U * np.abs(p)
     inside /= 1 + R.half_step(kind)[0]
-    value, _, value_error, _ = L.activation(p, act)
+    value, _, value_error, _ = L.activation(p, act, kind != "fp32")
     if P is not None:
         L.near(P, p, inside, kind)
     want = value + (0.0 if residual is None else residual)
@@ -281,7 +281,7 @@ def test_epilogue_without_a_product():
 def test_epilogue_with_fp32_sums_and_nan():
     (A, sa, B, sb), product, size = operands(300, 400, 512, 1)
     C = sg.gemm_fp8_epilogue(A, sa, B, sb, activation="silu", fp32_sums=True)
-    value, _, error, _ = L.activation(product, "silu")
+    value, _, error, _ = L.activation(product, "silu", True)
     inside = R.product_bound(product, size, 512, "fp32")
     L.near(C, value, 1.13 * inside + L.U * error, "bf16")
     residual = torch.zeros(300, 400, device="cuda", dtype=torch.bfloat16)
@@ -296,6 +296,39 @@ def test_epilogue_with_fp32_sums_and_nan():
 
 
 @pytest.mark.parametrize("act", L.ACTS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_epilogue_backward_over_the_activations_range(act, kind):
+    """Every magnitude that the type holds, both signs, the infinities and NaN."""
+    mags = np.concatenate([2.0 ** np.arange(-24, 16), np.linspace(0.01, 30, 3000), np.linspace(30, 200, 500), [0.0, 6e4]])
+    if kind != "fp16":
+        mags = np.concatenate([mags, 2.0 ** np.arange(-126, 128), [3.3e38]])
+    p = torch.from_numpy(np.concatenate([mags, -mags, [np.inf, -np.inf, np.nan]])).to(R.TYPES[kind]).to("cuda")[None]
+    dP, _ = sg.epilogue_backward(torch.ones_like(p), p, activation=act)
+    assert dP[0, -3] == 1.0 and dP[0, -2] == (1.0 if act == "none" else 0.0) and (act == "none" or bool(dP[0, -1].isnan()))
+    _, slope, _, error = L.activation(L.plain(p)[:, :-3], act, kind != "fp32")
+    L.near(dP[:, :-3], slope, L.U * (error + np.abs(slope)), kind)
+
+
+@pytest.mark.parametrize("act", L.ACTS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_epilogue_over_the_activations_range(act, kind):
+    """K = 0: p is the bias, every magnitude of it, the infinities and NaN, by each kernel's epilogue."""
+    mags = np.concatenate([2.0 ** np.arange(-24, 16), np.linspace(0.01, 30, 400), np.linspace(30, 200, 50), [0.0, 6e4]])
+    if kind != "fp16":
+        mags = np.concatenate([mags, 2.0 ** np.arange(-126, 128), [3.3e38]])
+    bias = torch.from_numpy(np.concatenate([mags, -mags, [np.inf, -np.inf, np.nan]])).float().to("cuda")
+    N = bias.numel()
+    want, _, error, _ = L.activation(L.plain(bias)[None, :-3], act, kind != "fp32")
+    for M, K in ((3, 0), (3, 128), (2000, 128), (2000, 127)):
+        A, B = torch.zeros(M, K + 1, device="cuda").to(torch.float8_e4m3fn)[:, :K], torch.zeros(N, K, device="cuda").to(torch.float8_e4m3fn)
+        sa, sb = torch.ones(M, -(-K // 128), device="cuda"), torch.ones(N, -(-K // 128), device="cuda")
+        C = sg.gemm_fp8_epilogue(A, sa, B, sb, bias=bias, activation=act, dtype=R.TYPES[kind])
+        assert bool((C[:1] == C)[:, :-1].all()) and C[0, -3] == float("inf") and bool(C[:, -1].isnan().all())
+        assert C[0, -2] == (-float("inf") if act == "none" else 0.0)
+        L.near(C[:1, :-3], want, L.U * (error + np.abs(want)), kind)
+
+
+@pytest.mark.parametrize("act", L.ACTS)
 @pytest.mark.parametrize("rows,cols,pad,offset", [(1, 1, 0, 0), (3, 127, 1, 1), (70, 128, 0, 0), (129, 129, 2, 0), (33, 512, 8, 3),
                                                   (700, 1030, 0, 0), (3000, 40, 0, 0), (5000, 600, 0, 0)])
 def test_epilogue_backward(act, rows, cols, pad, offset):
@@ -304,7 +337,7 @@ def test_epilogue_backward(act, rows, cols, pad, offset):
     P, dC = matrix(rows, cols, 1, kind, pad, offset, 1.5), matrix(rows, cols, 2, kind, pad, offset)
     dP, db = sg.epilogue_backward(dC, P, activation=act)
     torch.cuda.synchronize()
-    _, slope, _, slope_error = L.activation(L.plain(P), act)
+    _, slope, _, slope_error = L.activation(L.plain(P), act, kind != "fp32")
     dc = L.plain(dC)
     want, error = slope * dc, L.U * np.abs(dc) * (slope_error + np.abs(slope)) + 1e-37
     L.near(dP, want, error, kind)
