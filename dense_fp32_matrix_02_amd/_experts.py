@@ -8,8 +8,9 @@ from __future__ import annotations
 
 import ctypes
 
-from ._fp8 import _bind, _check, _F, _gpu, _I, _ints, _ld, _Library, _LL, _P, _result, _stream_of, _type_of, torch
-from ._layer import _launch
+from ._binding import MOST
+from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _ints, _ld, _Library, _LL, _P, _result, _stream_of, _type_of, torch
+from ._layer import _launch, _like, _matrix
 
 EXPERTS_FORWARD, EXPERTS_DGRAD, EXPERTS_WGRAD = 0, 1, 2
 
@@ -31,27 +32,31 @@ def sgemm_mi355_experts_kernel_name(form, rows, N, K, experts, A, lda, W, ldw, s
     return r.decode() if r is not None else None
 
 
-def _weights(W, A, on):
-    """Address, row stride and stride of the experts' weights, of A's type."""
-    _gpu(W, "W", A.dtype, on)
-    if W.dim() != 3 or W.shape[0] < 1:
-        raise ValueError("W must be experts x N x K")
-    return W.data_ptr(), _ld(W[0], "W"), W.stride(0)
+def _result_of(C, shape, dtype, A, on, stream):
+    """C, its type, address and row stride."""
+    if C is None:
+        kind = _type_of(dtype, "C")
+        C = _empty(shape, dtype, A.device, stream)
+        return C, kind, C.data_ptr(), shape[-1] or 1
+    C = _result(C, shape, dtype, A, on, 0.0, stream)
+    return C, _type_of(C.dtype, "C"), C.data_ptr(), _ld(C, "C")
 
 
-def _rows_by_expert(name, A, W, offsets, C, dtype, stream, inner, outer):
-    if A.dim() != 2 or W.dim() != 3:
+def _rows_by_expert(call, name, A, W, offsets, C, dtype, stream, inner, outer):
+    sizes, strides = W.shape, W.stride()
+    if len(sizes) != 3 or A.dim() != 2 or sizes[0] < 1:
         raise ValueError("A must be 2-D, W 3-D with the experts first")
-    E, N, K = W.shape
-    rows = A.shape[0]
-    if A.shape[1] != W.shape[inner]:
+    E, N, K = sizes
+    on, kind, a, lda, (rows, columns) = _matrix(A, "A")
+    if columns != sizes[inner]:
         raise ValueError("inner dimensions differ")
-    on = _gpu(A, "A")
-    w = _weights(W, A, on)
+    if W.get_device() != on or W.dtype != A.dtype:
+        _gpu(W, "W", A.dtype, on)
+    ldw = strides[1] if strides[2] == 1 and 1 < N <= MOST >= strides[1] >= K > 0 else _ld(W[0], "W")
     off = _ints(offsets, "offsets", on, E + 1)
-    C = _result(C, (rows, W.shape[outer]), dtype or A.dtype, A, on, 0.0, stream)
-    _check(_launch(getattr(_c, name), on, _type_of(A.dtype, "A"), _type_of(C.dtype, "C"), rows, N, K, E, A.data_ptr(), _ld(A, "A"),
-                   *w, off, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)), name)
+    C, c_kind, c, ldc = _result_of(C, (rows, sizes[outer]), dtype or A.dtype, A, on, stream)
+    _check(_launch(call, on, kind, c_kind, rows, N, K, E, a, lda, W.data_ptr(), ldw, strides[0], off, c, ldc,
+                   _stream_of(on, stream)), name)
     return C
 
 
@@ -63,13 +68,13 @@ def gemm_experts(A, W, offsets, C=None, *, dtype=None, stream=None):
     Rows from offsets[-1] on are set to zero. C (rows x N) is allocated with
     ``dtype`` (A's unless given, or float32) when omitted. Sums are float32.
     """
-    return _rows_by_expert("experts_gemm", A, W, offsets, C, dtype, stream, 2, 1)
+    return _rows_by_expert(_c.experts_gemm, "experts_gemm", A, W, offsets, C, dtype, stream, 2, 1)
 
 
 def gemm_experts_dgrad(A, W, offsets, C=None, *, dtype=None, stream=None):
     """The gradient of gemm_experts' rows: C[r] = A[r].W[e] for the gradient A
     (rows x N) of its result; C is rows x K. The rest as in gemm_experts."""
-    return _rows_by_expert("experts_gemm_dgrad", A, W, offsets, C, dtype, stream, 1, 2)
+    return _rows_by_expert(_c.experts_gemm_dgrad, "experts_gemm_dgrad", A, W, offsets, C, dtype, stream, 1, 2)
 
 
 def gemm_experts_wgrad(A, B, offsets, C=None, *, beta: float = 0.0, dtype=None, stream=None):
@@ -77,19 +82,25 @@ def gemm_experts_wgrad(A, B, offsets, C=None, *, beta: float = 0.0, dtype=None, 
     of A[r]^T.B[r] + beta*C[e], for the gradient A (rows x N) of its result and
     its rows B (rows x K). C is experts x N x K, allocated with ``dtype``
     (float32 unless given, or A's) when omitted."""
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError("A and B must be 2-D")
-    (rows, N), (rows_b, K) = A.shape, B.shape
-    if rows != rows_b:
-        raise ValueError("A and B must have as many rows")
-    on = _gpu(A, "A")
-    _gpu(B, "B", A.dtype, on)
+    on, kind, a, lda, (rows, N) = _matrix(A, "A")
+    if B.dim() != 2 or B.shape[0] != rows:
+        raise ValueError("A and B must be 2-D with as many rows")
+    K = B.shape[1]
+    b, ldb = _like(B, "B", A.dtype, on, (rows, K))
     off = _ints(offsets, "offsets", on)
     E = offsets.numel() - 1
     if E < 1:
         raise ValueError("offsets must have experts + 1 values")
-    C = _result(C, (E, N, K), dtype or torch.float32, A, on, beta, stream)
-    _check(_launch(_c.experts_gemm_wgrad, on, _type_of(A.dtype, "A"), _type_of(C.dtype, "C"), rows, N, K, E, A.data_ptr(),
-                   _ld(A, "A"), B.data_ptr(), _ld(B, "B"), off, beta, C.data_ptr(), _ld(C[0], "C"), C.stride(0),
+    if C is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs an input C")
+        dtype = dtype or torch.float32
+        c_kind = _type_of(dtype, "C")
+        C = _empty((E, N, K), dtype, A.device, stream)
+        ldc, apart = K or 1, N * K
+    else:
+        C = _result(C, (E, N, K), dtype, A, on, beta, stream)
+        c_kind, ldc, apart = _type_of(C.dtype, "C"), _ld(C[0], "C"), C.stride(0)
+    _check(_launch(_c.experts_gemm_wgrad, on, kind, c_kind, rows, N, K, E, a, lda, b, ldb, off, beta, C.data_ptr(), ldc, apart,
                    _stream_of(on, stream)), "experts_gemm_wgrad")
     return C

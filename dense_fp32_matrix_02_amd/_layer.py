@@ -97,6 +97,10 @@ def _room(need, device, stream):
 
 
 def _quantised_out(rows, cols, device, stream):
+    if stream is None:  # _bytes_out and _empty without their calls
+        ldq = max((cols + 15) & -16, 1)
+        return (torch.empty_strided((rows, cols), (ldq, 1), dtype=torch.float8_e4m3fn, device=device), ldq,
+                torch.empty_strided((rows, (cols + 127) // 128), (1, rows or 1), dtype=torch.float32, device=device))
     Q, ldq = _bytes_out(rows, cols, device, stream)
     return Q, ldq, _empty((rows, _blocks(cols)), torch.float32, device, stream, (1, rows or 1))
 
@@ -190,29 +194,32 @@ def gated_fp8(H, *, activation: str = "silu", wide: bool = False, stream=None):
     columns, as quantize_fp8 gives them, from its float32 values; g is the
     first half of H's columns, u the second. ``wide``: z in H's dtype too, as a
     third result. Activations: "silu", "gelu", "gelu_tanh", "relu", "none"."""
+    act = _act(activation)
     on, kind, h, ldh, rows, cols = _halves(H)
     Q, ldq, S = _quantised_out(rows, cols, H.device, stream)
     Z = _empty((rows, cols), H.dtype, H.device, stream) if wide else None
-    _check(_launch(_c.gated, on, kind, _act(activation), rows, cols, h, ldh, None if Z is None else Z.data_ptr(), cols or 1,
+    _check(_launch(_c.gated, on, kind, act, rows, cols, h, ldh, None if Z is None else Z.data_ptr(), cols or 1,
                     Q.data_ptr(), ldq, S.data_ptr(), 1, rows or 1, _stream_of(on, stream)), "gated")
     return (Q, S, Z) if wide else (Q, S)
 
 
 def gated(H, *, activation: str = "silu", stream=None):
     """z = act(g) * u in H's dtype; g is the first half of H's columns, u the second."""
+    act = _act(activation)
     on, kind, h, ldh, rows, cols = _halves(H)
     Z = _empty((rows, cols), H.dtype, H.device, stream)
-    _check(_launch(_c.gated, on, kind, _act(activation), rows, cols, h, ldh, Z.data_ptr(), cols or 1, None, 0, None, 0, 0,
+    _check(_launch(_c.gated, on, kind, act, rows, cols, h, ldh, Z.data_ptr(), cols or 1, None, 0, None, 0, 0,
                     _stream_of(on, stream)), "gated")
     return Z
 
 
 def gated_backward(dZ, H, *, activation: str = "silu", stream=None):
     """dH = [act'(g) * u * dZ | act(g) * dZ], of H's dtype, for the gradient dZ of z."""
+    act = _act(activation)
     on, kind, h, ldh, rows, cols = _halves(H)
     dz = _like(dZ, "dZ", H.dtype, on, (rows, cols))
     dH = _empty((rows, 2 * cols), H.dtype, H.device, stream)
-    _check(_launch(_c.gated_backward, on, kind, _act(activation), rows, cols, *dz, h, ldh, dH.data_ptr(), 2 * cols or 1,
+    _check(_launch(_c.gated_backward, on, kind, act, rows, cols, *dz, h, ldh, dH.data_ptr(), 2 * cols or 1,
                              _stream_of(on, stream)), "gated_backward")
     return dH
 
@@ -232,18 +239,24 @@ def gemm_fp8_epilogue(A, SA, B, SB, C=None, *, bias=None, activation=None, resid
     (M, K), (N, K2) = A.shape, B.shape
     if K != K2:
         raise ValueError("inner dimensions differ")
+    act = _act(activation)
     on = _gpu(A, "A")
     a = _operand(A, SA, "A", M, K, on)
     b = _operand(B, SB, "B", N, K, on, either=True)
     if dtype is None:
         dtype = torch.bfloat16 if residual is None else residual.dtype
-    C = _result(C, (M, N), dtype, A, on, 0.0, stream)
-    kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
+    if C is None:
+        kind = _type_of(dtype, "C")
+        C = _empty((M, N), dtype, A.device, stream)
+        c, ldc = C.data_ptr(), N or 1
+    else:
+        C = _result(C, (M, N), dtype, A, on, 0.0, stream)
+        kind, c, ldc = _type_of(C.dtype, "C"), C.data_ptr(), _ld(C, "C")
     v = None if bias is None else _vector(bias, "bias", N, on, torch.float32)
     r = (None, 0) if residual is None else _like(residual, "residual", C.dtype, on, (M, N))
     P = _empty((M, N), C.dtype, A.device, stream) if pre else None
-    _check(_launch(_c.fp8_gemm_epilogue, on, kind, M, N, K, *a[:5], *b, v, _act(activation), *r, None if P is None else P.data_ptr(),
-                                N or 1, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)), "fp8_gemm_epilogue")
+    _check(_launch(_c.fp8_gemm_epilogue, on, kind | FP32_SUMS if fp32_sums else kind, M, N, K, *a[:5], *b, v, act, *r,
+                   None if P is None else P.data_ptr(), N or 1, c, ldc, _stream_of(on, stream)), "fp8_gemm_epilogue")
     return (C, P) if pre else C
 
 
@@ -252,6 +265,7 @@ def epilogue_backward(dC, P, *, activation=None, bias: bool = True, stream=None)
     dtype, and its sum over the rows, the bias' gradient (float32; None without
     ``bias``), for the gradient dC of gemm_fp8_epilogue's result. The
     residual's gradient is dC."""
+    act = _act(activation)
     on, kind, p, ldp, shape = _matrix(P, "P")
     rows, cols = shape
     dc = _like(dC, "dC", P.dtype, on, shape)
@@ -259,7 +273,7 @@ def epilogue_backward(dC, P, *, activation=None, bias: bool = True, stream=None)
     db = _empty((cols,), torch.float32, P.device, stream) if bias else None
     need = _c.epilogue_backward_workspace_size(rows, cols) if bias else 0
     at, room = _room(need, P.device, stream)
-    _check(_launch(_c.epilogue_backward, on, kind, _act(activation), rows, cols, *dc, p, ldp, dP.data_ptr(), cols or 1,
+    _check(_launch(_c.epilogue_backward, on, kind, act, rows, cols, *dc, p, ldp, dP.data_ptr(), cols or 1,
                                 None if db is None else db.data_ptr(), at, need, _stream_of(on, stream)), "epilogue_backward")
     if bias and rows == 0:  # the C call writes nothing then
         _zero(db, stream)

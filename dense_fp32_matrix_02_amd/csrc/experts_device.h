@@ -164,15 +164,16 @@ __device__ __forceinline__ void store_experts(const ExpertsArgs& g, void* C, int
 }
 
 // A wave's accumulators to C by way of its own ROOM bytes of LDS at `out`, some
-// fragments of A's rows at a time, so that a lane stores eight neighbours and a
-// row's strip is stored at a stretch, in a loop of rows that is not unrolled:
-// its code runs once per tile. The strip begins at (wm, wn) of the tile; C has
-// rows up to rows_c.
+// fragments of A's rows at a time, so that a lane stores 16 bytes next to its
+// neighbour's and a row's strip is stored at a stretch, in a loop of rows that
+// is not unrolled: its code runs once per tile. (FP32 in two runs of 16 bytes a
+// lane, which leaves every other 16 to the next instruction: 8 experts of 512 rows, weight gradients of 4096 x 4096 233 us, 213 so.) The
+// strip begins at (wm, wn) of the tile; C has rows up to rows_c.
 template <class E, int MF, int NF, int ROOM>
 __device__ __forceinline__ void strips_to_c(const ExpertsArgs& g, const ExpertsTile& t, const f32x4 (&acc)[NF][MF], float* out,
                                             int wm, int wn, int rows_c, int lane) {
-  constexpr int WIDTH = 16 * NF, LANES = WIDTH / 8;  // floats of a row of the strip, and lanes that store one
-  constexpr int FIT = ROOM / (16 * WIDTH * 4);       // fragments that the room holds
+  constexpr int WIDTH = 16 * NF;                // floats of a row of the strip
+  constexpr int FIT = ROOM / (16 * WIDTH * 4);  // fragments that the room holds
   constexpr int ROUND = FIT >= MF ? MF : FIT >= 2 && MF % 2 == 0 ? 2 : 1;
   static_assert(FIT >= 1 && MF % ROUND == 0, "whole rounds");
   const int r16 = lane % 16, quad = lane / 16;
@@ -184,28 +185,33 @@ __device__ __forceinline__ void strips_to_c(const ExpertsArgs& g, const ExpertsT
 #pragma unroll
       for (int j = 0; j < NF; ++j) *(f32x4*)(out + (16 * i + r16) * WIDTH + 4 * ((4 * j + quad) ^ r16)) = acc[j][i0 + i];
     __builtin_amdgcn_wave_barrier();  // LDS serves a wave in order
-    const int c = 2 * (lane % LANES), n = t.n0 + wn + 4 * c;
     const int rows = min(16 * ROUND, rows_c - t.m0 - wm - 16 * i0);
-    const int64_t at = (int64_t)(t.m0 + wm + 16 * i0) * g.ldc + n;
     auto rows_to_c = [&](auto* C) __attribute__((always_inline)) {
       using T = std::remove_pointer_t<decltype(C)>;
-      auto strip = [&](int r, float (&v)[8]) __attribute__((always_inline)) {
-        *(f32x4*)v = *(const f32x4*)(out + r * WIDTH + 4 * (c ^ (r % 16)));
-        *(f32x4*)(v + 4) = *(const f32x4*)(out + r * WIDTH + 4 * ((c + 1) ^ (r % 16)));
+      constexpr int W = 16 / sizeof(T), LANES = WIDTH / W;  // values that a lane stores, and lanes that store a row
+      const int c = W / 4 * (lane % LANES), n = t.n0 + wn + 4 * c;
+      const int64_t at = (int64_t)(t.m0 + wm + 16 * i0) * g.ldc + n;
+      auto strip = [&](int r, float (&v)[W]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = 0; x < W / 4; ++x) *(f32x4*)(v + 4 * x) = *(const f32x4*)(out + r * WIDTH + 4 * ((c + x) ^ (r % 16)));
       };
-      if (g.beta == 0.0f && n + 8 <= g.N) {
+      if (g.beta == 0.0f && n + W <= g.N) {
 #pragma unroll 4
         for (int r = lane / LANES; r < rows; r += 64 / LANES) {
-          float v[8];
+          float v[W];
           strip(r, v);
-          store8(C + at + r * g.ldc, 8, v);
+          if (g.past) {
+            store16_once(C + at + r * g.ldc, v);
+          } else {
+            store_as<T, W>(C + at + r * g.ldc, W, v, 0.0f);
+          }
         }
       } else {
 #pragma unroll 1
         for (int r = lane / LANES; r < rows; r += 64 / LANES) {
-          float v[8];
+          float v[W];
           strip(r, v);
-          store_as<T, 8>(C + at + r * g.ldc, g.N - n, v, g.beta);
+          store_as<T, W>(C + at + r * g.ldc, g.N - n, v, g.beta);
         }
       }
     };

@@ -21,6 +21,7 @@ struct ExpertsArgs {
   float beta;
   void* C;
   int64_t ldc, strideC;
+  bool past;  // C goes past the caches
 };
 
 hipError_t launch_experts(ExpertsForm form, const ExpertsArgs& g, hipStream_t s);

@@ -118,6 +118,18 @@ __device__ __forceinline__ void store_as(T* c, int valid, const float (&v)[W], f
   for (int i = 0; i < W; ++i)
     if (i < valid) c[i] = from_f32<T>(beta != 0.0f ? __builtin_fmaf(beta, to_f32(c[i]), v[i]) : v[i]);
 }
+// 16 bytes of neighbours of C, past the caches.
+template <class T, int W>
+__device__ __forceinline__ void store16_once(T* c, const float (&v)[W]) {
+  static_assert(W * sizeof(T) == 16, "one store");
+  typedef int words __attribute__((ext_vector_type(4), aligned(2)));
+  T e[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) e[i] = from_f32<T>(v[i]);
+  words w;
+  __builtin_memcpy(&w, e, 16);
+  __builtin_nontemporal_store(w, (words*)c);
+}
 template <int W>
 __device__ __forceinline__ void store_c(const Fp8Args& g, void* C, int64_t at, int valid, const float (&v)[W]) {
   if (g.type == SGEMM_MI355_F32) store_as((float*)C + at, valid, v, g.beta);
@@ -133,9 +145,9 @@ __device__ __forceinline__ void finish_as(const Fp8Args& g, int64_t m, int n, in
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] += bias[i];
   auto put = [&](T* c) __attribute__((always_inline)) {
-    if constexpr (W == 8) {
-      if (g.past && valid >= 8) {
-        store8_once(c, 8, v);
+    if constexpr (W * sizeof(T) == 16) {
+      if (g.past && valid >= W) {
+        store16_once(c, v);
         return;
       }
     }

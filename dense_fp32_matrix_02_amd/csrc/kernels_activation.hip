@@ -108,22 +108,22 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(EpilogueBackArgs
 
 // out[c] = sum over the groups of P[group][c], in an order that depends on the
 // number of groups alone. A workgroup has 64 columns: 16 threads side by side,
-// 16 groups at a time.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* P, int groups, int cols, float* out) {
-  __shared__ __align__(16) float part[16][64];
+// 64 groups at a time, so that few columns have many loads on the way too.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* P, int groups, int cols, float* out) {
+  __shared__ __align__(16) float part[64][64];
   const int lane = threadIdx.x % 16, team = threadIdx.x / 16;
   const int col = blockIdx.x * 64 + 4 * lane;
   float sum[4] = {};
   if (col + 4 <= cols) {
 #pragma unroll 4
-    for (int g = team; g < groups; g += 16) {
+    for (int g = team; g < groups; g += 64) {
       float v[4];
       __builtin_memcpy(v, P + (int64_t)g * cols + col, 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] += v[i];
     }
   } else {
-    for (int g = team; g < groups; g += 16)
+    for (int g = team; g < groups; g += 64)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (col + i < cols) sum[i] += P[(int64_t)g * cols + col + i];
@@ -131,20 +131,21 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* P, int gr
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[team][4 * lane + i] = sum[i];
   __syncthreads();
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && c < cols) {
-    float total = 0.0f;
+  // 16 threads to a column, four groups' teams each, and then these in a wave's order.
+  const int c = threadIdx.x / 16, x = threadIdx.x % 16;
+  float total = part[4 * x][c];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) total += part[t][threadIdx.x];
-    out[c] = total;
-  }
+  for (int i = 1; i < 4; ++i) total += part[4 * x + i][c];
+#pragma unroll
+  for (int d = 1; d < 16; d *= 2) total += __shfl_xor(total, d, 64);
+  if (x == 0 && blockIdx.x * 64 + c < cols) out[blockIdx.x * 64 + c] = total;
 }
 
 }  // namespace
 
 hipError_t launch_column_sums(const float* sums, int groups, int cols, float* out, hipStream_t s) {
   void* args[] = {&sums, &groups, &cols, &out};
-  return hipLaunchKernel((const void*)&column_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), args, 0, s);
+  return hipLaunchKernel((const void*)&column_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), args, 0, s);
 }
 
 hipError_t launch_gated(int type, int act, const GatedArgs& a, hipStream_t s) {

@@ -10,9 +10,10 @@ namespace sgemm_impl {
 namespace {
 
 // A 128 x 128 tile by four waves of 64 x 64: operands of any alignment. Slabs
-// come through registers, the next one on the way while one is multiplied, and
+// come through registers, the next two on the way while one is multiplied, and
 // lie in LDS as in the kernel for aligned operands.
-template <int FORM, class E>
+// WIDE: rows of either operand have sixteen bytes.
+template <int FORM, class E, bool WIDE>
 __global__ void __launch_bounds__(256, 2) experts_staged_kernel(ExpertsArgs g) {
   constexpr bool ACROSS_A = FORM == EXPERTS_WGRAD, ACROSS_B = FORM != EXPERTS_FORWARD;
   constexpr int BM = 128, BN = 128, MF = 4, NF = 4, NW = 4;
@@ -27,38 +28,83 @@ __global__ void __launch_bounds__(256, 2) experts_staged_kernel(ExpertsArgs g) {
   const int wm = (wave / 2) * 64, wn = (wave % 2) * 64;
   const int rows_c = FORM == EXPERTS_WGRAD ? g.M : t.rows_a;
   const int count = (t.K + kSlab - 1) / kSlab;
-  i32x4 held[PA::REGIONS + PB::REGIONS];
-  // The 16 bytes that this lane brings of region q of a part: zeros past the summed axis' end.
-  auto fetch = [&](auto part, const uint8_t* base, int64_t ld, int first, int end, int q, int b) __attribute__((always_inline)) {
+  // What this lane brings of region q of a part in slab b: bytes [k, k + 16) of
+  // a row of `length`. Rows past the summed axis' end have none; rows past the
+  // tile's last are that one, for results that nobody stores.
+  struct Place {
+    const uint8_t* row;
+    int k, length;
+  };
+  auto place_of = [&](auto part, const uint8_t* base, int64_t ld, int first, int end, int q, int b) __attribute__((always_inline)) {
     using P = decltype(part);
     int row, in;
     P::source(wave, lane, row, in);
     row += q * P::STEP;
     if constexpr (P::ACROSS) {
-      const int k = b * kSlab + row, col = first + in / 2;
-      if (k >= t.K) return i32x4{0, 0, 0, 0};
-      return load16(base + 2 * (k * ld), 2 * col, 2 * end);
+      const int k = b * kSlab + row;
+      return Place{base + 2 * (min(k, t.K - 1) * ld), 2 * first + in, k < t.K ? 2 * end : 0};
     } else {
-      return load16(base + 2 * (min(first + row, end - 1) * ld), 2 * (b * kSlab) + in, 2 * t.K);
+      return Place{base + 2 * (min(first + row, end - 1) * ld), 2 * (b * kSlab) + in, 2 * t.K};
     }
   };
-  auto fetch_all = [&](int b) __attribute__((always_inline)) {
+  // Sixteen bytes at once, where a row's end is near its last sixteen, which are
+  // moved to their places only when they go to LDS, after the products that
+  // hide the load. (Byte by byte at the ends of rows, 16 experts of 512 rows, N
+  // 1538, K 2046, rows' gradients take 259 us; moved at once 259; so 96.)
+  auto fetch = [&](const Place& p) __attribute__((always_inline)) {
+    if constexpr (WIDE) {
+      i32x4 v;
+      __builtin_memcpy(&v, p.row + min(p.k, max(p.length, 16) - 16), 16);
+      return v;
+    } else {
+      return load16(p.row, p.k, p.length);
+    }
+  };
+  auto mended = [&](const Place& p, i32x4 v) __attribute__((always_inline)) {
+    const int skip = p.k - (p.length - 16);  // bytes that the load began too early
+    if (skip <= 0) return v;
+    uint64_t w[2];
+    __builtin_memcpy(w, &v, 16);
+    if (skip >= 8) w[0] = w[1], w[1] = 0;
+    const int bits = 8 * (skip % 8);
+    if (bits > 0) w[0] = w[0] >> bits | w[1] << (64 - bits), w[1] >>= bits;
+    if (skip >= 16) w[0] = 0;
+    __builtin_memcpy(&v, w, 16);
+    return v;
+  };
+  const int end_a = ACROSS_A ? g.M : t.rows_a, end_b = g.N;
+  typedef i32x4 Held[PA::REGIONS + PB::REGIONS];
+  auto fetch_all = [&](Held& held, int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < PA::REGIONS; ++q) held[q] = fetch(PA{}, t.A, g.lda, t.m0, ACROSS_A ? g.M : t.rows_a, q, b);
+    for (int q = 0; q < PA::REGIONS; ++q) held[q] = fetch(place_of(PA{}, t.A, g.lda, t.m0, end_a, q, b));
 #pragma unroll
-    for (int q = 0; q < PB::REGIONS; ++q) held[PA::REGIONS + q] = fetch(PB{}, t.B, g.ldb, t.n0, g.N, q, b);
+    for (int q = 0; q < PB::REGIONS; ++q) held[PA::REGIONS + q] = fetch(place_of(PB{}, t.B, g.ldb, t.n0, end_b, q, b));
+  };
+  // Whether a part's chunks of slab b may pass their rows' ends: the same for the whole tile.
+  auto mend_all = [&](Held& held, int b) __attribute__((always_inline)) {
+    if constexpr (!WIDE) return;
+    const bool last = (b + 1) * kSlab > t.K;
+    if (last || (ACROSS_A && t.m0 + BM > end_a)) {
+#pragma unroll
+      for (int q = 0; q < PA::REGIONS; ++q) held[q] = mended(place_of(PA{}, t.A, g.lda, t.m0, end_a, q, b), held[q]);
+    }
+    if (last || (ACROSS_B && t.n0 + BN > end_b)) {
+#pragma unroll
+      for (int q = 0; q < PB::REGIONS; ++q)
+        held[PA::REGIONS + q] = mended(place_of(PB{}, t.B, g.ldb, t.n0, end_b, q, b), held[PA::REGIONS + q]);
+    }
   };
   f32x4 acc[NF][MF] = {};
   const int at_a = PA::place(wm, lane), at_b = PB::place(wn, lane);
-  if (count > 0) fetch_all(0);
-#pragma unroll 1
-  for (int b = 0; b < count; ++b) {
-    uint8_t* slab = slabs[b % 2];
+  // Slab b, from registers to LDS and through the products, while slabs b + 1
+  // and b + 2 are on the way.
+  auto step = [&](Held& held, uint8_t* slab, int b) __attribute__((always_inline)) {
+    mend_all(held, b);
 #pragma unroll
     for (int q = 0; q < PA::REGIONS + PB::REGIONS; ++q) *(i32x4*)(slab + (q * NW + wave) * 1024 + 16 * lane) = held[q];
     // One barrier: the other buffer's readers passed it a slab ago.
     __syncthreads();
-    if (b + 1 < count) fetch_all(b + 1);
+    if (b + 2 < count) fetch_all(held, b + 2);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       i32x4 fa[MF];
@@ -71,6 +117,14 @@ __global__ void __launch_bounds__(256, 2) experts_staged_kernel(ExpertsArgs g) {
         for (int i = 0; i < MF; ++i) acc[j][i] = mfma16<E>(fb, fa[i], acc[j][i]);
       }
     }
+  };
+  Held even, odd;
+  if (count > 0) fetch_all(even, 0);
+  if (count > 1) fetch_all(odd, 1);
+#pragma unroll 1
+  for (int b = 0; b < count; b += 2) {
+    step(even, slabs[0], b);
+    if (b + 1 < count) step(odd, slabs[1], b + 1);
   }
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
@@ -116,8 +170,13 @@ __global__ void __launch_bounds__(64 * kRowsWaves, MF == 4 ? 2 : MF == 1 ? 6 : 4
   auto fetch = [&](Held& h, int slab, auto whole) __attribute__((always_inline)) {
     const int k = 2 * slab * kSlab + 16 * quad;
     auto chunk = [&](const uint8_t* row, int at) __attribute__((always_inline)) {
-      if constexpr (decltype(whole)::value) return *(const i32x4*)(row + at);
-      else return load16_end(row, at, 2 * t.K);
+      if constexpr (decltype(whole)::value) {
+        i32x4 v;
+        __builtin_memcpy(&v, row + at, 16);  // of any alignment
+        return v;
+      } else {
+        return load16_end(row, at, 2 * t.K);
+      }
     };
     h.b[0] = chunk(b, k), h.b[1] = chunk(b, k + 64);
 #pragma unroll
@@ -170,11 +229,16 @@ const void* rows_kernel(int bm) {
   return bm == 16 ? (const void*)&experts_rows_kernel<E, 1> : bm == 32 ? (const void*)&experts_rows_kernel<E, 2>
                                                                        : (const void*)&experts_rows_kernel<E, 4>;
 }
+template <class E, bool WIDE>
+const void* staged_kernel_of(ExpertsForm form) {
+  return form == EXPERTS_FORWARD ? (const void*)&experts_staged_kernel<EXPERTS_FORWARD, E, WIDE>
+         : form == EXPERTS_DGRAD ? (const void*)&experts_staged_kernel<EXPERTS_DGRAD, E, WIDE>
+                                 : (const void*)&experts_staged_kernel<EXPERTS_WGRAD, E, WIDE>;
+}
 template <class E>
-const void* staged_kernel(ExpertsForm form) {
-  return form == EXPERTS_FORWARD ? (const void*)&experts_staged_kernel<EXPERTS_FORWARD, E>
-         : form == EXPERTS_DGRAD ? (const void*)&experts_staged_kernel<EXPERTS_DGRAD, E>
-                                 : (const void*)&experts_staged_kernel<EXPERTS_WGRAD, E>;
+const void* staged_kernel(ExpertsForm form, const ExpertsArgs& g) {
+  const bool wide = (form == EXPERTS_WGRAD ? g.M : g.K) >= 8 && (form == EXPERTS_FORWARD || g.N >= 8);
+  return wide ? staged_kernel_of<E, true>(form) : staged_kernel_of<E, false>(form);
 }
 
 // The kernel for a call and its tile.
@@ -188,7 +252,7 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
   const bool direct = (((uintptr_t)g.A | (uintptr_t)g.B) & 15) == 0 && ((g.lda | g.ldb | g.strideB) & 7) == 0 &&
                       g.lda < 1 << 22 && g.ldb < 1 << 22 && (form == EXPERTS_WGRAD ? g.M % 8 == 0 : g.K >= 8) &&
                       (form == EXPERTS_FORWARD || g.N % 8 == 0);
-  if (!direct) return {Choice::STAGED, 128, 128, 256};
+  const Choice small = direct ? Choice{Choice::TILE, 128, 128, 256} : Choice{Choice::STAGED, 128, 128, 256};
   // The number of BM x BN tiles: an expert with rows has one tile of rows, and
   // half a tile more on average where it has many.
   const int used = g.experts < g.M ? g.experts : g.M < 1 ? 1 : g.M;
@@ -205,8 +269,8 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
   // and 63.0; 32 experts, N 2048, K 1024, of 128 rows 33.6 and 43.5, of 64 rows
   // 28.7 and 25.4; weights' gradients of 1024 rows, 2048 x 4096, 128 tiles 33.1
   // and 24.8, 4096 x 4096 41.3 and 46.2).
-  if (tiles(256, 256) >= 140 && (form == EXPERTS_WGRAD || g.M / used >= 96)) return {Choice::TILE, 256, 256, 512};
-  if (form != EXPERTS_FORWARD) return {Choice::TILE, 128, 128, 256};
+  if (direct && tiles(256, 256) >= 140 && (form == EXPERTS_WGRAD || g.M / used >= 96)) return {Choice::TILE, 256, 256, 512};
+  if (form != EXPERTS_FORWARD || g.K < 8) return small;
   // The least of the estimated times: for each round of the chip a start and
   // the slabs, or the weights at the rate that the kernel reaches, fitted to 1
   // to 32 experts of 1 to 128 rows, N and K 256 to 4096 (the choice is 1.018
@@ -216,8 +280,8 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
   // 32 rows 73, 66, 58 and 60).
   const double k = g.K / 1024.0, weights = (double)used * g.N * (double)g.K * 2.0 / 1.0e6;
   const double rounds = std::ceil(tiles(128, 128) / 512.0);
-  Choice best{Choice::TILE, 128, 128, 256};
-  double least = std::fmax(2.3 + rounds * (0.6 + 11.0 * k), 2.0 + weights / 4.8);
+  Choice best = small;
+  double least = std::fmax(2.3 + rounds * (0.6 + (direct ? 11.0 : 20.0) * k), 2.0 + weights / 4.8);
   auto offer = [&](int bm, double start, double slabs, double rate) {
     const double r = std::fmax(tiles(bm, 16) / 256.0, 1.0), time = std::fmax(3.2 + r * (start + slabs * k), 2.0 + weights / rate);
     if (time < least) best = {Choice::ROWS, bm, 16, 64 * kRowsWaves}, least = time;
@@ -248,7 +312,7 @@ hipError_t launch_experts(ExpertsForm form, const ExpertsArgs& g, hipStream_t s)
   const dim3 grid((unsigned)experts_grid(form, g, c.bm, c.bn), form == EXPERTS_WGRAD ? (unsigned)g.experts : 1u);
   const void* kernel = c.kernel == Choice::TILE   ? experts_tile_kernel_for(form, g.type, c.bm)
                        : c.kernel == Choice::ROWS ? (bf16 ? rows_kernel<__hip_bfloat16>(c.bm) : rows_kernel<__half>(c.bm))
-                                                  : (bf16 ? staged_kernel<__hip_bfloat16>(form) : staged_kernel<__half>(form));
+                                                  : (bf16 ? staged_kernel<__hip_bfloat16>(form, g) : staged_kernel<__half>(form, g));
   return launch_with(kernel, grid, dim3((unsigned)c.threads), g, s);
 }
 

@@ -280,6 +280,87 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
   constexpr int ROUND = ROOM >= MF ? MF : ROOM >= 2 && MF % 2 == 0 ? 2 : 1;
   static_assert(ROUND >= 1 && MF % ROUND == 0, "whole rounds");
   float* out = (float*)(wave < S::NW / 2 ? slab0 : slab1) + wave % (S::NW / 2) * (ROUND * 16 * WIDTH);
+  if constexpr (FORM == FP8_EPILOGUE) {
+    // The same with an epilogue: a lane stores 16 bytes next to its neighbour's
+    // (FP32 in two runs of 16 bytes a lane leave every other 16 to the next
+    // instruction: 3001 x 2047 with P 40 us, 34 so). Some rows at a time, the
+    // residual of the next ones asked for before these are stored, and of the
+    // first ones before the strip goes to LDS: past a store the compiler may not
+    // move a load (C can be the residual).
+    auto strip_to_c = [&](auto type) __attribute__((always_inline)) {
+      using T = decltype(type);
+      constexpr int W = 16 / sizeof(T), LANES = WIDTH / W, APART = 64 / LANES;  // values of a lane, lanes of a row, rows of a store
+      constexpr int MOST = 4, AT_ONCE = MOST * APART <= 16 * ROUND ? MOST : 16 * ROUND / APART;
+      static_assert(16 * ROUND % (AT_ONCE * APART) == 0, "a pass is in one round");
+      const int rows = min(16 * MF, t.rows_a - t.m0 - wm), r0 = lane / LANES;
+      const int64_t m = t.m0 + wm;
+      const int c = W / 4 * (lane % LANES), n = t.n0 + wn + 4 * c;
+      struct alignas(sizeof(T)) Run {
+        T e[W];
+      };
+      auto ask = [&](int r) __attribute__((always_inline)) {
+        Run x = {};
+        const T* at = (const T*)g.residual + (m + r) * g.ldr + n;
+        if (g.residual != nullptr && r < rows) {
+          if (n + W <= g.N) {
+            __builtin_memcpy(&x, at, sizeof(x));
+          } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+              if (n + i < g.N) x.e[i] = at[i];
+          }
+        }
+        return x;
+      };
+      float bias[W];
+      load_as(g.bias + n, g.bias != nullptr, g.N - n, bias);
+      Run next[AT_ONCE];
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) next[u] = ask(r0 + u * APART);
+      __syncthreads();  // all reads of the slabs have been made
+#pragma unroll
+      for (int i0 = 0; i0 < MF; i0 += ROUND) {
+        if (16 * i0 >= rows) break;
+#pragma unroll
+        for (int i = 0; i < ROUND; ++i)
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+            *(f32x4*)(out + (16 * i + r16) * WIDTH + 4 * ((4 * j + quad) ^ r16)) = acc[j][i0 + i];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int pass = 0; pass < 16 * ROUND; pass += AT_ONCE * APART) {
+          if (16 * i0 + pass >= rows) break;
+          Run now[AT_ONCE];
+          float v[AT_ONCE][W];
+#pragma unroll
+          for (int u = 0; u < AT_ONCE; ++u) {
+            const int r = pass + r0 + u * APART;  // past C's rows, perhaps, but in the strip
+            now[u] = next[u];
+            next[u] = ask(16 * i0 + r + AT_ONCE * APART);
+#pragma unroll
+            for (int x = 0; x < W / 4; ++x) *(f32x4*)(v[u] + 4 * x) = *(const f32x4*)(out + r * WIDTH + 4 * ((c + x) ^ (r % 16)));
+          }
+#pragma unroll
+          for (int u = 0; u < AT_ONCE; ++u) {
+            const int r = 16 * i0 + pass + r0 + u * APART;
+            float res[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) res[i] = to_f32(now[u].e[i]);
+            finish_as<T>(g, m + r, n, r < rows ? g.N - n : 0, bias, res, v[u]);
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    };
+    if (g.type == SGEMM_MI355_F32) {
+      if constexpr (WIDE) strip_to_c(float{});  // FP32 results have widened values
+    } else if (g.type == SGEMM_MI355_BF16) {
+      strip_to_c(__hip_bfloat16{});
+    } else {
+      strip_to_c(__half{});
+    }
+    return;
+  }
   __syncthreads();  // all reads of the slabs have been made
 #pragma unroll
   for (int i0 = 0; i0 < MF; i0 += ROUND) {
@@ -299,54 +380,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
     const int64_t at = (int64_t)(t.m0 + wm + 16 * i0) * g.ldc + n;
     auto rows_to_c = [&](auto* C) __attribute__((always_inline)) {
       using T = std::remove_pointer_t<decltype(C)>;
-      if constexpr (FORM == FP8_EPILOGUE) {
-        // Some rows at a time, the next ones' residual asked for before these are
-        // stored: past a store the compiler may not move a load (C can be the residual).
-        constexpr int APART = 64 / LANES, MOST = sizeof(T) == 2 ? 4 : 2, AT_ONCE = MOST * APART <= 16 * ROUND ? MOST : 16 * ROUND / APART;
-        static_assert(16 * ROUND % (AT_ONCE * APART) == 0, "the last rows of a pass are in the strip's own room");
-        const int64_t m = t.m0 + wm + 16 * i0;
-        struct alignas(sizeof(T)) Run {
-          T e[8];
-        };
-        auto ask = [&](int r) __attribute__((always_inline)) {
-          Run x = {};
-          const T* at = (const T*)g.residual + (m + r) * g.ldr + n;
-          if (g.residual != nullptr && r < rows) {
-            if (n + 8 <= g.N) {
-              __builtin_memcpy(&x, at, sizeof(x));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (n + i < g.N) x.e[i] = at[i];
-            }
-          }
-          return x;
-        };
-        float bias[8];
-        load_as(g.bias + n, g.bias != nullptr, g.N - n, bias);
-        int r0 = lane / LANES;
-        Run next[AT_ONCE];
-#pragma unroll
-        for (int u = 0; u < AT_ONCE; ++u) next[u] = ask(r0 + u * APART);
-#pragma unroll 1
-        for (; r0 < rows; r0 += AT_ONCE * APART) {
-          Run now[AT_ONCE];
-          float v[AT_ONCE][8];
-#pragma unroll
-          for (int u = 0; u < AT_ONCE; ++u) {
-            now[u] = next[u];
-            next[u] = ask(r0 + (AT_ONCE + u) * APART);
-            strip(r0 + u * APART, v[u]);  // past C's rows, but in the strip
-          }
-#pragma unroll
-          for (int u = 0; u < AT_ONCE; ++u) {
-            float res[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) res[i] = to_f32(now[u].e[i]);
-            finish_as<T>(g, m + r0 + u * APART, n, r0 + u * APART < rows ? g.N - n : 0, bias, res, v[u]);
-          }
-        }
-      } else if (g.beta == 0.0f && n + 8 <= g.N) {
+      if (g.beta == 0.0f && n + 8 <= g.N) {
 #pragma unroll 4
         for (int r = lane / LANES; r < rows; r += 64 / LANES) {
           float v[8];
@@ -362,9 +396,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) fp8_tile_kernel(Fp8Args g) {
         }
       }
     };
-    if (g.type == SGEMM_MI355_F32) {
-      if constexpr (WIDE || FORM != FP8_EPILOGUE) rows_to_c((float*)t.C);  // FP32 results have widened values
-    } else if (g.type == SGEMM_MI355_BF16) rows_to_c((__hip_bfloat16*)t.C);
+    if (g.type == SGEMM_MI355_F32) rows_to_c((float*)t.C);
+    else if (g.type == SGEMM_MI355_BF16) rows_to_c((__hip_bfloat16*)t.C);
     else rows_to_c((__half*)t.C);
     __builtin_amdgcn_wave_barrier();
   }

@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_kernel(NormArgs a) {
   }
 }
 
-// The backward pass: a team takes every groups-th row and keeps its share of dw
-// in registers; the groups' shares are added by column_sums.
+// The backward pass: the workgroups' teams take turns at the rows and keep
+// their shares of dw in registers; a workgroup's are added in the teams' order,
+// the groups' by column_sums.
 template <class T, int NT, int NC, int RUNS>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(NormBackArgs a) {
   constexpr int TEAMS = NT < 256 ? 256 / NT : 1;
@@ -133,8 +134,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(Norm
   __shared__ float room[2][NT / 64];
   TeamSum<NT, float> team_sum{room};
   const int t = threadIdx.x % NT;
-  const int group = blockIdx.x * TEAMS + threadIdx.x / NT;
-  if (group >= a.groups) return;  // a whole wave; a larger team is a workgroup with a group
+  const int group = blockIdx.x, team = threadIdx.x / NT;
   float w[NC][8], dw[NC][8];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(Norm
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
   }
-  for (int64_t row = group; row < a.rows; row += a.groups) {
+  for (int64_t row = (int64_t)group * TEAMS + team; row < a.rows; row += (int64_t)a.groups * TEAMS) {
     const float norm = a.rstd[row];
     float n[NC][8], g[NC][8], dot = 0.0f;
 #pragma unroll
@@ -172,6 +172,23 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_backward_kernel(Norm
     }
   }
   if (a.sums == nullptr) return;
+  if constexpr (TEAMS > 1) {
+    __shared__ __align__(16) float shares[TEAMS - 1][NC * NT * 8];
+    if (team > 0) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) shares[team - 1][(c * 8 + i) * NT + t] = dw[c][i];
+    }
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int x = 0; x < TEAMS - 1; ++x) dw[c][i] += shares[x][(c * 8 + i) * NT + t];
+  }
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int col = 8 * (t + NT * c);
@@ -208,17 +225,18 @@ hipError_t launch_norm(int type, const NormArgs& a, hipStream_t s) {
 }
 
 int norm_groups(int rows, int cols) {
-  const int most = cols <= 1024 ? 2048 : cols <= 4096 ? 1024 : 512;
-  return rows < most ? rows : most;
+  const int teams = cols <= 1024 ? 4 : 1, most = cols <= 1024 || cols > 4096 ? 512 : 1024;
+  const int all = rows / teams + (rows % teams != 0);
+  return all < most ? all : most;
 }
 
 hipError_t launch_norm_backward(int type, const NormBackArgs& a, float* dW, hipStream_t s) {
   const hipError_t e = by_type(type, [&](auto t) {
     using T = decltype(t);
     return by_columns(a.cols, [&](auto nt, auto nc) {
-      constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, TEAMS = NT < 256 ? 256 / NT : 1;
+      constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value;
       return by_runs(a.runs, [&](auto runs) {
-        return launch_with((const void*)&norm_backward_kernel<T, NT, NC, decltype(runs)::value>, dim3((unsigned)((a.groups + TEAMS - 1) / TEAMS)),
+        return launch_with((const void*)&norm_backward_kernel<T, NT, NC, decltype(runs)::value>, dim3((unsigned)a.groups),
                          dim3(NT < 256 ? 256 : NT), a, s);
       });
     });

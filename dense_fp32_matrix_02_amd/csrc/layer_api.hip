@@ -180,7 +180,7 @@ int sgemm_mi355_epilogue_backward(int type, int act, int rows, int cols, const v
   if (v != SGEMM_MI355_OK) return v;
   if (lddc < at_least_1(cols) || ldp < at_least_1(cols) || lddp < at_least_1(cols)) return SGEMM_MI355_ERR_LD;
   if (rows == 0 || cols == 0) return SGEMM_MI355_OK;
-  if (!launchable(((int64_t)cols + 63) / 64, 256)) return SGEMM_MI355_ERR_EXTENT;
+  if (!launchable(((int64_t)cols + 63) / 64, 1024)) return SGEMM_MI355_ERR_EXTENT;
   const size_t need = dbias != nullptr ? sgemm_mi355_epilogue_backward_workspace_size(rows, cols) : 0;
   Matrices m;
   m.dense(dC, rows, cols, lddc, element_size(type), false);

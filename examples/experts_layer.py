@@ -1,13 +1,15 @@
-"""A layer of experts in 8 bits, forward and backward, from this package's calls alone.
+"""A layer of experts in 8 or 16 bits, forward and backward, from this package's calls alone.
 
     z = silu(W1g x) * (W1u x);  y = W2 z        for each of a token's chosen experts
     out = sum over them of weight * y
 
 Weights stay in FP32 and are quantised to e4m3 by 128 x 128 tiles; activations
-and gradients by blocks of 128 of the summed axis. Run it on an MI355X from the
-repository root:
+and gradients by blocks of 128 of the summed axis. With 16 bits they are
+rounded to bfloat16 instead and nothing is quantised. Run it on an MI355X from
+the repository root:
 
     python examples/experts_layer.py
+    python examples/experts_layer.py --bits 16
     python examples/experts_layer.py --tokens 8192 --width 2048 --hidden 1024 --experts 32 --rate 0.05
 
 It fits the layer to a fixed target and prints the loss and the time of a step.
@@ -38,9 +40,12 @@ def quantized(w):
 class ExpertsLayer:
     """Weights of the router (experts x width), W1 (experts x 2 hidden x width) and W2 (experts x width x hidden)."""
 
-    def __init__(self, width, hidden, experts, choices, seed=0, device="cuda"):
+    def __init__(self, width, hidden, experts, choices, seed=0, device="cuda", bits=8):
         if width % 128 or hidden % 128:
             raise ValueError("width and hidden must be multiples of 128")
+        if bits not in (8, 16):
+            raise ValueError("bits must be 8 or 16")
+        self.bits = bits
         g = torch.Generator(device=device).manual_seed(seed)
 
         def normal(*shape):
@@ -51,7 +56,10 @@ class ExpertsLayer:
         self.load_weights()
 
     def load_weights(self):
-        """Quantises the weights; after each change of them."""
+        """Quantises or rounds the weights; after each change of them."""
+        if self.bits == 16:
+            self.r1, self.r2 = self.w1.bfloat16(), self.w2.bfloat16()
+            return
         (self.q1, self.q1t), (self.q2, self.q2t) = quantized(self.w1), quantized(self.w2)
 
     def forward(self, x):
@@ -59,32 +67,43 @@ class ExpertsLayer:
         logits = sg.matmul(x.float(), self.router.t().contiguous())
         weights, experts = sg.route(logits, self.choices)
         offsets, tokens, place = sg.route_plan(experts, self.router.shape[0])
-        h = sg.gemm_fp8_experts(*sg.quantize_fp8(x, index=tokens), *self.q1, offsets)
-        gate, up = h.float().chunk(2, dim=1)
-        z = (torch.sigmoid(gate) * gate * up).to(x.dtype)
-        y = sg.gemm_fp8_experts(*sg.quantize_fp8(z), *self.q2, offsets)
+        rows = x[tokens.long()] if self.bits == 16 else None
+        if self.bits == 16:
+            h = sg.gemm_experts(rows, self.r1, offsets)
+        else:
+            h = sg.gemm_fp8_experts(*sg.quantize_fp8(x, index=tokens), *self.q1, offsets)
+        z = sg.gated(h)
+        if self.bits == 16:
+            y = sg.gemm_experts(z, self.r2, offsets)
+        else:
+            y = sg.gemm_fp8_experts(*sg.quantize_fp8(z), *self.q2, offsets)
         out = sg.route_combine(y, place, weights)
-        return out, dict(x=x, logits=logits, weights=weights, experts=experts, offsets=offsets, tokens=tokens, place=place,
+        return out, dict(x=x, rows=rows, logits=logits, weights=weights, experts=experts, offsets=offsets, tokens=tokens, place=place,
                          h=h, z=z, y=y)
 
     def backward(self, dout, saved):
         """Gradients of x, the router's weights, W1 and W2 for the gradient of the output."""
         x, offsets, tokens, place = (saved[k] for k in ("x", "offsets", "tokens", "place"))
         dy, dweights = sg.route_combine_backward(dout, saved["y"], place, saved["weights"])
-        dz = sg.gemm_fp8_experts(*sg.quantize_fp8(dy), *self.q2t, offsets).float()
-        gate, up = saved["h"].float().chunk(2, dim=1)
-        open_ = torch.sigmoid(gate)
-        dh = torch.cat([dz * up * open_ * (1 + gate * (1 - open_)), dz * open_ * gate], 1).to(x.dtype)
-        dx_rows = sg.gemm_fp8_experts(*sg.quantize_fp8(dh), *self.q1t, offsets)
-        dw2 = sg.gemm_fp8_experts_wgrad(*sg.quantize_fp8_cols(dy, offsets=offsets),
-                                        *sg.quantize_fp8_cols(saved["z"], offsets=offsets), offsets)
-        dw1 = sg.gemm_fp8_experts_wgrad(*sg.quantize_fp8_cols(dh, offsets=offsets),
-                                        *sg.quantize_fp8_cols(x, index=tokens, offsets=offsets), offsets)
+        if self.bits == 16:
+            dz = sg.gemm_experts_dgrad(dy, self.r2, offsets)
+            dh = sg.gated_backward(dz, saved["h"])
+            dx_rows = sg.gemm_experts_dgrad(dh, self.r1, offsets)
+            dw2 = sg.gemm_experts_wgrad(dy, saved["z"], offsets)
+            dw1 = sg.gemm_experts_wgrad(dh, saved["rows"], offsets)
+        else:
+            dz = sg.gemm_fp8_experts(*sg.quantize_fp8(dy), *self.q2t, offsets)
+            dh = sg.gated_backward(dz, saved["h"])
+            dx_rows = sg.gemm_fp8_experts(*sg.quantize_fp8(dh), *self.q1t, offsets)
+            dw2 = sg.gemm_fp8_experts_wgrad(*sg.quantize_fp8_cols(dy, offsets=offsets),
+                                            *sg.quantize_fp8_cols(saved["z"], offsets=offsets), offsets)
+            dw1 = sg.gemm_fp8_experts_wgrad(*sg.quantize_fp8_cols(dh, offsets=offsets),
+                                            *sg.quantize_fp8_cols(x, index=tokens, offsets=offsets), offsets)
         dlogits = sg.route_backward(saved["logits"], saved["experts"], dweights)
         dx = sg.route_combine(dx_rows, place, torch.ones_like(saved["weights"])).float()
         dx += sg.matmul(dlogits, self.router)
         drouter = sg.gemm(dlogits, x.float(), opA=1)
-        return dict(x=dx, router=drouter, w1=dw1, w2=dw2, dy=dy, dweights=dweights, dh=dh, dz=dz, dlogits=dlogits)
+        return dict(x=dx, router=drouter, w1=dw1, w2=dw2, dy=dy, dweights=dweights, dh=dh, dz=dz, dx_rows=dx_rows, dlogits=dlogits)
 
 
 def main(argv=None):
@@ -92,8 +111,9 @@ def main(argv=None):
     for name, value in (("tokens", 2048), ("width", 512), ("hidden", 256), ("experts", 16), ("choices", 4), ("steps", 5)):
         p.add_argument(f"--{name}", type=int, default=value)
     p.add_argument("--rate", type=float, default=0.5)
+    p.add_argument("--bits", type=int, choices=(8, 16), default=8)
     a = p.parse_args(argv)
-    layer = ExpertsLayer(a.width, a.hidden, a.experts, a.choices)
+    layer = ExpertsLayer(a.width, a.hidden, a.experts, a.choices, bits=a.bits)
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn(a.tokens, a.width, generator=g, device="cuda").bfloat16()
     target = torch.randn(a.tokens, a.width, generator=g, device="cuda") * 0.1

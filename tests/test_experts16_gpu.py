@@ -97,7 +97,10 @@ def test_products(form, counts, N, K):
         print(f"[gpu] {form} {kind} {counts} {N}x{K} pad {pad} offset {offset}: {name}", flush=True)
         aligned = offset % 8 == 0 and x.stride(0) % 8 == 0 and w.stride(-2) % 8 == 0
         whole = {"forward": K >= 8, "dgrad": K % 8 == 0 and N >= 8, "wgrad": N % 8 == 0 and K % 8 == 0}[form]
-        assert name.startswith("staged") != (aligned and whole)
+        if not aligned or not whole:
+            assert name.startswith(("staged", "rows") if form == "forward" and K >= 8 else "staged")
+        else:
+            assert not name.startswith("staged")
         inner = {"forward": K, "dgrad": N, "wgrad": max(counts)}[form]
         want, size = expected(form, a, b, off.tolist())
         for c_type in (torch.float32, TYPES[kind]):
@@ -128,12 +131,25 @@ def test_larger_products_of_whole_numbers_are_exact(form, counts, N, K, kind):
     assert torch.equal(C, torch.from_numpy(want).float().to(TYPES[kind]).to("cuda"))
 
 
+ODD_ROWS = [([3, 9, 0, 16], 100, 333), ([100, 90, 128, 1, 140], 301, 327), ([30, 40, 64, 1, 61], 1001, 1031)]
+
+
+@pytest.mark.parametrize("counts,N,K", ODD_ROWS)
+def test_few_rows_of_any_alignment(counts, N, K):
+    off, rows = counts_to(counts), sum(counts)
+    for pad, offset in ((0, 0), (1, 1), (2, 3)):
+        x, w = matrix((rows, K), 1, "bf16", pad, offset), matrix((len(counts), N, K), 2, "bf16", pad, offset)
+        assert name_of("forward", rows, N, K, len(counts), x, w).startswith("rows")
+        want, size = expected("forward", x, w, off.tolist())
+        check(run("forward", x, w, off), want, size, K, "bf16")
+
+
 KERNELS = {  # calls whose kernel is known
     ("forward", "rows_16"): ([3, 9, 0, 16], 100, 328), ("forward", "rows_32"): ([100, 90, 128, 1, 140], 300, 328),
     ("forward", "rows_64"): ([30, 40, 64, 1, 61], 1000, 1032), ("forward", "tile_128x128"): ([250, 300, 280, 1, 270], 600, 72),
     ("forward", "tile_256x256"): ([2000, 1000, 1999], 4000, 136), ("dgrad", "tile_128x128"): ([100, 90, 128, 1, 140], 328, 304),
     ("dgrad", "tile_256x256"): ([2000, 1000, 1999], 136, 4000), ("wgrad", "tile_128x128"): ([100, 90, 128, 1, 140], 328, 304),
-    ("wgrad", "tile_256x256"): ([70, 1, 200, 64], 2000, 2008), ("forward", "staged_128x128"): ([100, 90, 128, 1, 140], 301, 333),
+    ("wgrad", "tile_256x256"): ([70, 1, 200, 64], 2000, 2008), ("forward", "staged_128x128"): ([250, 300, 280, 1, 270], 601, 73),
     ("dgrad", "staged_128x128"): ([100, 90, 128, 1, 140], 301, 333), ("wgrad", "staged_128x128"): ([100, 90, 128, 1, 140], 301, 333)}
 
 

@@ -35,7 +35,7 @@ def no_allocation(monkeypatch):
 NORM = dict(type=1, rows=10, cols=300, X=X, ldx=300, R=R, ldr=300, W=W, w_type=0, eps=1e-6, H=H, ldh=300, rstd=A, Y=Y, ldy=300,
             Q=Q, ldq=304, S=S, s_row=1, s_block=10, stream=0)
 BACK = dict(type=1, rows=100, cols=300, dY=Y, lddy=300, H=H, ldh=300, rstd=A, W=W, w_type=1, dH=D, lddh=300, dX=X, lddx=300, dW=G,
-            workspace=O, bytes=100 * 1200, stream=0)
+            workspace=O, bytes=25 * 1200, stream=0)
 GATED = dict(type=2, act=2, rows=10, cols=300, H=H, ldh=600, Z=Y, ldz=300, Q=Q, ldq=304, S=S, s_row=1, s_block=10, stream=0)
 GBACK = dict(type=0, act=1, rows=10, cols=300, dZ=D, lddz=300, H=H, ldh=600, dH=G, lddh=600, stream=0)
 EBACK = dict(type=0, act=3, rows=1000, cols=300, dC=C, lddc=300, P=P, ldp=300, dP=D, lddp=300, dbias=G, workspace=O, bytes=32 * 1200,
@@ -61,7 +61,7 @@ BAD = [
         (dict(cols=16385, lddy=BIG, ldh=BIG, lddh=BIG, lddx=BIG), sg.ERR_EXTENT), (dict(lddy=299), sg.ERR_LD),
         (dict(ldh=299), sg.ERR_LD), (dict(lddh=299), sg.ERR_LD), (dict(lddx=299), sg.ERR_LD), (dict(dY=None), sg.ERR_NULL),
         (dict(rstd=None), sg.ERR_NULL), (dict(dX=None), sg.ERR_NULL), (dict(workspace=None), sg.ERR_NULL),
-        (dict(bytes=100 * 1200 - 1), sg.ERR_WORKSPACE), (dict(workspace=None, bytes=0), sg.ERR_WORKSPACE),
+        (dict(bytes=25 * 1200 - 1), sg.ERR_WORKSPACE), (dict(workspace=None, bytes=0), sg.ERR_WORKSPACE),
         (dict(workspace=O + 2), sg.ERR_ALIGN), (dict(workspace=D), sg.ERR_ALIAS), (dict(dX=H), sg.ERR_ALIAS),
         (dict(dX=Y, lddx=301), sg.ERR_ALIAS), (dict(dX=D, lddx=301), sg.ERR_ALIAS), (dict(dW=W), sg.ERR_ALIAS), (dict(rows=0), sg.OK)]),
     (sg.sgemm_mi355_gated, GATED, [
@@ -81,7 +81,7 @@ BAD = [
         (dict(ldp=1), sg.ERR_LD), (dict(lddp=1), sg.ERR_LD), (dict(P=None), sg.ERR_NULL), (dict(dP=None), sg.ERR_NULL),
         (dict(dP=P), sg.ERR_ALIAS), (dict(dP=C), sg.ERR_ALIAS), (dict(dbias=P), sg.ERR_ALIAS), (dict(dbias=G + 1), sg.ERR_ALIGN),
         (dict(bytes=32 * 1200 - 1), sg.ERR_WORKSPACE), (dict(workspace=None), sg.ERR_NULL), (dict(workspace=D), sg.ERR_ALIAS),
-        (dict(rows=BIG), sg.ERR_EXTENT), (dict(rows=1, cols=1 << 30, lddc=BIG, ldp=BIG, lddp=BIG), sg.ERR_EXTENT), (dict(rows=0), sg.OK),
+        (dict(rows=BIG), sg.ERR_EXTENT), (dict(rows=1, cols=1 << 28, lddc=BIG, ldp=BIG, lddp=BIG), sg.ERR_EXTENT), (dict(rows=0), sg.OK),
         (dict(cols=0), sg.OK)]),
     (sg.sgemm_mi355_fp8_gemm_epilogue, EPILOGUE, [
         (dict(type=3), sg.ERR_TYPE), (dict(act=5), sg.ERR_OP), (dict(act=-1), sg.ERR_OP), (dict(sb_rows=2), sg.ERR_OP),
@@ -101,7 +101,7 @@ def test_refusals(fn, good, bad, code):
 
 def test_workspaces():
     norm, epilogue = sg.sgemm_mi355_rms_norm_backward_workspace_size, sg.sgemm_mi355_epilogue_backward_workspace_size
-    assert norm(1, 300) == 0 and norm(100, 300) == 100 * 300 * 4 and norm(0, 300) == 0 and norm(10, 0) == 0 and norm(10, 16385) == 0
+    assert norm(4, 300) == 0 and norm(100, 300) == 25 * 300 * 4 and norm(2, 3000) == 2 * 3000 * 4 and norm(0, 300) == 0 and norm(10, 0) == 0 and norm(10, 16385) == 0
     assert norm(BIG - 2000, 16384) <= 2048 * 16384 * 4
     assert epilogue(32, 300) == 0 and epilogue(33, 300) == 2 * 300 * 4 and epilogue(0, 3) == 0 and epilogue(3, 0) == 0
     assert epilogue(64, 100) == 0 and epilogue(65, 100) == 2 * 100 * 4 and 0 < epilogue(BIG - 2000, 8192) <= 2048 * 8192 * 4

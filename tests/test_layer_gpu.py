@@ -79,8 +79,8 @@ def test_norm_backward(kind, rows, cols, pad, offset):
         other = np.zeros((rows, cols)) if more is None else L.plain(more)
         want, want_w, error, size = L.norm_backward(L.plain(dy), L.plain(h), L.plain(rstd), L.plain(w), other)
         L.near(dX, want, error, kind)
-        # a group's rows (3 at most here) in turn, the groups by sixteens and these sixteen, and the two products
-        assert (np.abs(L.plain(dw) - want_w) <= (3 + rows / 16 + 16 + 3) * L.U * size + 1e-40).all()
+        # a team's rows (3 at most here) in turn, the four teams, the groups by 64 and these, and the two products
+        assert (np.abs(L.plain(dw) - want_w) <= (3 + 4 + rows / 64 + 8 + 3) * L.U * size + 1e-40).all()
         again = sg.rms_norm_backward(dy, h, rstd, w, dH=more)
         assert torch.equal(again[0], dX) and torch.equal(again[1], dw)
 
