@@ -222,8 +222,8 @@ __device__ __forceinline__ void strips_to_c(const ExpertsArgs& g, const ExpertsT
 }
 
 inline int64_t experts_grid(ExpertsForm form, const ExpertsArgs& g, int bm, int bn) {
-  const int64_t tiles_n = (g.N + bn - 1) / bn;
-  return tiles_n * (form == EXPERTS_WGRAD ? (int64_t)((g.M + bm - 1) / bm) : (int64_t)g.M / bm + g.experts + 1);
+  const int64_t tiles_n = ((int64_t)g.N + bn - 1) / bn;
+  return tiles_n * (form == EXPERTS_WGRAD ? ((int64_t)g.M + bm - 1) / bm : (int64_t)g.M / bm + g.experts + 1);
 }
 
 }  // namespace

@@ -257,11 +257,11 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
   // half a tile more on average where it has many.
   const int used = g.experts < g.M ? g.experts : g.M < 1 ? 1 : g.M;
   auto tiles = [&](int bm, int bn) {
-    const int64_t whole = (g.M + bm - 1) / bm;
+    const int64_t whole = ((int64_t)g.M + bm - 1) / bm;
     const int64_t tiles_m = form == EXPERTS_WGRAD ? whole * g.experts
                             : g.experts == 1      ? whole
-                            : whole + used / 2 > used ? whole + used / 2 : used;
-    return (double)(tiles_m * ((g.N + bn - 1) / bn));
+                            : whole + used / 2 > used ? whole + used / 2 : (int64_t)used;
+    return (double)tiles_m * (double)(((int64_t)g.N + bn - 1) / bn);
   };
   // 256 x 256 tiles, one to a CU, where they fill more than half of the chip
   // and have rows to fill (us, 256 x 256 and 128 x 128 tiles: 8 experts of 512

@@ -141,3 +141,8 @@ def test_no_name_where_nothing_runs(bad):
 
 def test_weights_gradients_without_rows_have_a_kernel():
     assert name(form=2, rows=0) == "tile_256x256"  # it sets them to zero
+
+
+@pytest.mark.parametrize("form", [0, 1, 2])
+def test_the_largest_sizes_have_a_name(form):
+    assert name(form=form, rows=2**31 - 1, N=2**31 - 1, K=2**31 - 1, experts=2**31 - 1, lda=2**31 - 1, ldw=2**31 - 1) in ("staged_128x128", "rows_16", "rows_32", "rows_64")

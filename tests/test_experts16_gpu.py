@@ -235,3 +235,16 @@ def test_gradients_against_the_products():
     total = sum(float((np.abs(plain(dy[s:t])) @ np.abs(plain(w[e])) * np.abs(plain(x[s:t]))).sum())
                 for e, (s, t) in enumerate(zip(off.tolist(), off.tolist()[1:])))
     assert abs(one - two) <= 600 * 2.0 ** -23 * total and abs(one - three) <= 600 * 2.0 ** -23 * total
+
+
+def test_weights_that_experts_share():
+    """A stride of 0 between experts: one matrix for all of them, read where it is."""
+    counts = [70, 0, 200, 33]
+    off, rows = counts_to(counts), sum(counts)
+    for N, K in ((136, 264), (135, 263)):
+        w = matrix((1, N, K), 1, "bf16")
+        x, dy = matrix((rows, K), 2, "bf16"), matrix((rows, N), 3, "bf16")
+        want, size = expected("forward", x, w.expand(4, N, K), off.tolist())
+        check(run("forward", x, w.expand(4, N, K), off), want, size, K, "bf16")
+        want, size = expected("dgrad", dy, w.expand(4, N, K), off.tolist())
+        check(run("dgrad", dy, w.expand(4, N, K), off), want, size, N, "bf16")
