@@ -97,13 +97,24 @@ struct ExpertsTile {
   int m0, n0;
   int K;
   void* C;
+  int pieces;  // this is one of so many of its tile
 };
 
-template <int FORM, int BM, int BN>
+// The kernel with 256 x 256 tiles, one to a CU, multiplies the tiles left for the
+// chip's last round in pieces where these fit the round: up to 64 tiles in four
+// (128 x 128), up to 128 in two (256 x 128). Us without and with pieces: 8 experts
+// of 1024 rows, N 2048, K 1024, 32 tiles left 49.3 and 40.7; rows' gradients of 8
+// of 512 rows, N and K 4096, 32 left 188 and 159; 32 of 512 rows, N 2048, K 4096,
+// 120 left 316 and 304. (That in four pieces, two rounds then: 324. 144 left in
+// halves, two rounds: 58.5 against 44.6 whole.)
+constexpr int kCUs = 256, kMostPieces = 256;
+constexpr bool splits_last_round(int form, int bm) { return form != EXPERTS_WGRAD && bm == 256; }
+
+template <int FORM, int BM, int BN, bool SPLIT = false>
 __device__ __forceinline__ bool find_experts_tile(const ExpertsArgs& g, ExpertsTile& t) {
   const int tiles_n = (g.N + BN - 1) / BN;
   t.A = (const uint8_t*)g.A, t.B = (const uint8_t*)g.B, t.C = g.C;
-  t.rows_a = g.M, t.K = g.K;
+  t.rows_a = g.M, t.K = g.K, t.pieces = 1;
   if constexpr (FORM == EXPERTS_WGRAD) {
     int tm, tn, begin, end;
     tile_coords(blockIdx.x, (g.M + BM - 1) / BM, tiles_n, 8, tm, tn);
@@ -129,9 +140,22 @@ __device__ __forceinline__ bool find_experts_tile(const ExpertsArgs& g, ExpertsT
     }
     total += (g.M - last_end + BM - 1) / BM;
     const int64_t tiles = (int64_t)total * tiles_n;
-    if (blockIdx.x >= tiles) return false;
-    const int64_t each = tiles / 8, more = tiles % 8, xcd = blockIdx.x % 8;
-    const int64_t id = xcd * each + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    int64_t whole = tiles, block = blockIdx.x, parts = tiles;
+    int pieces = 1;
+    if (SPLIT && tiles % kCUs <= kMostPieces / 2) {
+      whole -= tiles % kCUs, parts = whole;
+      if (block >= whole) pieces = tiles - whole <= kMostPieces / 4 ? 4 : 2, block -= whole, parts = (tiles - whole) * pieces;
+    }
+    if (block >= parts) return false;
+    const int64_t each = parts / 8, more = parts % 8, xcd = block % 8;
+    int64_t id = xcd * each + (xcd < more ? xcd : more) + block / 8;
+    int down = 0, right = 0;  // a piece's place in its tile
+    if (pieces > 1) {
+      const int piece = (int)(id & (pieces - 1));
+      id = whole + (pieces == 4 ? id >> 2 : id >> 1);
+      down = piece >> 1, right = piece & 1;
+    }
+    t.pieces = pieces;
     const int tm = (int)(id / tiles_n);
     t.n0 = (int)(id - (int64_t)tm * tiles_n) * BN;
     int before = 0;
@@ -144,14 +168,15 @@ __device__ __forceinline__ bool find_experts_tile(const ExpertsArgs& g, ExpertsT
         t.m0 = __builtin_amdgcn_readlane(begin, l) + (tm - before - __builtin_amdgcn_readlane(upto - own, l)) * BM;
         t.rows_a = __builtin_amdgcn_readlane(end, l);
         t.B += 2 * (e0 + l) * g.strideB;
-        return true;
+        t.m0 += down * (BM / 2), t.n0 += right * (BN / 2);
+        return !SPLIT || (t.m0 < t.rows_a && t.n0 < g.N);
       }
       before += __builtin_amdgcn_readlane(upto, 63);
     }
     // Rows no expert has: a product over nothing.
-    t.m0 = last_end + (tm - before) * BM;
+    t.m0 = last_end + (tm - before) * BM + down * (BM / 2), t.n0 += right * (BN / 2);
     t.K = 0;
-    return t.m0 < g.M;
+    return t.m0 < g.M && t.n0 < g.N;
   }
 }
 
@@ -223,7 +248,8 @@ __device__ __forceinline__ void strips_to_c(const ExpertsArgs& g, const ExpertsT
 
 inline int64_t experts_grid(ExpertsForm form, const ExpertsArgs& g, int bm, int bn) {
   const int64_t tiles_n = ((int64_t)g.N + bn - 1) / bn;
-  return tiles_n * (form == EXPERTS_WGRAD ? ((int64_t)g.M + bm - 1) / bm : (int64_t)g.M / bm + g.experts + 1);
+  return tiles_n * (form == EXPERTS_WGRAD ? ((int64_t)g.M + bm - 1) / bm : (int64_t)g.M / bm + g.experts + 1) +
+         (splits_last_round(form, bm) ? kMostPieces : 0);
 }
 
 }  // namespace

@@ -14,18 +14,16 @@
 namespace sgemm_impl {
 namespace {
 
+// The tile t of BM x BN by WM x WN waves; a slab each at slab0 and slab1, two
+// arrays, so that the compiler sees that reads of one do not wait for loads
+// into the other.
 template <int FORM, class E, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsArgs g) {
+__device__ __forceinline__ void multiply_tile(const ExpertsArgs& g, const ExpertsTile& t, uint8_t* slab0, uint8_t* slab1) {
   constexpr bool ACROSS_A = FORM == EXPERTS_WGRAD, ACROSS_B = FORM != EXPERTS_FORWARD;
   constexpr int NW = WM * WN, NT = 64 * NW, MF = BM / WM / 16, NF = BN / WN / 16;
   using PA = Part<ACROSS_A, BM, NW>;
   using PB = Part<ACROSS_B, BN, NW>;
   constexpr int REGIONS = PA::REGIONS + PB::REGIONS, BYTES_A = PA::BYTES, BYTES = BYTES_A + PB::BYTES;
-  // One array per stage, so that the compiler sees that reads of one do not
-  // wait for loads into the other.
-  __shared__ __align__(1024) uint8_t slab0[BYTES], slab1[BYTES];
-  ExpertsTile t;
-  if (!find_experts_tile<FORM, BM, BN>(g, t)) return;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
   const int rows_c = FORM == EXPERTS_WGRAD ? g.M : t.rows_a;  // C's end below the tile
@@ -165,6 +163,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsAr
   float* out = (float*)(wave < NW / 2 ? slab0 : slab1) + wave % (NW / 2) * (BYTES * 2 / NW / 4);
   __syncthreads();  // all reads of the slabs have been made
   strips_to_c<E, MF, NF, BYTES * 2 / NW>(g, t, acc, out, wm, wn, rows_c, lane);
+}
+
+// Tiles of 256 x 256 that begin a last round of the chip with few workgroups are
+// multiplied in pieces (find_experts_tile).
+template <int FORM, class E, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsArgs g) {
+  constexpr bool SPLIT = splits_last_round(FORM, BM);
+  constexpr int BYTES = 2 * kSlab * (BM + BN);
+  __shared__ __align__(1024) uint8_t slab0[BYTES], slab1[BYTES];
+  ExpertsTile t;
+  if (!find_experts_tile<FORM, BM, BN, SPLIT>(g, t)) return;
+  if constexpr (SPLIT) {
+    if (t.pieces > 1) {
+      if (t.pieces == 4) multiply_tile<FORM, E, BM / 2, BN / 2, WM, WN>(g, t, slab0, slab1);
+      else multiply_tile<FORM, E, BM, BN / 2, WM, WN>(g, t, slab0, slab1);
+      return;
+    }
+  }
+  multiply_tile<FORM, E, BM, BN, WM, WN>(g, t, slab0, slab1);
 }
 
 template <class E, int BM, int BN, int WM, int WN>

@@ -248,3 +248,25 @@ def test_weights_that_experts_share():
         check(run("forward", x, w.expand(4, N, K), off), want, size, K, "bf16")
         want, size = expected("dgrad", dy, w.expand(4, N, K), off.tolist())
         check(run("dgrad", dy, w.expand(4, N, K), off), want, size, N, "bf16")
+
+
+@pytest.mark.parametrize("form", ["forward", "dgrad"])
+@pytest.mark.parametrize("counts,left", [([3000, 100, 4900], 8), ([5, 3000, 0, 5200], 16), ([2048, 6144], 0), ([3000, 100, 7700], 96), ([2560, 2560, 7168], 128),
+                                         ([300, 3000, 100, 14100], 56), ([3000, 100, 10000], 168)])
+@pytest.mark.parametrize("wide", [2048, 2000, 1904])
+def test_the_last_round_in_pieces(form, counts, left, wide):
+    """Tiles of 256 x 256 past whole rounds of 256, in four pieces, in two or whole: every element, bit for bit."""
+    rows, spare, off, inner = sum(counts), 300, counts_to(counts), 72
+    assert sum(-(-c // 256) for c in counts) * 8 % 256 == left
+    N, K = (wide, inner) if form == "forward" else (inner, wide)
+    for extra in (0, spare):
+        x, w = matrix((rows + extra, inner), 1, "bf16", 8, whole=True), matrix((len(counts), N, K), 2, "bf16", 8, whole=True)
+        assert name_of(form, rows + extra, N, K, len(counts), x, w) == "tile_256x256"
+        x[rows:] = float("nan")
+        want = torch.zeros(rows + extra, wide, dtype=torch.float64, device="cuda")
+        for e, (s, t) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+            want[s:t] = x[s:t].double() @ (w[e].double().t().contiguous() if form == "forward" else w[e].double())
+        room = torch.full((rows + extra, wide + 8), float("nan"), device="cuda")
+        run(form, x, w, off, C=room[:, :wide])
+        assert torch.equal(room[:, :wide].double(), want) and bool(room[:, wide:].isnan().all())
+        assert torch.equal(run(form, x, w, off), want.float().bfloat16())
