@@ -263,13 +263,16 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
                             : whole + used / 2 > used ? whole + used / 2 : (int64_t)used;
     return (double)tiles_m * (double)(((int64_t)g.N + bn - 1) / bn);
   };
-  // 256 x 256 tiles, one to a CU, where they fill more than half of the chip
-  // and have rows to fill (us, 256 x 256 and 128 x 128 tiles: 8 experts of 512
-  // rows, N 2048, K 4096, 160 tiles 99.7 and 115.8, of 256 rows, 96 tiles 96.9
-  // and 63.0; 32 experts, N 2048, K 1024, of 128 rows 33.6 and 43.5, of 64 rows
-  // 28.7 and 25.4; weights' gradients of 1024 rows, 2048 x 4096, 128 tiles 33.1
-  // and 24.8, 4096 x 4096 41.3 and 46.2).
-  if (direct && tiles(256, 256) >= 140 && (form == EXPERTS_WGRAD || g.M / used >= 96)) return {Choice::TILE, 256, 256, 512};
+  // 256 x 256 tiles, one to a CU, where tiles of 128 x 128, two to a CU, would
+  // need more than one round of the chip, and where they have rows to fill (us,
+  // 256 x 256 and 128 x 128 tiles: 8 experts of 512 rows, N 2048, K 4096, 576
+  // small tiles 99.7 and 115.8, of 256 rows, 320 of them 80.8 and 64.1; 4200 rows,
+  // N and K 2048, 528 of them 41.6 and 49.2; 16 experts of 128 rows, N 2304, K
+  // 2048, 432 of them 57.2 and 44.1; weights' gradients of 1024 rows, 2048 x 4096,
+  // 512 of them 33.1 and 24.8, of 2048 rows, 2176 x 4096, 544 of them 47.4 and
+  // 54.2; 32 experts, N 2048, K 1024, of 128 rows 33.6 and 43.5, of 64 rows 28.7
+  // and 25.4).
+  if (direct && tiles(128, 128) > 2 * kCUs && (form == EXPERTS_WGRAD || g.M / used >= 96)) return {Choice::TILE, 256, 256, 512};
   if (form != EXPERTS_FORWARD || g.K < 8) return small;
   // The least of the estimated times: for each round of the chip a start and
   // the slabs, or the weights at the rate that the kernel reaches, fitted to 1
