@@ -3,8 +3,10 @@
 The computation lives in libsgemm_mi355.so (hand-written HIP for gfx950,
 C ABI in include/sgemm_mi355.h); this package only loads it and marshals
 arguments. Beside it: FP8 products with a scale for each block of 128 and their
-quantisers (include/sgemm_mi355_fp8.h), and routing to experts
-(include/sgemm_mi355_route.h). Build it with ``python -m dense_fp32_matrix_02_amd.build``.
+quantisers (include/sgemm_mi355_fp8.h), routing to experts
+(include/sgemm_mi355_route.h), norms, activations and epilogues around the
+products (include/sgemm_mi355_layer.h), and experts' products of 16-bit operands
+(include/sgemm_mi355_experts.h). Build it with ``python -m dense_fp32_matrix_02_amd.build``.
 """
 from ._binding import (  # noqa: F401
     ERR_ALIAS, ERR_ALIGN, ERR_CONFIG, ERR_DIM, ERR_EXTENT, ERR_LAUNCH, ERR_LD, ERR_NULL, ERR_OP,

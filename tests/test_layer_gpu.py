@@ -341,7 +341,7 @@ def test_epilogue_backward(act, rows, cols, pad, offset):
     dc = L.plain(dC)
     want, error = slope * dc, L.U * np.abs(dc) * (slope_error + np.abs(slope)) + 1e-37
     L.near(dP, want, error, kind)
-    # 64 rows of a group by fours or sixteens, these, the groups by sixteens and these: under 16 + 16 + 13 + 16 additions
+    # a thread's rows (8 here at most), a group's threads (16), every 64th group (3), and these by fours and pairs (8): under 64 additions
     assert (np.abs(L.plain(db) - want.sum(0)) <= error.sum(0) + 64 * L.U * np.abs(want).sum(0)).all()
     again, none = sg.epilogue_backward(dC, P, activation=act, bias=False)
     assert none is None and torch.equal(again, dP)
