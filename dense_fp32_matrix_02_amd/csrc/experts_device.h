@@ -97,7 +97,7 @@ struct ExpertsTile {
   int m0, n0;
   int K;
   void* C;
-  int pieces;  // this is one of so many of its tile
+  int rows, pieces;  // this is one of so many pieces of a tile of so many rows
 };
 
 // The kernel with 256 x 256 tiles, one to a CU, multiplies the tiles left for the
@@ -107,17 +107,90 @@ struct ExpertsTile {
 // of 512 rows, N and K 4096, 32 left 188 and 159; 32 of 512 rows, N 2048, K 4096,
 // 120 left 316 and 304. (That in four pieces, two rounds then: 324. 144 left in
 // halves, two rounds: 58.5 against 44.6 whole.)
-constexpr int kCUs = 256, kMostPieces = 256;
+constexpr int kCUs = 256, kMostPieces = 256, kLowerRows = 192;
 constexpr bool splits_last_round(int form, int bm) { return form != EXPERTS_WGRAD && bm == 256; }
 
+// Tiles of BM rows in all, of experts and then of the rows that no expert has,
+// which begin at last_end.
+template <int BM>
+__device__ __forceinline__ int count_experts_tiles(const ExpertsArgs& g, int& last_end) {
+  const int lane = threadIdx.x % 64;
+  int begin, end, upto, total = 0;
+  for (int e0 = 0; e0 < g.experts; e0 += 64) {
+    expert_tiles<BM>(g, e0, lane, begin, end, upto);
+    total += __builtin_amdgcn_readlane(upto, 63);
+    last_end = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
+  }
+  return total + (g.M - last_end + BM - 1) / BM;
+}
+
+// Workgroup `block` of `total` rows of BM x BN tiles, those of the last round in
+// pieces where SPLIT.
+template <int BM, int BN, bool SPLIT>
+__device__ __forceinline__ bool place_experts_tile(const ExpertsArgs& g, int total, int last_end, ExpertsTile& t) {
+  const int lane = threadIdx.x % 64, tiles_n = (g.N + BN - 1) / BN;
+  const int64_t tiles = (int64_t)total * tiles_n;
+  int64_t block = blockIdx.x, whole = tiles, parts = tiles;
+  int pieces = 1;
+  if (SPLIT && tiles % kCUs <= kMostPieces / 2) {
+    whole -= tiles % kCUs, parts = whole;
+    if (block >= whole) {
+      pieces = BM == 256 && tiles - whole <= kMostPieces / 4 ? 4 : 2;
+      block -= whole, parts = (tiles - whole) * pieces;
+    }
+  }
+  if (block >= parts) return false;
+  // Each XCD gets a run of neighbouring tiles, so that its L2 serves the rows
+  // they share. (Whole tiles first and partial ones last, for a shorter last
+  // round, measured 352 us against 318 for 16384 rows of 32 experts, N 2048, K
+  // 4096: the weights are then read twice.)
+  const int64_t each = parts / 8, more = parts % 8, xcd = block % 8;
+  int64_t id = xcd * each + (xcd < more ? xcd : more) + block / 8;
+  int down = 0, right = 0;  // a piece's place in its tile
+  if (pieces > 1) {
+    const int piece = (int)(id & (pieces - 1));
+    id = whole + (pieces == 4 ? id >> 2 : id >> 1);
+    down = piece >> 1, right = piece & 1;
+  }
+  t.pieces = pieces;
+  const int tm = (int)(id / tiles_n);
+  t.n0 = (int)(id - (int64_t)tm * tiles_n) * BN + right * (BN / 2);
+  int begin, end, upto, before = 0;
+  for (int e0 = 0; e0 < g.experts; e0 += 64) {
+    const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto);
+    const uint64_t past = __ballot(tm < before + upto);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      // The same in every lane: kept in scalar registers.
+      t.m0 = __builtin_amdgcn_readlane(begin, l) + (tm - before - __builtin_amdgcn_readlane(upto - own, l)) * BM + down * (BM / 2);
+      t.rows_a = __builtin_amdgcn_readlane(end, l);
+      t.B += 2 * (e0 + l) * g.strideB;
+      return !SPLIT || (t.m0 < t.rows_a && t.n0 < g.N);
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  // Rows no expert has: a product over nothing.
+  t.m0 = last_end + (tm - before) * BM + down * (BM / 2);
+  t.K = 0;
+  return t.m0 < g.M && t.n0 < g.N;
+}
+
+// Hundredths of the time of a full round of 256 x 256 tiles that so many tiles
+// take, each round of them `round`, a last one in pieces `halves` or `quarters`.
+__device__ __forceinline__ int64_t rounds_of(int64_t tiles, int round, int halves, int quarters) {
+  const int64_t left = tiles % kCUs;
+  return tiles / kCUs * round + (left == 0 ? 0 : left <= kMostPieces / 4 ? quarters : left <= kMostPieces / 2 ? halves : round);
+}
+
+// The tile of this workgroup. SPLIT: of 256 x 256 or 192 x 256 (t.rows), as the
+// experts' rows decide, which the host does not know.
 template <int FORM, int BM, int BN, bool SPLIT = false>
 __device__ __forceinline__ bool find_experts_tile(const ExpertsArgs& g, ExpertsTile& t) {
-  const int tiles_n = (g.N + BN - 1) / BN;
   t.A = (const uint8_t*)g.A, t.B = (const uint8_t*)g.B, t.C = g.C;
-  t.rows_a = g.M, t.K = g.K, t.pieces = 1;
+  t.rows_a = g.M, t.K = g.K, t.rows = BM, t.pieces = 1;
   if constexpr (FORM == EXPERTS_WGRAD) {
     int tm, tn, begin, end;
-    tile_coords(blockIdx.x, (g.M + BM - 1) / BM, tiles_n, 8, tm, tn);
+    tile_coords(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, 8, tm, tn);
     t.m0 = tm * BM, t.n0 = tn * BN;
     const int e = blockIdx.y;
     expert_rows(g.offsets, e, g.K, begin, end);
@@ -126,57 +199,23 @@ __device__ __forceinline__ bool find_experts_tile(const ExpertsArgs& g, ExpertsT
     t.C = (char*)g.C + e * g.strideC * (g.c_type == SGEMM_MI355_F32 ? 4 : 2);
     return true;
   } else {
-    // The experts' tiles of BM rows in their order, then those of the rows that
-    // no expert has. Each XCD gets a run of neighbouring tiles, so that its L2
-    // serves the rows they share. (Whole tiles first and partial ones last, for
-    // a shorter last round, measured 352 us against 318 for 16384 rows of 32
-    // experts, N 2048, K 4096: the weights are then read twice.)
-    const int lane = threadIdx.x % 64;
-    int begin, end, upto, total = 0, last_end = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 64) {
-      expert_tiles<BM>(g, e0, lane, begin, end, upto);
-      total += __builtin_amdgcn_readlane(upto, 63);
-      last_end = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
-    }
-    total += (g.M - last_end + BM - 1) / BM;
-    const int64_t tiles = (int64_t)total * tiles_n;
-    int64_t whole = tiles, block = blockIdx.x, parts = tiles;
-    int pieces = 1;
-    if (SPLIT && tiles % kCUs <= kMostPieces / 2) {
-      whole -= tiles % kCUs, parts = whole;
-      if (block >= whole) pieces = tiles - whole <= kMostPieces / 4 ? 4 : 2, block -= whole, parts = (tiles - whole) * pieces;
-    }
-    if (block >= parts) return false;
-    const int64_t each = parts / 8, more = parts % 8, xcd = block % 8;
-    int64_t id = xcd * each + (xcd < more ? xcd : more) + block / 8;
-    int down = 0, right = 0;  // a piece's place in its tile
-    if (pieces > 1) {
-      const int piece = (int)(id & (pieces - 1));
-      id = whole + (pieces == 4 ? id >> 2 : id >> 1);
-      down = piece >> 1, right = piece & 1;
-    }
-    t.pieces = pieces;
-    const int tm = (int)(id / tiles_n);
-    t.n0 = (int)(id - (int64_t)tm * tiles_n) * BN;
-    int before = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 64) {
-      const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto);
-      const uint64_t past = __ballot(tm < before + upto);
-      if (past != 0) {
-        const int l = __builtin_ctzll(past);
-        // The same in every lane: kept in scalar registers.
-        t.m0 = __builtin_amdgcn_readlane(begin, l) + (tm - before - __builtin_amdgcn_readlane(upto - own, l)) * BM;
-        t.rows_a = __builtin_amdgcn_readlane(end, l);
-        t.B += 2 * (e0 + l) * g.strideB;
-        t.m0 += down * (BM / 2), t.n0 += right * (BN / 2);
-        return !SPLIT || (t.m0 < t.rows_a && t.n0 < g.N);
+    int last_end = 0;
+    const int total = count_experts_tiles<BM>(g, last_end);
+    // Tiles of 192 rows where they fill the chip's rounds better: as many in one
+    // round do less, in less time (us, 256 and 192 rows: rows' gradients of 8
+    // experts of 1024 rows, N 2048, K 1024, 144 and 192 tiles 45.6 and 38.3; of
+    // 32 of 256 rows, N 4096, K 1024, 192 and 256 tiles 107.7 and 96.3; 8192
+    // rows, N 8192, K 4096, 1024 and 1376 tiles 437 and 554). A short axis is all
+    // start and end (6144 rows, N 2048, 192 and 256 tiles: K 8192 186 and 174, K
+    // 2048 45.9 and 46.3, K 256 14.8 and 16.9).
+    if constexpr (SPLIT) {
+      const int lower = count_experts_tiles<kLowerRows>(g, last_end), tiles_n = (g.N + BN - 1) / BN;
+      if (g.K >= 512 && rounds_of((int64_t)lower * tiles_n, 88, 54, 54) < rounds_of((int64_t)total * tiles_n, 100, 60, 40)) {
+        t.rows = kLowerRows;
+        return place_experts_tile<kLowerRows, BN, true>(g, lower, last_end, t);
       }
-      before += __builtin_amdgcn_readlane(upto, 63);
     }
-    // Rows no expert has: a product over nothing.
-    t.m0 = last_end + (tm - before) * BM + down * (BM / 2), t.n0 += right * (BN / 2);
-    t.K = 0;
-    return t.m0 < g.M && t.n0 < g.N;
+    return place_experts_tile<BM, BN, SPLIT>(g, total, last_end, t);
   }
 }
 
@@ -248,7 +287,8 @@ __device__ __forceinline__ void strips_to_c(const ExpertsArgs& g, const ExpertsT
 
 inline int64_t experts_grid(ExpertsForm form, const ExpertsArgs& g, int bm, int bn) {
   const int64_t tiles_n = ((int64_t)g.N + bn - 1) / bn;
-  return tiles_n * (form == EXPERTS_WGRAD ? ((int64_t)g.M + bm - 1) / bm : (int64_t)g.M / bm + g.experts + 1) +
+  return tiles_n * (form == EXPERTS_WGRAD ? ((int64_t)g.M + bm - 1) / bm
+                                         : (int64_t)g.M / (splits_last_round(form, bm) ? kLowerRows : bm) + g.experts + 1) +
          (splits_last_round(form, bm) ? kMostPieces : 0);
 }
 

@@ -183,6 +183,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) experts_tile_kernel(ExpertsAr
   ExpertsTile t;
   if (!find_experts_tile<FORM, BM, BN, SPLIT>(g, t)) return;
   if constexpr (SPLIT) {
+    if (t.rows == kLowerRows) {
+      if (t.pieces == 1) multiply_tile<FORM, E, kLowerRows, BN, WM, WN>(g, t, slab0, slab1);
+      else multiply_tile<FORM, E, kLowerRows, BN / 2, WM, WN>(g, t, slab0, slab1);
+      return;
+    }
     if (t.pieces > 1) {
       if (t.pieces == 4) multiply_tile<FORM, E, BM / 2, BN / 2, WM, WN>(g, t, slab0, slab1);
       else multiply_tile<FORM, E, BM, BN / 2, WM, WN>(g, t, slab0, slab1);

@@ -50,7 +50,8 @@ int sgemm_mi355_experts_gemm_wgrad(int type, int c_type, int rows, int N, int K,
 /*
  * Name of the kernel that a call with these arguments runs (host only; the
  * pointers are inspected, never read): staged_*, rows_* or tile_*, then its tile of C (rows_*:
- * the rows of A in it). form: one of the three below; W is B, and strideW
+ * the rows of A in it; tile_256x256 takes tiles of 192 rows, or the last ones in pieces, where the
+ * experts' rows, which only the device knows, fill the chip better so). form: one of the three below; W is B, and strideW
  * unused, in the weights' form. Null where nothing would be launched.
  */
 #define SGEMM_MI355_EXPERTS_FORWARD 0

@@ -270,3 +270,23 @@ def test_the_last_round_in_pieces(form, counts, left, wide):
         run(form, x, w, off, C=room[:, :wide])
         assert torch.equal(room[:, :wide].double(), want) and bool(room[:, wide:].isnan().all())
         assert torch.equal(run(form, x, w, off), want.float().bfloat16())
+
+
+@pytest.mark.parametrize("form", ["forward", "dgrad"])
+@pytest.mark.parametrize("counts,wide", [([1100] * 8, 1024), ([300] * 24, 2048), ([300, 0, 301] * 12, 2000), ([1, 500] * 13 + [190] * 4, 1904), ([6144], 2048)])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_tiles_of_fewer_rows(form, counts, wide, kind):
+    """Experts that fill rounds of 192-row tiles better, whole and in halves, and some that do not: every element, bit for bit."""
+    rows, off, inner = sum(counts), counts_to(counts), 520
+    N, K = (wide, inner) if form == "forward" else (inner, wide)
+    for spare in (0, 200):
+        x, w = matrix((rows + spare, inner), 1, kind, 8, whole=True), matrix((len(counts), N, K), 2, kind, 8, whole=True)
+        assert name_of(form, rows + spare, N, K, len(counts), x, w) == "tile_256x256"
+        x[rows:] = float("nan")
+        want = torch.zeros(rows + spare, wide, dtype=torch.float64, device="cuda")
+        for e, (s, t) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+            want[s:t] = x[s:t].double() @ (w[e].double().t().contiguous() if form == "forward" else w[e].double())
+        room = torch.full((rows + spare, wide + 8), float("nan"), device="cuda")
+        run(form, x, w, off, C=room[:, :wide])
+        assert torch.equal(room[:, :wide].double(), want) and bool(room[:, wide:].isnan().all())
+        assert torch.equal(run(form, x, w, off), want.float().to(TYPES[kind]))
