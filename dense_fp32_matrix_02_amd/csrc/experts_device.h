@@ -45,6 +45,29 @@ __device__ __forceinline__ s16x4 read_transposed(const uint8_t* p) {
 #endif
 }
 
+// Sixteen bytes whose address is a multiple of two only, as a load of them from
+// the next multiple of four and a load of the first value: one load of that
+// alignment takes four times as long (the few-rows kernel, 64 rows of 16
+// experts, N 2048, K 4095: 148 us, 65 so). Two bytes more than the sixteen are
+// read.
+struct OddChunk {
+  i32x4 v;
+  uint32_t first, odd;
+};
+__device__ __forceinline__ OddChunk load_odd(const uint8_t* p) {
+  OddChunk c;
+  c.odd = (uint32_t)(uintptr_t)p & 2;
+  __builtin_memcpy(&c.v, __builtin_assume_aligned(p + c.odd, 4), 16);
+  c.first = *(const uint16_t*)p;
+  return c;
+}
+__device__ __forceinline__ i32x4 in_place(const OddChunk& c) {
+  if (c.odd == 0) return c.v;
+  return i32x4{(int)(c.first | (uint32_t)c.v[0] << 16), (int)__builtin_amdgcn_alignbit(c.v[1], c.v[0], 16),
+               (int)__builtin_amdgcn_alignbit(c.v[2], c.v[1], 16), (int)__builtin_amdgcn_alignbit(c.v[3], c.v[2], 16)};
+}
+__device__ __forceinline__ i32x4 in_place(const i32x4& v) { return v; }
+
 // An operand's part of a slab: BX rows (or, ACROSS, columns) of the tile.
 template <bool ACROSS_, int BX, int NW>
 struct Part {

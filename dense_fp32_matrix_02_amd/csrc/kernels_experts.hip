@@ -144,8 +144,9 @@ constexpr int kRowsWaves = 8;
 // FORWARD with few rows (a decoding step): a workgroup has 16 rows of an
 // expert's weights and 16*MF of A over the whole of K. Its waves take every
 // eighth slab, straight from memory to registers, and their sums are added in
-// wave order through LDS. Bound by the weights' bytes.
-template <class E, int MF>
+// wave order through LDS. Bound by the weights' bytes. ODD: rows need not begin
+// at a multiple of four bytes.
+template <class E, int MF, bool ODD>
 __global__ void __launch_bounds__(64 * kRowsWaves, MF == 4 ? 2 : MF == 1 ? 6 : 4) experts_rows_kernel(ExpertsArgs g) {
   constexpr int BM = 16 * MF, BN = 16, NW = kRowsWaves;
   constexpr int AHEAD = 2;  // slabs that a wave has in flight
@@ -163,52 +164,61 @@ __global__ void __launch_bounds__(64 * kRowsWaves, MF == 4 ? 2 : MF == 1 ? 6 : 4
     a[i] = t.A + 2 * ((there[i] ? t.m0 + 16 * i + r16 : t.m0) * g.lda);
   }
   f32x4 acc[MF] = {};
+  using Chunk = std::conditional_t<ODD, OddChunk, i32x4>;
   struct Held {
+    Chunk b[2], a[MF][2];
+  };
+  struct HeldEnd {
     i32x4 b[2], a[MF][2];
   };
-  // `whole`: no value of the slab lies past K.
-  auto fetch = [&](Held& h, int slab, auto whole) __attribute__((always_inline)) {
-    const int k = 2 * slab * kSlab + 16 * quad;
-    auto chunk = [&](const uint8_t* row, int at) __attribute__((always_inline)) {
-      if constexpr (decltype(whole)::value) {
-        i32x4 v;
-        __builtin_memcpy(&v, row + at, 16);  // of any alignment
-        return v;
-      } else {
-        return load16_end(row, at, 2 * t.K);
-      }
-    };
-    h.b[0] = chunk(b, k), h.b[1] = chunk(b, k + 64);
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      h.a[i][0] = h.a[i][1] = i32x4{0, 0, 0, 0};
-      if (there[i]) h.a[i][0] = chunk(a[i], k), h.a[i][1] = chunk(a[i], k + 64);
+  auto chunk = [&](const uint8_t* p) __attribute__((always_inline)) {
+    if constexpr (ODD) {
+      return load_odd(p);
+    } else {
+      i32x4 v;
+      __builtin_memcpy(&v, __builtin_assume_aligned(p, 4), 16);
+      return v;
     }
   };
-  auto multiply = [&](const Held& h) __attribute__((always_inline)) {
+  auto fetch_with = [&](auto& h, int slab, auto&& load) __attribute__((always_inline)) {
+    const int k = 2 * slab * kSlab + 16 * quad;
+    h.b[0] = load(b, k), h.b[1] = load(b, k + 64);
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int i = 0; i < MF; ++i) acc[i] = mfma16<E>(h.b[x], h.a[i][x], acc[i]);
+    for (int i = 0; i < MF; ++i) {
+      h.a[i][0] = h.a[i][1] = {};
+      if (there[i]) h.a[i][0] = load(a[i], k), h.a[i][1] = load(a[i], k + 64);
+    }
   };
-  const int full = t.K / kSlab;
+  auto fetch = [&](Held& h, int slab) __attribute__((always_inline)) {
+    fetch_with(h, slab, [&](const uint8_t* row, int at) __attribute__((always_inline)) { return chunk(row + at); });
+  };
+  auto multiply = [&](const auto& h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const i32x4 fb = in_place(h.b[x]);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) acc[i] = mfma16<E>(fb, in_place(h.a[i][x]), acc[i]);
+    }
+  };
+  // Slabs that can be loaded whole, with ODD's two bytes behind them, and one that cannot.
+  const int full = (t.K - (ODD ? 1 : 0)) / kSlab;
   int slab = wave;
   for (; slab + (AHEAD - 1) * NW < full; slab += NW * AHEAD) {
     Held h[AHEAD];
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) fetch(h[u], slab + u * NW, std::true_type{});
+    for (int u = 0; u < AHEAD; ++u) fetch(h[u], slab + u * NW);
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) multiply(h[u]);
   }
 #pragma unroll 1
   for (; slab < full; slab += NW) {
     Held h;
-    fetch(h, slab, std::true_type{});
+    fetch(h, slab);
     multiply(h);
   }
-  if (slab == full && t.K % kSlab != 0) {  // the wave whose turn the partial slab is
-    Held h;
-    fetch(h, slab, std::false_type{});
+  if (slab == full && t.K > full * kSlab) {  // the wave whose turn the last slab is
+    HeldEnd h;
+    fetch_with(h, slab, [&](const uint8_t* row, int at) __attribute__((always_inline)) { return load16_end(row, at, 2 * t.K); });
     multiply(h);
   }
 #pragma unroll
@@ -224,10 +234,17 @@ __global__ void __launch_bounds__(64 * kRowsWaves, MF == 4 ? 2 : MF == 1 ? 6 : 4
   }
 }
 
+template <class E, bool ODD>
+const void* rows_kernel_of(int bm) {
+  return bm == 16   ? (const void*)&experts_rows_kernel<E, 1, ODD>
+         : bm == 32 ? (const void*)&experts_rows_kernel<E, 2, ODD>
+                    : (const void*)&experts_rows_kernel<E, 4, ODD>;
+}
+// Whether some row or expert begins at no multiple of four bytes.
+bool odd_rows(const ExpertsArgs& g) { return (((uintptr_t)g.A | (uintptr_t)g.B) & 2) != 0 || ((g.lda | g.ldb | g.strideB) & 1) != 0; }
 template <class E>
-const void* rows_kernel(int bm) {
-  return bm == 16 ? (const void*)&experts_rows_kernel<E, 1> : bm == 32 ? (const void*)&experts_rows_kernel<E, 2>
-                                                                       : (const void*)&experts_rows_kernel<E, 4>;
+const void* rows_kernel(const ExpertsArgs& g, int bm) {
+  return odd_rows(g) ? rows_kernel_of<E, true>(bm) : rows_kernel_of<E, false>(bm);
 }
 template <class E, bool WIDE>
 const void* staged_kernel_of(ExpertsForm form) {
@@ -284,14 +301,20 @@ Choice choose(ExpertsForm form, const ExpertsArgs& g) {
   const double k = g.K / 1024.0, weights = (double)used * g.N * (double)g.K * 2.0 / 1.0e6;
   const double rounds = std::ceil(tiles(128, 128) / 512.0);
   Choice best = small;
-  double least = std::fmax(2.3 + rounds * (0.6 + (direct ? 11.0 : 20.0) * k), 2.0 + weights / 4.8);
+  // Rows that begin at odd multiples of two bytes cost the few-rows kernel loads
+  // and shifts by the rows that there are, and the staged kernel less (16 experts,
+  // us, few rows at best and staged: 1224 rows, N 604, K 1817 53 and 36, K 1818 28
+  // and 29; 64 rows, N 2048, K 4095 65 and 91).
+  const bool odd = odd_rows(g);
+  double least = std::fmax(2.3 + rounds * (0.6 + (direct ? 11.0 : odd ? 20.0 : 14.0) * k), 2.0 + weights / 4.8);
   auto offer = [&](int bm, double start, double slabs, double rate) {
     const double r = std::fmax(tiles(bm, 16) / 256.0, 1.0), time = std::fmax(3.2 + r * (start + slabs * k), 2.0 + weights / rate);
     if (time < least) best = {Choice::ROWS, bm, 16, 64 * kRowsWaves}, least = time;
   };
-  offer(64, 1.08, 1.65, 5.0);
-  offer(32, 0.76, 1.58, 5.0);
-  offer(16, 0.58, 1.43, 5.7);
+  const double each = (double)g.M / used;  // rows of an expert
+  offer(64, 1.08, odd ? 1.9 + 3.9 * std::fmin(each / 64.0, 1.0) : 1.65, odd ? 4.0 : 5.0);
+  offer(32, 0.76, odd ? 1.55 + 1.7 * std::fmin(each / 32.0, 1.0) : 1.58, 5.0);
+  offer(16, 0.58, odd ? 1.4 + 0.75 * std::fmin(each / 16.0, 1.0) : 1.43, odd ? 5.0 : 5.7);
   return best;
 }
 
@@ -314,7 +337,7 @@ hipError_t launch_experts(ExpertsForm form, const ExpertsArgs& g, hipStream_t s)
   const bool bf16 = g.type == SGEMM_MI355_BF16;
   const dim3 grid((unsigned)experts_grid(form, g, c.bm, c.bn), form == EXPERTS_WGRAD ? (unsigned)g.experts : 1u);
   const void* kernel = c.kernel == Choice::TILE   ? experts_tile_kernel_for(form, g.type, c.bm)
-                       : c.kernel == Choice::ROWS ? (bf16 ? rows_kernel<__hip_bfloat16>(c.bm) : rows_kernel<__half>(c.bm))
+                       : c.kernel == Choice::ROWS ? (bf16 ? rows_kernel<__hip_bfloat16>(g, c.bm) : rows_kernel<__half>(g, c.bm))
                                                   : (bf16 ? staged_kernel<__hip_bfloat16>(form, g) : staged_kernel<__half>(form, g));
   return launch_with(kernel, grid, dim3((unsigned)c.threads), g, s);
 }
