@@ -32,18 +32,21 @@ int check(ExpertsForm form, const ExpertsArgs& g, int rows) {
   return m.check();
 }
 
-int run(ExpertsForm form, const ExpertsArgs& g, int rows, hipStream_t stream) {
+int run(ExpertsForm form, ExpertsArgs g, int rows, hipStream_t stream) {
   const int v = check(form, g, rows);
   if (v != SGEMM_MI355_OK || g.M == 0 || g.N == 0) return v;
+  // A single row has no stride that could keep it from direct loads.
+  if (rows == 1) g.lda = (g.lda + 7) / 8 * 8;
+  if ((form == EXPERTS_FORWARD ? g.N : form == EXPERTS_DGRAD ? g.K : rows) == 1) g.ldb = (g.ldb + 7) / 8 * 8;
+  if (g.experts == 1) g.strideB = 0;
   if (!experts_launchable(form, g)) return SGEMM_MI355_ERR_EXTENT;
   // Past the caches go results that they do not hold for whoever comes next, as
   // long as rows share no lines (weights' gradients of 8 experts of 512 rows,
   // 4096 x 4096 FP32: 181 us against 213 through them).
-  ExpertsArgs a = g;
   const int size = element_size(g.c_type);
-  a.past = (int64_t)(form == EXPERTS_WGRAD ? g.experts : 1) * g.M * g.N * size >= (int64_t)64 << 20 &&
+  g.past = (int64_t)(form == EXPERTS_WGRAD ? g.experts : 1) * g.M * g.N * size >= (int64_t)64 << 20 &&
            (((uintptr_t)g.C | (uint64_t)(g.ldc * size) | (uint64_t)(g.strideC * size)) & 15) == 0;
-  return done(launch_experts(form, a, stream));
+  return done(launch_experts(form, g, stream));
 }
 
 }  // namespace
