@@ -256,6 +256,17 @@ def test_epilogue(kind, M, N, K, tall):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", [(1, 500, 1559), (1, 70, 100), (60, 1, 333), (1, 1, 1001)])
+def test_epilogue_of_single_rows(kind, M, N, K):
+    """A row's stride is its length where there is one row: any number."""
+    g = torch.Generator().manual_seed(6)
+    bias, residual = torch.randn(N, generator=g).to("cuda"), torch.randn(M, N, generator=g).to(R.TYPES[kind]).to("cuda")
+    (A, sa, B, sb), product, size = operands(M, N, K, 1)
+    C, P = sg.gemm_fp8_epilogue(A, sa, B, sb, bias=bias, activation="gelu", residual=residual, pre=True)
+    check_epilogue(C, P, product, size, K, kind, "gelu", L.plain(bias), L.plain(residual))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("pad,offset", [(4, 0), (3, 5)])
 def test_epilogue_of_any_alignment(kind, pad, offset):
     M, N, K = 200, 270, 333
