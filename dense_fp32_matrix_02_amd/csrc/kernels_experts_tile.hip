@@ -11,7 +11,8 @@
 //
 // 256 x 256 tiles by eight waves of 64 x 128, one workgroup to a CU: a wave's
 // slab is 64 matrix instructions for 24 reads of 16 bytes, and LDS holds two
-// slabs of 64 KiB. Where these are too few for the chip, 128 x 128 by four
+// slabs of 64 KiB; or 192 x 256, and pieces of either, where rounds of the chip
+// are better filled so. Where these are too few for the chip, 128 x 128 by four
 // waves, two to a CU. Bound by the matrix unit and the power it may draw: one
 // expert of 8192 rows, N 8192, K 4096 bf16 440 us (1.25 PFLOP/s, half of its
 // cycles busy); 32 ragged ones of 512 rows on average, N 2048, K 4096 304 us
