@@ -88,45 +88,36 @@ __device__ __forceinline__ void activation(float p, float& value, float& slope) 
   }
 }
 
-// The same for results that are rounded to 16 bits, in a third of the
-// instructions: a product's epilogue, and its way back, are bound by them (8192
-// x 8192 results with K 4096, the tanh form, with P: 246 us against 257). s =
-// 1 / (1 + exp(-x)) as it stands, so that it loses |x| steps of FP32 where it is small, and 1 - s
-// half a step of 1; Phi with a polynomial off by 8.6e-6 (half a step of fp16
-// is 4.9e-4).
+// act'(p) for P of 16 bits, in fewer instructions where a sigmoid is all of it
+// (8192 x 8192 bf16, an epilogue's way back: SiLU 74 us against 79, the tanh form
+// 74 against 78). s = 1 / (1 + exp(-x)) as it stands, so that s and 1 - s lose |x|
+// steps of FP32 where they are small, and the slope, which has their product, a few
+// steps of 1: the bias' gradient is an FP32 sum of these. (A polynomial for GELU off by
+// 8.6e-6 saves 1 us of 76 and puts that sum off by 2.6e-6.)
 template <int ACT>
-__device__ __forceinline__ void activation16(float p, float& value, float& slope) {
+__device__ __forceinline__ float slope16(float p) {
   if constexpr (ACT == SGEMM_MI355_SILU) {
-    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p * -kLog2eF));
-    value = fmaxf(p, -kMost) * s;
-    slope = __builtin_fmaf(limited(p, 104.0f) * (1.0f - s), s, s);
-  } else if constexpr (ACT == SGEMM_MI355_GELU) {
-    const float e = __builtin_amdgcn_exp2f(p * p * (-0.5f * kLog2eF));
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.46f, fabsf(p), 1.0f));
-    float f = 0.07222823139699422f;
-    f = __builtin_fmaf(f, t, -0.23654518202696215f);
-    f = __builtin_fmaf(f, t, 0.17780173501059884f);
-    f = __builtin_fmaf(f, t, 0.11610638975355263f);
-    f = __builtin_fmaf(f, t, 0.18706677743249758f);
-    f = __builtin_fmaf(f, t, 0.18334633299676129f);
-    const float tail = e * (f * t), below = p < 0.0f ? tail : 1.0f - tail;
-    value = fmaxf(p, -kMost) * below;
-    slope = __builtin_fmaf(limited(p, 20.0f) * 0.3989422804014327f, e, below);
+    const float e = __builtin_amdgcn_exp2f(p * -kLog2eF), s = __builtin_amdgcn_rcpf(1.0f + e);
+    return __builtin_fmaf(limited(p, 104.0f) * (fminf(e, kMost) * s), s, s);  // an infinite e has s = 0
   } else if constexpr (ACT == SGEMM_MI355_GELU_TANH) {
     constexpr float a = -kTwoA * kLog2eF, b = -kTwoA * kLog2eF * kB;
-    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p * __builtin_fmaf(b, p * p, a)));
+    const float e = __builtin_amdgcn_exp2f(p * __builtin_fmaf(b, p * p, a)), s = __builtin_amdgcn_rcpf(1.0f + e);
     const float q = limited(p, 12.0f);
-    value = fmaxf(p, -kMost) * s;
-    slope = __builtin_fmaf(q * (1.0f - s) * __builtin_fmaf(3.0f * kTwoA * kB, q * q, kTwoA), s, s);
+    return __builtin_fmaf(q * (fminf(e, kMost) * s) * __builtin_fmaf(3.0f * kTwoA * kB, q * q, kTwoA), s, s);
   } else {
+    float value, slope;
     activation<ACT>(p, value, slope);
+    return slope;
   }
 }
 
 // The values of W arguments of an activation that the whole launch shares, in
 // little code: it is fetched once for each tile of a product. SiLU and the tanh
 // form of GELU are one expression, p sigmoid(a p + b p^3), with other numbers.
-// SHORT: for results of 16 bits.
+// SHORT: for values that are rounded to 16 bits as they are, s = 1 / (1 +
+// exp(-x)) as it stands, which loses |x| steps of FP32 where it is small and takes
+// a third of the instructions (8192 x 8192 results with K 4096, the tanh form,
+// with P: 246 us against 257).
 template <bool SHORT, int W>
 __device__ __forceinline__ void activate(int act, float (&v)[W]) {
   if (act == SGEMM_MI355_SILU || act == SGEMM_MI355_GELU_TANH) {
@@ -154,8 +145,7 @@ __device__ __forceinline__ void activate(int act, float (&v)[W]) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       float value, slope;
-      if constexpr (SHORT) activation16<SGEMM_MI355_GELU>(v[i], value, slope);
-      else activation<SGEMM_MI355_GELU>(v[i], value, slope);
+      activation<SGEMM_MI355_GELU>(v[i], value, slope);
       v[i] = value;
     }
   } else if (act == SGEMM_MI355_RELU) {

@@ -1,0 +1,53 @@
+"""FP32 results of 16-bit matrices: the bias' gradient and activations to which something is added before the rounding."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+from scipy import special
+
+import dense_fp32_matrix_02_amd as sg
+from tests import _fp8 as R
+from tests import _gpu as G
+from tests import _layer as L
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["fp32", "bf16", "fp16"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu_ready():
+    G.require_gpu()
+
+
+def arguments(kind):
+    """Every magnitude that an activation tells apart, both signs, as the type holds them."""
+    mags = np.concatenate([2.0 ** np.arange(-24, 8), np.linspace(0.001, 12, 4000), np.linspace(12, 200, 500), [0.0]])
+    return torch.from_numpy(np.concatenate([mags, -mags])).to(R.TYPES[kind])
+
+
+@pytest.mark.parametrize("act", L.ACTS)
+@pytest.mark.parametrize("kind", KINDS)
+def test_bias_gradient_is_an_fp32_value(act, kind):
+    """Of a single row the sum is the FP32 value of dP itself: off by the long slope's error, and SiLU's by what an
+    exponent without correction (off by two roundings) changes s and 1 - s by."""
+    p = arguments(kind).to("cuda")[None]
+    _, db = sg.epilogue_backward(torch.ones_like(p), p, activation=act)
+    q = L.plain(p)[0]
+    _, slope, _, error = L.activation(q, act)
+    if act == "silu":
+        error = error + 2 * np.abs(q) * special.expit(q) * special.expit(-q) * (1 + np.abs(q))
+    off = np.abs(L.plain(db) - slope) / (L.U * (error + np.abs(slope)) + 1e-300)
+    assert (off <= 1.0).all(), (off.max(), q[off.argmax()])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_bias_gradient_of_like_rows(act, kind):
+    """Rows of one value each: an error of the slope enters every term alike. 40 rows are added by 64 additions at most."""
+    p = arguments(kind)[:4500:9].to("cuda").expand(40, -1).contiguous()
+    _, db = sg.epilogue_backward(torch.ones_like(p), p, activation=act)
+    q = L.plain(p[0])
+    _, slope, _, error = L.activation(q, act)
+    assert (np.abs(L.plain(db) - 40 * slope) <= 40 * L.U * (error + 2 * np.abs(q) + 65 * np.abs(slope))).all()
