@@ -51,3 +51,48 @@ def test_bias_gradient_of_like_rows(act, kind):
     q = L.plain(p[0])
     _, slope, _, error = L.activation(q, act)
     assert (np.abs(L.plain(db) - 40 * slope) <= 40 * L.U * (error + 2 * np.abs(q) + 65 * np.abs(slope))).all()
+
+
+def biases(M, N, K):
+    """Operands of zeros, so that p is the bias; M and K choose the kernel."""
+    A, B = (torch.zeros(n, K + K % 2, device="cuda").to(torch.float8_e4m3fn)[:, :K] for n in (M, N))
+    return A, torch.ones(M, -(-K // 128), device="cuda"), B, torch.ones(N, -(-K // 128), device="cuda")
+
+
+def forward_error(p, act, kind):
+    """(value, its FP32 error in U): SiLU's exponent goes uncorrected in 16-bit results, off by two roundings."""
+    value, _, error, _ = L.activation(p, act)
+    if act == "silu" and kind != "fp32":
+        error = error + 2 * np.abs(p) * special.expit(-p) * np.abs(value)
+    return value, error
+
+
+KERNELS = [(3, 0), (3, 128), (2000, 128), (2000, 127), (300, 4096)]
+
+
+@pytest.mark.parametrize("act", L.ACTS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,K", KERNELS)
+def test_residual_that_cancels_the_activation(act, kind, M, K):
+    """A residual of -act(p) rounded to its type leaves what that rounding lost: act(p) has to be an FP32 value."""
+    bias = arguments(kind)[:4100:3].float().to("cuda")
+    value, error = forward_error(L.plain(bias)[None], act, kind)
+    residual = torch.from_numpy(-value).to(R.TYPES[kind]).to("cuda").expand(M, -1).contiguous()
+    for sums in (False, True):
+        C = sg.gemm_fp8_epilogue(*biases(M, bias.numel(), K), bias=bias, activation=act, residual=residual, fp32_sums=sums)
+        want = value + L.plain(residual[:1])
+        assert bool((C == C[:1]).all())
+        # the value's error, and the addition's
+        L.near(C[:1], want, L.U * (error + np.abs(want)) + 1e-300, kind)
+
+
+@pytest.mark.parametrize("act", L.ACTS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,K", KERNELS)
+def test_activations_with_fp32_sums(act, kind, M, K):
+    """fp32_sums without a residual: the FP32 value, rounded once."""
+    bias = arguments(kind).float().to("cuda")
+    value, error = forward_error(L.plain(bias)[None], act, kind)
+    C = sg.gemm_fp8_epilogue(*biases(M, bias.numel(), K), bias=bias, activation=act, dtype=R.TYPES[kind], fp32_sums=True)
+    L.near(C[:1], value, L.U * error + 1e-300, kind)
+    assert bool((C == C[:1]).all())
