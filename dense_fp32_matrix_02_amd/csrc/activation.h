@@ -8,7 +8,9 @@ namespace {
 
 // exp(x) for x <= 0: the exponent in base 2 as a rounded product and what its
 // rounding lost, which enters as a factor 1 + r ln 2. Without it the result
-// would be off by |x| half-units in the last place. Below -104 the result is zero.
+// would be off by |x| half-units in the last place. The hardware's power of two has
+// no subnormal results: from x = -87.34 down (2^-126) the result is zero. The bound
+// of -104 keeps an infinity out of the fused products.
 __device__ __forceinline__ float exp_below(float x) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
   x = fmaxf(x, -104.0f);
@@ -60,8 +62,10 @@ __device__ __forceinline__ float within(float p, float most) { return p < -most 
 constexpr float kTwoA = 1.5957691216057308f, kB = 0.044715f;
 
 // value = act(p) and slope = act'(p), at the infinities their limits; a NaN
-// gives NaN (but NONE's slope, 1). Beyond the bounds below s, or Phi, is 0 or 1
-// to the last bit and the other factor is cut, so that no infinity meets a zero.
+// gives NaN (but NONE's slope, 1). Beyond the bounds below the exponential is zero,
+// s, or Phi, 0 or 1, and the other factor is cut, so that no infinity meets a zero. An s
+// or Phi under 2^-126 is 0: SiLU of -87.34 to -104 is zero where it is -1.0e-36 to
+// -7e-44.
 template <int ACT>
 __device__ __forceinline__ void activation(float p, float& value, float& slope) {
   if constexpr (ACT == SGEMM_MI355_NONE) {

@@ -96,3 +96,14 @@ def test_activations_with_fp32_sums(act, kind, M, K):
     C = sg.gemm_fp8_epilogue(*biases(M, bias.numel(), K), bias=bias, activation=act, dtype=R.TYPES[kind], fp32_sums=True)
     L.near(C[:1], value, L.U * error + 1e-300, kind)
     assert bool((C == C[:1]).all())
+
+
+def test_silu_near_the_least_exponential():
+    """Down to p = -87.3 a relative error; below, where exp(p) < 2^-126 counts as zero, 1.1e-36 at most."""
+    g = torch.linspace(-110, -80, 3001)
+    z = L.plain(sg.gated(torch.stack([g, torch.ones_like(g)], 1).to("cuda")))[:, 0]
+    p = g.double().numpy()
+    value, _, error, _ = L.activation(p, "silu")
+    above = p > -87.3
+    assert (np.abs(z - value)[above] <= (L.U * 12 * np.abs(value))[above]).all()  # tests/_layer.py: 10, and gated's product
+    assert (np.abs(z - value) <= 1.1e-36 + L.U * 12 * np.abs(value)).all() and (z[p < -87.4] == 0).all()
