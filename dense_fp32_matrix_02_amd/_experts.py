@@ -42,6 +42,11 @@ def _result_of(C, shape, dtype, A, on, stream):
     return C, _type_of(C.dtype, "C"), C.data_ptr(), _ld(C, "C")
 
 
+def _stride(ld, rows):
+    """The row stride to give for so many rows: of a single one, which may have any, one that direct loads take."""
+    return ld + -ld % 8 if rows == 1 else ld
+
+
 def _rows_by_expert(call, name, A, W, offsets, C, dtype, stream, inner, outer):
     sizes, strides = W.shape, W.stride()
     if len(sizes) != 3 or A.dim() != 2 or sizes[0] < 1:
@@ -55,7 +60,7 @@ def _rows_by_expert(call, name, A, W, offsets, C, dtype, stream, inner, outer):
     ldw = strides[1] if strides[2] == 1 and 1 < N <= MOST >= strides[1] >= K > 0 else _ld(W[0], "W")
     off = _ints(offsets, "offsets", on, E + 1)
     C, c_kind, c, ldc = _result_of(C, (rows, sizes[outer]), dtype or A.dtype, A, on, stream)
-    _check(_launch(call, on, kind, c_kind, rows, N, K, E, a, lda, W.data_ptr(), ldw, strides[0], off, c, ldc,
+    _check(_launch(call, on, kind, c_kind, rows, N, K, E, a, _stride(lda, rows), W.data_ptr(), _stride(ldw, N), strides[0], off, c, ldc,
                    _stream_of(on, stream)), name)
     return C
 
@@ -101,6 +106,6 @@ def gemm_experts_wgrad(A, B, offsets, C=None, *, beta: float = 0.0, dtype=None, 
     else:
         C = _result(C, (E, N, K), dtype, A, on, beta, stream)
         c_kind, ldc, apart = _type_of(C.dtype, "C"), _ld(C[0], "C"), C.stride(0)
-    _check(_launch(_c.experts_gemm_wgrad, on, kind, c_kind, rows, N, K, E, a, lda, b, ldb, off, beta, C.data_ptr(), ldc, apart,
-                   _stream_of(on, stream)), "experts_gemm_wgrad")
+    _check(_launch(_c.experts_gemm_wgrad, on, kind, c_kind, rows, N, K, E, a, _stride(lda, rows), b, _stride(ldb, rows), off, beta,
+                   C.data_ptr(), ldc, apart, _stream_of(on, stream)), "experts_gemm_wgrad")
     return C

@@ -32,13 +32,15 @@ int check(ExpertsForm form, const ExpertsArgs& g, int rows) {
   return m.check();
 }
 
+// What a call's kernel is chosen by: one expert has no stride between experts.
+void settle(ExpertsArgs& g) {
+  if (g.experts == 1) g.strideB = 0;
+}
+
 int run(ExpertsForm form, ExpertsArgs g, int rows, hipStream_t stream) {
   const int v = check(form, g, rows);
   if (v != SGEMM_MI355_OK || g.M == 0 || g.N == 0) return v;
-  // A single row has no stride that could keep it from direct loads.
-  if (rows == 1) g.lda = (g.lda + 7) / 8 * 8;
-  if ((form == EXPERTS_FORWARD ? g.N : form == EXPERTS_DGRAD ? g.K : rows) == 1) g.ldb = (g.ldb + 7) / 8 * 8;
-  if (g.experts == 1) g.strideB = 0;
+  settle(g);
   if (!experts_launchable(form, g)) return SGEMM_MI355_ERR_EXTENT;
   // Past the caches go results that they do not hold for whoever comes next, as
   // long as rows share no lines (weights' gradients of 8 experts of 512 rows,
@@ -76,14 +78,16 @@ int sgemm_mi355_experts_gemm_wgrad(int type, int c_type, int rows, int N, int K,
 
 const char* sgemm_mi355_experts_kernel_name(int form, int rows, int N, int K, int experts, const void* A, int lda,
                                             const void* W, int ldw, long long strideW) {
-  if (form < EXPERTS_FORWARD || form > EXPERTS_WGRAD || rows < 0 || N < 1 || K < 1 || experts < 1 || lda < 1 || ldw < 1 || strideW < 0)
+  if (form < EXPERTS_FORWARD || form > EXPERTS_WGRAD || rows < 0 || N < 0 || K < 0 || experts < 1 || lda < 1 || ldw < 1 || strideW < 0)
     return nullptr;
-  if (form != EXPERTS_WGRAD && rows == 0) return nullptr;
+  // No results; a sum over nothing has some, zeros.
+  if (form == EXPERTS_FORWARD ? rows == 0 || N == 0 : form == EXPERTS_DGRAD ? rows == 0 || K == 0 : N == 0 || K == 0) return nullptr;
   ExpertsArgs g{};
   g.experts = experts, g.A = A, g.lda = lda, g.B = W, g.ldb = ldw;
   g.M = form == EXPERTS_WGRAD ? N : rows, g.N = form == EXPERTS_FORWARD ? N : K;
   g.K = form == EXPERTS_FORWARD ? K : form == EXPERTS_DGRAD ? N : rows;
   if (form != EXPERTS_WGRAD) g.strideB = strideW;
+  settle(g);
   return experts_kernel_name((ExpertsForm)form, g);
 }
 

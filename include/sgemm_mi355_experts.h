@@ -15,7 +15,9 @@
  * `type`. Row strides count elements. Ownership, streams and errors are those
  * of sgemm_mi355.h: one kernel on `stream`, no allocation. Operands of any
  * alignment are accepted; 16-byte aligned ones whose strides are multiples of
- * 8 elements are loaded directly to LDS.
+ * 8 elements are loaded directly to LDS. The stride of a single row is looked at
+ * like any other: as no row follows, a multiple of 8 may be given for it. That of a
+ * single expert's weights is not.
  */
 #ifndef SGEMM_MI355_EXPERTS_H
 #define SGEMM_MI355_EXPERTS_H
@@ -49,10 +51,12 @@ int sgemm_mi355_experts_gemm_wgrad(int type, int c_type, int rows, int N, int K,
 
 /*
  * Name of the kernel that a call with these arguments runs (host only; the
- * pointers are inspected, never read): staged_*, rows_* or tile_*, then its tile of C (rows_*:
- * the rows of A in it; tile_256x256 takes tiles of 192 rows, or the last ones in pieces, where the
- * experts' rows, which only the device knows, fill the chip better so). form: one of the three below; W is B, and strideW
- * unused, in the weights' form. Null where nothing would be launched.
+ * pointers are inspected, never read): staged_*, rows_* or tile_*, then its
+ * tile of C (rows_*: the rows of A in it; tile_256x256 takes tiles of 192 rows,
+ * or the last ones in pieces, where the experts' rows, which only the device
+ * knows, fill the chip better so). form: one of the three below; W is B, and
+ * strideW unused, in the weights' form. Null where a call has no results to
+ * write (those of a sum over nothing are zeros), and for a stride under 1.
  */
 #define SGEMM_MI355_EXPERTS_FORWARD 0
 #define SGEMM_MI355_EXPERTS_DGRAD 1
