@@ -145,10 +145,6 @@ int sgemm_mi355_fp8_gemm_epilogue(int type, int M, int N, int K, const unsigned 
   g.bias = bias, g.act = act, g.residual = residual, g.ldr = ldr, g.P = P, g.ldp = ldp;
   const int v = check_product(g, FP8_EPILOGUE, K, 1);
   if (v != SGEMM_MI355_OK || M == 0 || N == 0) return v;
-  // A single row has no stride that could keep it from direct loads (1 x 6487, K
-  // 1559, lda 1559: 58 us without them, 5.6 with).
-  if (M == 1) g.lda = (g.lda + 15) / 16 * 16;
-  if (N == 1) g.ldb = (g.ldb + 15) / 16 * 16;
   // Past the caches go results that they do not hold for whoever comes next, as
   // long as rows share no lines (8192 x 8192 bf16, K 4096, with P: 267 us against
   // 302 through them; 3001 x 2047 FP32 57 and 41).

@@ -121,7 +121,9 @@ int sgemm_mi355_fp8_gemm(int type, int M, int N, int K,
  * P = p each rounded once to `type`. bias: N floats, or null. residual: M x N
  * of `type`, or null; it may be C itself, at the same address and row stride.
  * P: M x N of `type`, or null. Everything else is as in sgemm_mi355_fp8_gemm
- * (K == 0 gives p = bias). SGEMM_MI355_ERR_OP: an unknown activation.
+ * (K == 0 gives p = bias), the kernel too: SGEMM_MI355_FP8_DENSE names it. A
+ * single row's lda or ldb is looked at like any other; as no row follows, a multiple
+ * of 16 may be given for it. SGEMM_MI355_ERR_OP: an unknown activation.
  */
 int sgemm_mi355_fp8_gemm_epilogue(int type, int M, int N, int K,
                                   const unsigned char *A, int lda, const float *SA, long long sa_row, long long sa_block,
