@@ -139,10 +139,10 @@ template <int BM>
 __device__ __forceinline__ int count_experts_tiles(const ExpertsArgs& g, int& last_end) {
   const int lane = threadIdx.x % 64;
   int begin, end, upto, total = 0;
+  last_end = 0;
   for (int e0 = 0; e0 < g.experts; e0 += 64) {
-    expert_tiles<BM>(g, e0, lane, begin, end, upto);
+    expert_tiles<BM>(g, e0, lane, begin, end, upto, last_end);
     total += __builtin_amdgcn_readlane(upto, 63);
-    last_end = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
   }
   return total + (g.M - last_end + BM - 1) / BM;
 }
@@ -178,9 +178,9 @@ __device__ __forceinline__ bool place_experts_tile(const ExpertsArgs& g, int tot
   t.pieces = pieces;
   const int tm = (int)(id / tiles_n);
   t.n0 = (int)(id - (int64_t)tm * tiles_n) * BN + right * (BN / 2);
-  int begin, end, upto, before = 0;
+  int begin, end, upto, before = 0, last = 0;
   for (int e0 = 0; e0 < g.experts; e0 += 64) {
-    const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto);
+    const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto, last);
     const uint64_t past = __ballot(tm < before + upto);
     if (past != 0) {
       const int l = __builtin_ctzll(past);

@@ -189,11 +189,27 @@ __device__ __forceinline__ void finish_c(const Fp8Args& g, int64_t m, int n, flo
 }
 
 // The experts' tiles of BM rows, numbered expert by expert and then those of
-// the rows that no expert has. The wave counts 64 experts at a time.
+// the rows that no expert has. The wave counts 64 experts at a time; `last` is
+// where the rows of those before them end, and then where theirs do. An offset
+// below an earlier one counts as that one, so that whatever the offsets no row
+// belongs to two experts, and the grid has a workgroup for every tile.
 template <int BM, class Args>
-__device__ __forceinline__ int expert_tiles(const Args& g, int e0, int lane, int& begin, int& end, int& upto) {
-  begin = 0, end = 0;
-  if (e0 + lane < g.experts) expert_rows(g.offsets, e0 + lane, g.M, begin, end);
+__device__ __forceinline__ int expert_tiles(const Args& g, int e0, int lane, int& begin, int& end, int& upto, int& last) {
+  const bool there = e0 + lane < g.experts;
+  auto limited_to_rows = [&](int e) __attribute__((always_inline)) { return min(max(g.offsets[e], 0), g.M); };
+  begin = !there || e0 + lane == 0 ? 0 : limited_to_rows(e0 + lane);
+  end = there ? limited_to_rows(e0 + lane + 1) : 0;
+  if (__ballot(there && (end < begin || begin < last)) != 0) {
+    end = max(end, last);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int x = __shfl_up(end, d, 64);
+      if (lane >= d) end = max(end, x);
+    }
+    begin = __shfl_up(end, 1, 64);
+    if (lane == 0) begin = last;
+  }
+  last = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
   const int own = (end - begin + BM - 1) / BM;
   upto = own;
 #pragma unroll
@@ -215,11 +231,10 @@ __device__ __forceinline__ bool find_tile(const Fp8Args& g, Tile& t) {
   if constexpr (FORM == FP8_EXPERTS) {
     const int lane = threadIdx.x % 64;
     int begin, end, upto;
-    int total = 0, last_end = 0;
+    int total = 0, last_end = 0, last = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
-      expert_tiles<BM>(g, e0, lane, begin, end, upto);
+      expert_tiles<BM>(g, e0, lane, begin, end, upto, last_end);
       total += __builtin_amdgcn_readlane(upto, 63);
-      last_end = __builtin_amdgcn_readlane(end, min(63, g.experts - 1 - e0));
     }
     total += (g.M - last_end + BM - 1) / BM;
     const int64_t tiles = (int64_t)total * tiles_n;
@@ -230,7 +245,7 @@ __device__ __forceinline__ bool find_tile(const Fp8Args& g, Tile& t) {
     t.n0 = (int)(id - (int64_t)tm * tiles_n) * BN;
     int before = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
-      const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto);
+      const int own = expert_tiles<BM>(g, e0, lane, begin, end, upto, last);
       const uint64_t past = __ballot(tm < before + upto);
       if (past != 0) {
         const int l = __builtin_ctzll(past);

@@ -6,8 +6,9 @@
  * `offsets` are experts + 1 device ints, ascending, as sgemm_mi355_route_plan
  * makes them: rows offsets[e] .. offsets[e+1]-1 of the rows' matrices belong
  * to expert e. They are bounded as in sgemm_mi355_fp8.h: limited to 0 .. rows,
- * an expert whose end is before its beginning has no rows, and offsets[0]
- * counts as 0. An expert's weights W_e = W + e*strideW are N x K, row-major,
+ * offsets[0] counts as 0, and one below an earlier one as that one, so that every
+ * row of C is written once; in the weights' gradient, where an expert's end before
+ * its beginning leaves it no rows, each expert's offsets count by themselves. An expert's weights W_e = W + e*strideW are N x K, row-major,
  * as in a linear layer.
  *
  * Operands are bf16 or fp16 (`type`, else SGEMM_MI355_ERR_TYPE). Their products

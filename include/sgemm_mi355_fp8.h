@@ -36,8 +36,10 @@
  * Integers the device reads (index, offsets) cannot be checked on the host;
  * the kernels bound them: an index outside the matrix reads as a row of
  * zeros, offsets are limited to 0 .. rows, an expert whose end is before its
- * beginning has no rows, and offsets[0] counts as 0. `experts` is at least 1
- * where it counts (else SGEMM_MI355_ERR_DIM).
+ * beginning has no rows, and offsets[0] counts as 0. Where rows of C belong to
+ * experts, an offset below an earlier one counts as that one, so that every row
+ * is written once; where experts' rows are summed, each expert's offsets count by
+ * themselves. `experts` is at least 1 where it counts (else SGEMM_MI355_ERR_DIM).
  */
 #ifndef SGEMM_MI355_FP8_H
 #define SGEMM_MI355_FP8_H
