@@ -11,6 +11,7 @@ fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -331,6 +332,25 @@ def _ld(x, name):
     return max(cols, 1)
 
 
+def run_on(several, call, on, *args):
+    """call(*args) with GPU `on` as the current one: a launch on a default stream goes to the current GPU. `several`: a
+    list that keeps whether there is more than one."""
+    if several and not several[0]:  # before the import statement: calls for single tokens wait for the host
+        return call(*args)
+    import torch
+
+    if not several:
+        several.append(torch.cuda.device_count() > 1)
+    if not several[0] or on == torch._C._cuda_getDevice():
+        return call(*args)
+    with torch.cuda.device(on):
+        return call(*args)
+
+
+_several = []
+_launch = functools.partial(run_on, _several)
+
+
 def matmul(A, B, out=None, *, kind: str = "mfma", config: int | None = None, stream=None):
     """C = A.B for FP32 torch tensors on the GPU through the C ABI.
 
@@ -358,11 +378,11 @@ def matmul(A, B, out=None, *, kind: str = "mfma", config: int | None = None, str
     args = (M, N, K, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"),
             out.data_ptr(), _ld(out, "C"), s)
     if config is not None:
-        rc = sgemm_mi355_with_config(*args, config)
+        rc = _launch(sgemm_mi355_with_config, A.device.index, *args, config)
     elif kind == "mfma":
-        rc = sgemm_mi355(*args)
+        rc = _launch(sgemm_mi355, A.device.index, *args)
     elif kind == "valu":
-        rc = sgemm_mi355_valu(*args)
+        rc = _launch(sgemm_mi355_valu, A.device.index, *args)
     else:
         raise ValueError(f"unknown kind {kind!r}")
     if rc != OK:
@@ -401,8 +421,8 @@ def gemm(A, B, C=None, *, opA: int = OP_N, opB: int = OP_N, alpha: float = 1.0, 
     s = s_obj.cuda_stream
     args = (opA, opB, M, N, K, alpha, A.data_ptr(), _ld(A, "A"), 0, B.data_ptr(), _ld(B, "B"), 0,
             beta, C.data_ptr(), _ld(C, "C"), 0, 1, s)
-    rc = (sgemm_mi355_strided_batched(*args) if config is None
-          else sgemm_mi355_strided_batched_with_config(*args, config))
+    rc = (_launch(sgemm_mi355_strided_batched, A.device.index, *args) if config is None
+          else _launch(sgemm_mi355_strided_batched_with_config, A.device.index, *args, config))
     if rc != OK:
         raise SgemmError(rc, "sgemm_mi355_strided_batched")
     return C
@@ -434,8 +454,8 @@ def gemm_strided_batched(A, B, C=None, *, opA: int = OP_N, opB: int = OP_N, alph
     sb = B.stride(0) if B.shape[0] > 1 else 0
     args = (opA, opB, M, N, K, alpha, A.data_ptr(), _ld(A[0], "A"), sa, B.data_ptr(), _ld(B[0], "B"),
             sb, beta, C.data_ptr(), _ld(C[0], "C"), C.stride(0), batch, s)
-    rc = (sgemm_mi355_strided_batched(*args) if config is None
-          else sgemm_mi355_strided_batched_with_config(*args, config))
+    rc = (_launch(sgemm_mi355_strided_batched, A.device.index, *args) if config is None
+          else _launch(sgemm_mi355_strided_batched_with_config, A.device.index, *args, config))
     if rc != OK:
         raise SgemmError(rc, "sgemm_mi355_strided_batched")
     return C
@@ -470,7 +490,8 @@ def gemm_splitk(A, B, C=None, *, splits: int | None = None, opA: int = OP_N, opB
     s = s_obj.cuda_stream
     args = (opA, opB, M, N, K, alpha, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"), beta,
             C.data_ptr(), _ld(C, "C"), splits, workspace.data_ptr(), workspace.numel() * 4, s)
-    rc = (sgemm_mi355_splitk(*args) if config is None else sgemm_mi355_splitk_with_config(*args, config))
+    rc = (_launch(sgemm_mi355_splitk, A.device.index, *args) if config is None
+          else _launch(sgemm_mi355_splitk_with_config, A.device.index, *args, config))
     if rc != OK:
         raise SgemmError(rc, "sgemm_mi355_splitk")
     return C
@@ -502,7 +523,8 @@ def gemm_streamk(A, B, C=None, *, opA: int = OP_N, opB: int = OP_N, alpha: float
     s = s_obj.cuda_stream
     args = (opA, opB, M, N, K, alpha, A.data_ptr(), _ld(A, "A"), B.data_ptr(), _ld(B, "B"), beta,
             C.data_ptr(), _ld(C, "C"), workspace.data_ptr(), workspace.numel() * 4, s)
-    rc = (sgemm_mi355_streamk(*args) if config is None else sgemm_mi355_streamk_with_config(*args, config))
+    rc = (_launch(sgemm_mi355_streamk, A.device.index, *args) if config is None
+          else _launch(sgemm_mi355_streamk_with_config, A.device.index, *args, config))
     if rc != OK:
         raise SgemmError(rc, "sgemm_mi355_streamk")
     return C

@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 
 from ._binding import MOST, OK, SgemmError, load
-from ._binding import _ld as _any_ld
+from ._binding import _launch, _ld as _any_ld
 
 ERR_TYPE, ERR_ROUTE = -13, -14
 F32, BF16, F16 = 0, 1, 2
@@ -188,7 +188,7 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
         Q, ldq = _bytes_out(rows, cols, X.device, stream)
         tiles = _blocks(cols)
         S = _empty((_blocks(rows), tiles), torch.float32, X.device, stream)
-        _check(_c.fp8_quantize_tiles(kind, rows, cols, X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), max(tiles, 1), 1, s),
+        _check(_launch(_c.fp8_quantize_tiles, on, kind, rows, cols, X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), max(tiles, 1), 1, s),
                "fp8_quantize_tiles")
         return Q, S
     n = rows if index is None else index.numel()
@@ -197,7 +197,7 @@ def quantize_fp8(X, *, index=None, blocks: bool = False, stream=None):
     S = _empty((n, _blocks(cols)), torch.float32, X.device, stream, (1, max(n, 1)))  # block by block
     if at is not None and n == 0:
         return Q, S
-    _check(_c.fp8_quantize_rows(kind, rows, cols, X.data_ptr(), ldx, at, n, Q.data_ptr(), ldq, S.data_ptr(), 1, max(n, 1), s),
+    _check(_launch(_c.fp8_quantize_rows, on, kind, rows, cols, X.data_ptr(), ldx, at, n, Q.data_ptr(), ldq, S.data_ptr(), 1, max(n, 1), s),
            "fp8_quantize_rows")
     return Q, S
 
@@ -226,7 +226,7 @@ def quantize_fp8_cols(X, *, index=None, offsets=None, stream=None):
     S = _empty((cols, _blocks(width)), torch.float32, X.device, stream, (1, max(cols, 1)))
     if at is not None and n == 0:
         at, rows = None, 0
-    _check(_c.fp8_quantize_cols(kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts, Q.data_ptr(), ldq, S.data_ptr(), 1,
+    _check(_launch(_c.fp8_quantize_cols, on, kind, rows, cols, X.data_ptr(), ldx, at, n, off, experts, Q.data_ptr(), ldq, S.data_ptr(), 1,
                                 max(cols, 1), _stream_of(on, stream)), "fp8_quantize_cols")
     return Q, S
 
@@ -281,7 +281,7 @@ def gemm_fp8(A, SA, B, SB, C=None, *, beta: float = 0.0, dtype=None, fp32_sums: 
     b = _operand(B, SB, "B", N, K, on, either=True)
     C = _result(C, (M, N), dtype or torch.bfloat16, A, on, beta, stream)
     kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
-    _check(_c.fp8_gemm(kind, M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)),
+    _check(_launch(_c.fp8_gemm, on, kind, M, N, K, *a[:5], *b, beta, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)),
            "fp8_gemm")
     return C
 
@@ -305,7 +305,7 @@ def gemm_fp8_experts(A, SA, B, SB, offsets, C=None, *, dtype=None, fp32_sums: bo
     b = _operand(B, SB, "B", N, K, on, either=True)
     C = _result(C, (R, N), dtype or torch.bfloat16, A, on, 0.0, stream)
     kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
-    _check(_c.fp8_gemm_experts(kind, R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5],
+    _check(_launch(_c.fp8_gemm_experts, on, kind, R, N, K, E, *a[:5], *b[:2], B.stride(0), *b[2:5], SB.stride(0), b[5],
                                off, C.data_ptr(), _ld(C, "C"), _stream_of(on, stream)), "fp8_gemm_experts")
     return C
 
@@ -338,6 +338,6 @@ def gemm_fp8_experts_wgrad(A, SA, B, SB, offsets, C=None, *, beta: float = 0.0, 
         raise ValueError("C must be experts x M x N")
     ldc = _ld(C[0], "C")
     kind = _type_of(C.dtype, "C") | (FP32_SUMS if fp32_sums else 0)
-    _check(_c.fp8_gemm_experts_wgrad(kind, rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
+    _check(_launch(_c.fp8_gemm_experts_wgrad, on, kind, rows, M, N, E, *a[:5], *b[:5], off, beta, C.data_ptr(), ldc,
                                      C.stride(0), _stream_of(on, stream)), "fp8_gemm_experts_wgrad")
     return C

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import MOST
+from ._binding import MOST, run_on
 from ._fp8 import (_bind, _blocks, _bytes_out, _check, _empty, _F, FP32_SUMS, _gpu, _I, _ld, _Library, _operand, _P,
                    _result, _SCALES, _stream_of, _type_of, _types, torch)
 
@@ -39,13 +39,9 @@ _several = []  # whether there is more than one GPU, once that is known
 
 
 def _launch(call, on, *args):
-    """call(*args) with GPU `on` as the current one: a launch on a default stream goes to the current GPU."""
-    if not _several:
-        _several.append(torch.cuda.device_count() > 1)
-    if not _several[0] or on == torch._C._cuda_getDevice():
+    if _several and not _several[0]:  # run_on's own first test, without the call
         return call(*args)
-    with torch.cuda.device(on):
-        return call(*args)
+    return run_on(_several, call, on, *args)
 
 
 def _act(name):

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import MOST
+from ._binding import MOST, _launch
 from ._fp8 import _bind, _check, _empty, _F, _gpu, _I, _ld, _Library, _P, _stream_of, _type_of, torch
 
 SOFTMAX, SIGMOID = 0, 1
@@ -71,7 +71,7 @@ def route(logits, k: int, *, bias=None, score: str = "softmax", groups: int = 1,
     at = None if bias is None else _dense(bias, "bias", torch.float32, (experts,), on)
     weights = _empty((tokens, max(k, 0)), torch.float32, logits.device, stream)
     ids = _empty((tokens, max(k, 0)), torch.int32, logits.device, stream)
-    _check(_c.route(kind, tokens, experts, logits.data_ptr(), ld, at, how, groups, top_groups, k,
+    _check(_launch(_c.route, on, kind, tokens, experts, logits.data_ptr(), ld, at, how, groups, top_groups, k,
                              int(bool(renorm)), scale, weights.data_ptr(), ids.data_ptr(), _stream_of(on, stream)),
            "route")
     return weights, ids
@@ -88,7 +88,7 @@ def route_backward(logits, experts, dweights, *, score: str = "softmax", renorm:
     ids = _dense(experts, "experts", torch.int32, (tokens, k), on)
     dw = _dense(dweights, "dweights", torch.float32, (tokens, k), on)
     out = _empty((tokens, count), torch.float32, logits.device, stream)
-    _check(_c.route_backward(kind, tokens, count, logits.data_ptr(), ld, ids, dw, how, k,
+    _check(_launch(_c.route_backward, on, kind, tokens, count, logits.data_ptr(), ld, ids, dw, how, k,
                                       int(bool(renorm)), scale, out.data_ptr(), max(count, 1), _stream_of(on, stream)),
            "route_backward")
     return out
@@ -114,7 +114,7 @@ def route_plan(experts, num_experts: int, *, stream=None):
     rows = _empty((tokens * k,), torch.int32, experts.device, stream)
     place = _empty((tokens, k), torch.int32, experts.device, stream)
     room = _empty((need // 4,), torch.int32, experts.device, stream) if need else None
-    _check(_c.route_plan(tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),
+    _check(_launch(_c.route_plan, on, tokens, k, num_experts, ids, offsets.data_ptr(), rows.data_ptr(),
                                   place.data_ptr(), None if room is None else room.data_ptr(), need, _stream_of(on, stream)),
            "route_plan")
     return offsets, rows, place
@@ -133,7 +133,7 @@ def route_combine(Z, place, weights, Y=None, *, stream=None):
     _gpu(Y, "Y", Z.dtype, on)
     if tuple(Y.shape) != (tokens, cols):
         raise ValueError("Y must be tokens x cols")
-    _check(_c.route_combine(kind, tokens, k, rows, cols, Z.data_ptr(), ldz, at, w, Y.data_ptr(), _ld(Y, "Y"),
+    _check(_launch(_c.route_combine, on, kind, tokens, k, rows, cols, Z.data_ptr(), ldz, at, w, Y.data_ptr(), _ld(Y, "Y"),
                                      _stream_of(on, stream)), "route_combine")
     return Y
 
@@ -154,7 +154,7 @@ def route_combine_backward(dY, Z, place, weights, *, stream=None):
     at, w = _dense(place, "place", torch.int32, (tokens, k), on), _dense(weights, "weights", torch.float32, (tokens, k), on)
     dZ = _empty((rows, cols), Z.dtype, Z.device, stream)
     dw = _empty((tokens, k), torch.float32, Z.device, stream)
-    _check(_c.route_combine_backward(kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,
+    _check(_launch(_c.route_combine_backward, on, kind, tokens, k, rows, cols, dY.data_ptr(), ldy, Z.data_ptr(), ldz, at, w,
                                               dZ.data_ptr(), max(cols, 1), dw.data_ptr(), _stream_of(on, stream)),
            "route_combine_backward")
     if tokens * k == 0 and dZ.numel() > 0:  # the C call writes nothing then
