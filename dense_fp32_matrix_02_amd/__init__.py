@@ -23,7 +23,7 @@ from ._binding import (  # noqa: F401
     sgemm_mi355_valu, sgemm_mi355_validate, sgemm_mi355_validate_ex, sgemm_mi355_version,
     sgemm_mi355_with_config, strerror)
 from ._fp8 import (  # noqa: F401
-    BF16, ERR_ROUTE, ERR_TYPE, F16, F32, FP8_DENSE, FP8_EXPERTS, FP8_WGRAD, FP32_SUMS, gemm_fp8,
+    BF16, ERR_ROUTE, ERR_TYPE, F16, F32, FP8_DENSE, FP8_EPILOGUE, FP8_EXPERTS, FP8_WGRAD, FP32_SUMS, gemm_fp8,
     gemm_fp8_experts, gemm_fp8_experts_wgrad, quantize_fp8, quantize_fp8_cols, sgemm_mi355_fp8_gemm,
     sgemm_mi355_fp8_gemm_experts, sgemm_mi355_fp8_gemm_experts_wgrad, sgemm_mi355_fp8_kernel_name,
     sgemm_mi355_fp8_quantize_cols, sgemm_mi355_fp8_quantize_rows, sgemm_mi355_fp8_quantize_tiles)

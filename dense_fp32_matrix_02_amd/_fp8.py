@@ -19,7 +19,7 @@ from ._binding import _launch, _ld as _any_ld
 ERR_TYPE, ERR_ROUTE = -13, -14
 F32, BF16, F16 = 0, 1, 2
 FP32_SUMS = 0x100  # added to a product's type
-FP8_DENSE, FP8_EXPERTS, FP8_WGRAD = 0, 1, 2
+FP8_DENSE, FP8_EXPERTS, FP8_WGRAD, FP8_EPILOGUE = 0, 1, 2, 4
 
 _P, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 _SCALES = [_P, _LL, _LL]

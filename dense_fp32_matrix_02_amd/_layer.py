@@ -239,12 +239,6 @@ def gemm_fp8_epilogue(A, SA, B, SB, C=None, *, bias=None, activation=None, resid
     on = _gpu(A, "A")
     a = _operand(A, SA, "A", M, K, on)
     b = _operand(B, SB, "B", N, K, on, either=True)
-    lda, ldb = a[1], b[1]
-    # A single row may have any stride: one that direct loads take (1 x 6487, K 1559: 5.6 us, 58 with 1559).
-    if M == 1:
-        lda += -lda % 16
-    if N == 1:
-        ldb += -ldb % 16
     if dtype is None:
         dtype = torch.bfloat16 if residual is None else residual.dtype
     if C is None:
@@ -257,7 +251,7 @@ def gemm_fp8_epilogue(A, SA, B, SB, C=None, *, bias=None, activation=None, resid
     v = None if bias is None else _vector(bias, "bias", N, on, torch.float32)
     r = (None, 0) if residual is None else _like(residual, "residual", C.dtype, on, (M, N))
     P = _empty((M, N), C.dtype, A.device, stream) if pre else None
-    _check(_launch(_c.fp8_gemm_epilogue, on, kind | FP32_SUMS if fp32_sums else kind, M, N, K, a[0], lda, *a[2:5], b[0], ldb, *b[2:], v, act, *r,
+    _check(_launch(_c.fp8_gemm_epilogue, on, kind | FP32_SUMS if fp32_sums else kind, M, N, K, *a[:5], *b, v, act, *r,
                    None if P is None else P.data_ptr(), N or 1, c, ldc, _stream_of(on, stream)), "fp8_gemm_epilogue")
     return (C, P) if pre else C
 

@@ -35,7 +35,7 @@ hipError_t launch_quantize_tiles(int type, const QuantArgs& q, hipStream_t s);
 // rows of A and C belong to experts by `offsets`, B_e = B + e*strideB.
 // WGRAD: the summed axis belongs to experts, C_e = C + e*strideC. EPILOGUE:
 // C = act(p) + residual with p = A.B^T + bias.
-enum Fp8Form { FP8_DENSE = 0, FP8_EXPERTS = 1, FP8_WGRAD = 2, FP8_EPILOGUE = 3 };
+enum Fp8Form { FP8_DENSE = 0, FP8_EXPERTS = 1, FP8_WGRAD = 2, FP8_EPILOGUE = 4 };  // as in sgemm_mi355_fp8.h
 
 struct Fp8Args {
   int type, M, N, K;  // WGRAD: K = the rows that offsets count

@@ -123,9 +123,8 @@ int sgemm_mi355_fp8_gemm(int type, int M, int N, int K,
  * P = p each rounded once to `type`. bias: N floats, or null. residual: M x N
  * of `type`, or null; it may be C itself, at the same address and row stride.
  * P: M x N of `type`, or null. Everything else is as in sgemm_mi355_fp8_gemm
- * (K == 0 gives p = bias), the kernel too: SGEMM_MI355_FP8_DENSE names it. A
- * single row's lda or ldb is looked at like any other; as no row follows, a multiple
- * of 16 may be given for it. SGEMM_MI355_ERR_OP: an unknown activation.
+ * (K == 0 gives p = bias), but that a single row is loaded directly whatever its
+ * lda or ldb. SGEMM_MI355_ERR_OP: an unknown activation.
  */
 int sgemm_mi355_fp8_gemm_epilogue(int type, int M, int N, int K,
                                   const unsigned char *A, int lda, const float *SA, long long sa_row, long long sa_block,
@@ -163,13 +162,14 @@ int sgemm_mi355_fp8_gemm_experts_wgrad(int type, int rows, int M, int N, int exp
  * Name of the kernel that a product with these arguments runs (host only; the
  * pointers are inspected, never read): staged_*, rows_* or tile_*, then its
  * tile of C (rows_*: the rows of A in it), then the matrix instructions that
- * form a block's sum, fp8 or bf16. form: one of the three below; the sizes are
+ * form a block's sum, fp8 or bf16. form: one of the four below; the sizes are
  * those of the call (weight gradients: K is `rows`), experts and strideB count
  * where the form has them. Null where nothing would be launched.
  */
-#define SGEMM_MI355_FP8_DENSE 0   /* sgemm_mi355_fp8_gemm */
-#define SGEMM_MI355_FP8_EXPERTS 1 /* sgemm_mi355_fp8_gemm_experts */
-#define SGEMM_MI355_FP8_WGRAD 2   /* sgemm_mi355_fp8_gemm_experts_wgrad */
+#define SGEMM_MI355_FP8_DENSE 0    /* sgemm_mi355_fp8_gemm */
+#define SGEMM_MI355_FP8_EXPERTS 1  /* sgemm_mi355_fp8_gemm_experts */
+#define SGEMM_MI355_FP8_WGRAD 2    /* sgemm_mi355_fp8_gemm_experts_wgrad */
+#define SGEMM_MI355_FP8_EPILOGUE 4 /* sgemm_mi355_fp8_gemm_epilogue */
 const char *sgemm_mi355_fp8_kernel_name(int form, int type, int M, int N, int K, int experts,
                                         const unsigned char *A, int lda,
                                         const unsigned char *B, int ldb, long long strideB);
